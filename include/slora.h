@@ -447,6 +447,155 @@ int slora_lora_apply_noalloc(const void* d_pool, int32_t page_elems, int32_t dty
                              int32_t T, const void* d_x, int64_t ldx, void* d_y, int64_t ldy, float s,
                              void* stream, int32_t* status);
 
+/*
+ * ---- Paged key-value cache ----------------------------------------------
+ * The KV half of the unified pool (dongaigc.com summary, section 1 "Unified
+ * Paging": KV-cache tensors and adapter weights in the pages of one pool;
+ * fatihsoysal.com page, section "vLLM'in PagedAttention Mekanizmasi": a
+ * request's tokens in fixed-size blocks found through a table).  A slora_kv
+ * is one model's cache over a pool: slora_kv_plan turns a step's request
+ * lengths into block-table entries and a slot map, slora_kv_append norms and
+ * rotates the new tokens' queries and keys and stores keys and values, and
+ * slora_kv_attend lets the new tokens attend over everything stored.
+ *
+ * A page of page_elems elements holds P = page_elems / (heads_kv * head_dim)
+ * whole tokens' K (or V) vectors of one layer: one token where the page is
+ * the hidden size and every query head has its own key head, several with
+ * shared key heads.  P consecutive positions of a request are a block; in
+ * every layer it has one page for K and one for V.  Position t of table row i
+ * is token t % P of page table[layer][kv][i][t / P], that is row
+ * page * P + t % P of the pool seen as a matrix of heads_kv * head_dim
+ * columns.
+ *
+ * All calls enqueue work on the pool's compute stream, allocate nothing after
+ * slora_kv_create, never block the host, and can be captured in a CUDA graph
+ * (lengths, rows and pages are read on the device at replay).
+ */
+typedef struct slora_kv slora_kv; /* opaque, owned by the library */
+
+#define SLORA_KV_MAX_REQUESTS 4096 /* table rows, and requests of one batch */
+#define SLORA_KV_MAX_HEAD_DIM 256
+
+typedef struct slora_kv_config {
+  int32_t layers;        /* >= 1 */
+  int32_t heads_q;       /* query heads, a multiple of heads_kv: heads_q / heads_kv of them share a key head */
+  int32_t heads_kv;      /* key (and value) heads */
+  int32_t head_dim;      /* a multiple of 16, at most SLORA_KV_MAX_HEAD_DIM */
+  int32_t max_requests;  /* rows of the block table, 1 .. SLORA_KV_MAX_REQUESTS */
+  int32_t max_blocks;    /* entries of a row: a request holds at most max_blocks * P tokens */
+} slora_kv_config;
+
+/*
+ * The planned batch.  Its arrays lie in the caller's d_arrays (see
+ * slora_kv_create), at the same places in every batch: the next slora_kv_plan
+ * on the cache overwrites them and makes earlier batches stale (generation
+ * check).
+ */
+typedef struct slora_kv_batch {
+  int32_t R;                /* requests */
+  int32_t T;                /* tokens the batch has room for */
+  int32_t max_new;
+  const int32_t* q_start;   /* [R + 1] first token of each request; q_start[R] = tokens in use */
+  const int32_t* kv_len;    /* [R] tokens each request holds once the step's are appended; 0: left out */
+  const int32_t* tok_req;   /* [T] request of each token, -1: none */
+  const int32_t* tok_pos;   /* [T] position of each token in its request, -1: none */
+  const int32_t* slots;     /* [layers][2][slot_stride] pool row of each token's K and V, -1: none */
+  int64_t slot_stride;      /* the pool's max_tokens */
+  uint64_t generation;
+} slora_kv_batch;
+
+/*
+ * A cache over `pool` (not a planning pool), which must outlive it.  d_table:
+ * caller-owned device memory, int32 [layers][2][max_requests][max_blocks],
+ * set to -1 here on the compute stream; slora_kv_plan writes the entries of
+ * the blocks a step opens.  The caller may write entries too, on the compute
+ * stream: a row that starts with another row's entries shares that prefix.
+ * page_elems must be a multiple of heads_kv * head_dim.  Batches are of at
+ * most the pool's max_tokens tokens.  d_arrays: caller-owned device memory,
+ * int32, as many as slora_kv_array_ints says, zeroed here; the batch arrays.
+ * Both must outlive the cache.  Allocates the rotary table and the
+ * attention's scratch with cudaMalloc.
+ */
+int slora_kv_array_ints(const slora_pool* pool, const slora_kv_config* config, int64_t* n);
+int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* config, int32_t* d_table,
+                    int32_t* d_arrays);
+/* Synchronises the compute stream and frees what slora_kv_create allocated. */
+int slora_kv_destroy(slora_kv* kv);
+
+/*
+ * Rotary positions for slora_kv_append: the first rot_dim elements of every
+ * query and key head (a multiple of 16, at most head_dim; 0: no rotation, the
+ * state after create) are rot_dim / 2 pairs, and pair i of a token at
+ * position t turns by t * h_inv_freq[i] radians and is multiplied by mscale:
+ *     (a, b) -> mscale * (a cos - b sin, a sin + b cos).
+ * layout SLORA_ROTARY_HALF: pair i = elements i and i + rot_dim / 2;
+ * SLORA_ROTARY_INTERLEAVED: elements 2i and 2i + 1.  h_inv_freq: host, copied
+ * before the call returns.  Every scaling of the frequencies for long
+ * contexts is a choice of h_inv_freq and mscale.  The turn is reduced as a
+ * 64-bit fixed-point fraction of a circle (t times the frequency modulo
+ * 2^64), so it is exact to 2^-32 turn at every position below 2^31.
+ * Errors: SLORA_ERR_INVALID (sizes, layout, a frequency or mscale that is not
+ * finite).  Blocks the host until the compute stream has taken the table;
+ * not to be called while the stream is being captured.
+ */
+#define SLORA_ROTARY_HALF 0
+#define SLORA_ROTARY_INTERLEAVED 1
+int slora_kv_set_rotary(slora_kv* kv, int32_t rot_dim, int32_t layout, const double* h_inv_freq, float mscale);
+
+/*
+ * Plans one step for R requests: request r of table row d_row[r] (NULL: row
+ * r; rows of one batch are distinct) holds d_ctx[r] tokens and gets d_new[r]
+ * more (0 allowed), whose tokens follow each other in the batch, request by
+ * request.  It opens ceil((ctx + new) / P) - ceil(ctx / P) blocks; their
+ * pages are taken from d_pages in order, n_pages entries laid out
+ * [block][layer][K, V], so one slora_pages_alloc of 2 * layers pages per
+ * opened block serves a step as it is.  Entries past the last one needed are
+ * not read.  T: the tokens the batch has room for (the rows of q, k, v and
+ * out), at least the sum of d_new; a graph captured with a larger T replays
+ * smaller batches.  max_new: no request gets more new tokens than this (it
+ * picks the kernels slora_kv_attend launches).
+ *
+ * Arrays are device int32.  What the host cannot check is checked on the GPU
+ * and raises the device status SLORA_ERR_INVALID: a row outside the table, a
+ * negative length, more new tokens than max_new, or more tokens than a row
+ * holds leaves that request out (no tokens, kv_len 0); new tokens beyond T in
+ * sum, or blocks beyond d_pages, leave every request out; a page outside the
+ * pool becomes entry -1, and its tokens are not stored.
+ */
+int slora_kv_plan(slora_kv* kv, int32_t R, const int32_t* d_row, const int32_t* d_ctx, const int32_t* d_new,
+                  const int32_t* d_pages, int64_t n_pages, int32_t T, int32_t max_new, slora_kv_batch* out);
+
+/*
+ * Queries, keys and values of the batch's tokens in one layer.  d_q: T rows
+ * of heads_q * head_dim elements, d_k and d_v: T rows of heads_kv * head_dim,
+ * row strides ldq, ldk, ldv (so slices of one fused product serve).  With
+ * d_q_weight / d_k_weight (head_dim elements each; NULL: no norm) every head
+ * x becomes x / sqrt(mean(x^2) + eps) * weight, in fp32; then the rotary turn,
+ * in fp32; then one rounding.  Queries go to d_q_out (stride ldqo; may be d_q
+ * itself with the same stride, must not overlap it otherwise), keys and
+ * values to the tokens' slots; values keep their bits.  Tokens without a
+ * request are skipped.  Pointers 16-byte aligned, strides multiples of 8.
+ */
+int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, const void* d_q, int64_t ldq,
+                    const void* d_k, int64_t ldk, const void* d_v, int64_t ldv, const void* d_q_weight,
+                    const void* d_k_weight, float eps, void* d_q_out, int64_t ldqo);
+
+/*
+ * Causal attention of the batch's tokens in one layer over their requests'
+ * stored keys and values: for a token at position p, query head h and its key
+ * head h / (heads_q / heads_kv),
+ *     out = sum_{j <= p} softmax_j(c(scale * q . k_j)) v_j,
+ * c(s) = softcap * tanh(s / softcap), or s itself for softcap 0.  The step's
+ * own keys and values must be appended first.  Scores, softmax and sums are
+ * fp32, the result is rounded once.  d_q, d_out: T rows of heads_q * head_dim,
+ * strides ldq, ldo; out rows of tokens without a request are not written;
+ * d_out must not overlap d_q.  Slots past a request's length are never used,
+ * whatever they hold; a value that is not finite within a request's stored
+ * tokens may reach any of that request's outputs, and no other request's.
+ */
+int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, const void* d_q, int64_t ldq,
+                    void* d_out, int64_t ldo, float scale, float softcap);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,96 @@
+// Internal interface of the paged key-value cache: kv.cpp (host), kv.cu and
+// attend.cu (kernels), pool.cpp (the pool).  Not installed; the public ABI is
+// include/slora.h.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+struct slora_pool;
+
+namespace slora {
+
+constexpr int kKvMaxRequests = 4096;   // == SLORA_KV_MAX_REQUESTS
+constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
+
+// What the kernels of one cache share.  The pool's buffer is addressed as a
+// matrix of token rows of heads_kv * head_dim elements: position t of a
+// request is row page(t / P) * P + t % P.
+struct KvDev {
+  uint16_t* pool;
+  int64_t num_rows;              // num_pages * per_page (< 2^31)
+  int32_t* table;                // [layers][2][max_rows][max_blocks] page of each block, -1: none
+  int32_t num_pages;
+  int32_t per_page;              // P, tokens per page
+  int32_t layers, heads_q, heads_kv, head_dim;
+  int32_t max_rows, max_blocks, max_tokens;
+  // the planned batch
+  int32_t* q_start;              // [R + 1]
+  int32_t* kv_len;               // [R] tokens held after the step (0: request left out)
+  int32_t* row;                  // [R] table row
+  int32_t* tok_req;              // [T] request of each token, -1: none
+  int32_t* tok_pos;              // [T] position of each token in its request
+  int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
+  int32_t* error;                // the pool's device error word
+};
+
+struct KvPlanArgs {
+  KvDev kv;
+  int32_t R, T, max_new;
+  const int32_t* row;            // NULL: request r has row r
+  const int32_t* ctx;
+  const int32_t* fresh;          // new tokens per request
+  const int32_t* pages;          // [blocks][layers][2]
+  int64_t n_blocks;              // blocks `pages` has entries for
+};
+cudaError_t prepare_kv_kernels();   // opt-in shared memory sizes
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st);
+
+struct KvAppendArgs {
+  KvDev kv;
+  int32_t T, layer;
+  const uint16_t *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  uint16_t* q_out;
+  int64_t ldqo;
+  const uint16_t *qw, *kw;       // norm weights [head_dim], NULL: no norm
+  float eps;
+  const uint64_t* freq;          // [rot_dim / 2] turns a position, in units of 2^-64 turn
+  int32_t rot_dim;
+  int32_t interleaved;
+  float mscale;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, int num_sms, cudaStream_t st);
+
+struct KvAttendArgs {
+  KvDev kv;
+  int32_t R, T, layer;
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* out;
+  int64_t ldo;
+  float scale, softcap;
+};
+cudaError_t launch_kv_attend(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
+
+// What kv.cpp uses of a pool (pool.cpp).
+struct PoolView {
+  uint16_t* d_pool;
+  int64_t num_pages;
+  int32_t H, dtype, max_tokens, num_sms;
+  cudaStream_t compute;
+  int32_t* d_error;
+  bool planning;
+};
+PoolView pool_view(const slora_pool* p);
+enum KvTimer { kKvTimerPlan = 0, kKvTimerAppend, kKvTimerAttend };
+// Brackets a launch with the pool's timing events when timing is on.
+struct KvTimed {
+  KvTimed(slora_pool* p, KvTimer which);
+  void done();
+  slora_pool* pool;
+  int kind;
+  cudaEvent_t start;
+};
+
+}  // namespace slora

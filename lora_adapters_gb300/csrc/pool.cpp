@@ -32,6 +32,7 @@
 
 #include "../../include/slora.h"
 #include "internal.h"
+#include "kv.h"
 
 using namespace slora;
 
@@ -70,10 +71,12 @@ constexpr int32_t kOwnerFree = -1;
 constexpr int32_t kOwnerKV = -2;
 constexpr int32_t kOwnerPending = -3;
 
-enum TimerKind { kTBuild = 0, kTApplyCC, kTShrinkTC, kTExpandTC, kTScatter, kTLoadWait, kTNum };
+enum TimerKind { kTBuild = 0, kTApplyCC, kTShrinkTC, kTExpandTC, kTScatter, kTLoadWait,
+                 kTKvPlan, kTKvAppend, kTKvAttend, kTNum };
 // load_wait is not a kernel: the time the compute stream waited for adapter
 // copies before a segment build (recorded only when it had to wait)
-const char* kTimerNames[kTNum] = {"build_segments", "apply_cc", "shrink_tc", "expand_tc", "scatter", "load_wait"};
+const char* kTimerNames[kTNum] = {"build_segments", "apply_cc", "shrink_tc", "expand_tc", "scatter", "load_wait",
+                                   "kv_plan", "kv_append", "kv_attend"};
 
 }  // namespace
 
@@ -401,6 +404,27 @@ void free_device(slora_pool* p) {
 }  // namespace
 
 void slora::set_last_error(const char* msg) { g_err = msg ? msg : ""; }
+
+slora::PoolView slora::pool_view(const slora_pool* p) {
+  return PoolView{p->d_pool, p->num_pages, p->H, p->dtype, p->max_tokens, p->num_sms, p->compute, p->d_error,
+                  p->planning};
+}
+
+slora::KvTimed::KvTimed(slora_pool* p, KvTimer which) : pool(p), kind(kTKvPlan + which), start(nullptr) {
+  if (p->timing) {
+    start = get_event(p);
+    if (start) cudaEventRecord(start, p->compute);
+  }
+}
+
+void slora::KvTimed::done() {
+  if (!start) return;
+  cudaEvent_t end = get_event(pool);
+  if (!end) return;
+  cudaEventRecord(end, pool->compute);
+  pool->recs.push_back({kind, start, end});
+  start = nullptr;
+}
 
 // =================================================================================
 extern "C" {

@@ -44,7 +44,12 @@ EXPORTED = (
     "slora_lora_apply_bmm", "slora_bmm_scratch_bytes", "slora_set_tc_min_batch", "slora_debug_set_fault",
     "slora_debug_set_wait_limit", "slora_adapter_ready", "slora_build_segments_for",
     "slora_debug_poke_page_table",
+    "slora_kv_array_ints", "slora_kv_create", "slora_kv_destroy", "slora_kv_set_rotary", "slora_kv_plan", "slora_kv_append",
+    "slora_kv_attend",
 )
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+KV_MAX_REQUESTS = 4096
+KV_MAX_HEAD_DIM = 256
 FAULT_NONE, FAULT_PAGE_ALLOC, FAULT_COPY = 0, 1, 2
 
 
@@ -58,6 +63,18 @@ class slora_segments(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("max_segs", ctypes.c_int32),
                 ("perm", ctypes.c_void_p), ("seg_start", ctypes.c_void_p),
                 ("seg_adapter", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("generation", ctypes.c_uint64)]
+
+
+class slora_kv_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "heads_q", "heads_kv", "head_dim", "max_requests",
+                                              "max_blocks")]
+
+
+class slora_kv_batch(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("T", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("tok_req", ctypes.c_void_p),
+                ("tok_pos", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("slot_stride", ctypes.c_int64),
                 ("generation", ctypes.c_uint64)]
 
 
@@ -92,6 +109,13 @@ _SIGS = {
     "slora_debug_poke_page_table": [P, I64, I32, P],
     "slora_lora_apply_noalloc": [P, I32, I32, P, I64, P, I32, I32, P, P, I32, P, I32, P, I64, P, I64,
                                  ctypes.c_float, P, P],
+    "slora_kv_array_ints": [P, ctypes.POINTER(slora_kv_config), P],
+    "slora_kv_create": [ctypes.POINTER(P), P, ctypes.POINTER(slora_kv_config), P, P],
+    "slora_kv_destroy": [P],
+    "slora_kv_set_rotary": [P, I32, I32, P, ctypes.c_float],
+    "slora_kv_plan": [P, I32, P, P, P, P, I64, I32, I32, ctypes.POINTER(slora_kv_batch)],
+    "slora_kv_append": [P, ctypes.POINTER(slora_kv_batch), I32, P, I64, P, I64, P, I64, P, P, ctypes.c_float, P, I64],
+    "slora_kv_attend": [P, ctypes.POINTER(slora_kv_batch), I32, P, I64, P, I64, ctypes.c_float, ctypes.c_float],
 }
 
 
@@ -317,12 +341,66 @@ def slora_lora_apply_noalloc(d_pool: int, page_elems: int, dtype: int, d_page_ta
                                           stream or None, status or None), "slora_lora_apply_noalloc")
 
 
+# ---- paged key-value cache -------------------------------------------------------------
+def slora_kv_array_ints(pool: int, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
+                        max_blocks: int) -> int:
+    n = I64()
+    cfg = slora_kv_config(layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
+    _check(lib().slora_kv_array_ints(pool or None, ctypes.byref(cfg), ctypes.byref(n)), "slora_kv_array_ints")
+    return n.value
+
+
+def slora_kv_create(pool: int, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
+                    max_blocks: int, d_table: int, d_arrays: int) -> int:
+    out = P()
+    cfg = slora_kv_config(layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
+    _check(lib().slora_kv_create(ctypes.byref(out), pool or None, ctypes.byref(cfg), d_table or None,
+                                 d_arrays or None), "slora_kv_create")
+    return out.value
+
+
+def slora_kv_destroy(kv: int) -> None:
+    _check(lib().slora_kv_destroy(kv), "slora_kv_destroy")
+
+
+def slora_kv_set_rotary(kv: int, rot_dim: int, layout: int, inv_freq: Sequence[float], mscale: float = 1.0) -> None:
+    """inv_freq: rot_dim / 2 host floats, radians a position."""
+    if len(inv_freq) < rot_dim // 2:
+        raise ValueError(f"{rot_dim // 2} frequencies are needed, got {len(inv_freq)}")
+    _check(lib().slora_kv_set_rotary(kv, rot_dim, layout, _arr([float(f) for f in inv_freq], ctypes.c_double),
+                                     float(mscale)), "slora_kv_set_rotary")
+
+
+def slora_kv_plan(kv: int, R: int, d_row: int, d_ctx: int, d_new: int, d_pages: int, n_pages: int, T: int,
+                  max_new: int) -> slora_kv_batch:
+    b = slora_kv_batch()
+    _check(lib().slora_kv_plan(kv, R, d_row or None, d_ctx or None, d_new or None, d_pages or None, n_pages, T,
+                               max_new, ctypes.byref(b)), "slora_kv_plan")
+    return b
+
+
+def slora_kv_append(kv: int, batch: slora_kv_batch, layer: int, d_q: int, ldq: int, d_k: int, ldk: int, d_v: int,
+                    ldv: int, d_q_weight: int, d_k_weight: int, eps: float, d_q_out: int, ldqo: int) -> None:
+    _check(lib().slora_kv_append(kv, ctypes.byref(batch), layer, d_q or None, ldq, d_k or None, ldk, d_v or None, ldv,
+                                 d_q_weight or None, d_k_weight or None, eps, d_q_out or None, ldqo),
+           "slora_kv_append")
+
+
+def slora_kv_attend(kv: int, batch: slora_kv_batch, layer: int, d_q: int, ldq: int, d_out: int, ldo: int,
+                    scale: float, softcap: float = 0.0) -> None:
+    _check(lib().slora_kv_attend(kv, ctypes.byref(batch), layer, d_q or None, ldq, d_out or None, ldo, scale, softcap),
+           "slora_kv_attend")
+
+
 # ---- convenience wrapper for torch tensors -----------------------------------------
 class Pool:
-    """A pool over a torch device buffer (or a planning pool when device=None)."""
+    """A pool over a torch device buffer (or a planning pool when device=None).
+
+    buffer: the device buffer, a contiguous [num_pages, H] tensor of the
+    pool's type (default: one is allocated)."""
 
     def __init__(self, num_pages: int, H: int, dtype: str, projections, max_adapters: int, max_rank: int,
-                 max_tokens: int, device=None, compute_stream=None, copy_stream=None):
+                 max_tokens: int, device=None, compute_stream=None, copy_stream=None, buffer=None):
         import torch
 
         self.H, self.dtype = int(H), dtype
@@ -331,7 +409,12 @@ class Pool:
         self.buffer = None
         d_pool, cs, ps = 0, 0, 0
         if device is not None:
-            self.buffer = torch.empty((int(num_pages), int(H)), dtype=self.tdtype, device=device)
+            if buffer is None:
+                buffer = torch.empty((int(num_pages), int(H)), dtype=self.tdtype, device=device)
+            elif (buffer.dtype != self.tdtype or tuple(buffer.shape) != (num_pages, H) or not buffer.is_contiguous()
+                  or not buffer.is_cuda):
+                raise ValueError(f"buffer must be a contiguous CUDA tensor of {num_pages} x {H} {dtype} elements")
+            self.buffer = buffer
             d_pool = self.buffer.data_ptr()
             self.compute_stream = compute_stream or torch.cuda.current_stream(device)
             self.copy_stream = copy_stream or torch.cuda.Stream(device)
@@ -432,3 +515,109 @@ class Pool:
 
     def status(self) -> int:
         return slora_device_status(self.handle)
+
+
+class KVBatch:
+    """A planned step: the arrays of slora_kv_batch as views of the cache's
+    ``arrays`` tensor (the cache's next plan overwrites them)."""
+
+    def __init__(self, raw: slora_kv_batch, arrays, layers: int):
+        self.raw = raw
+        R, T, n = raw.R, raw.T, raw.slot_stride
+        base = arrays.data_ptr()
+
+        def view(ptr, length):
+            return arrays[(ptr - base) // 4:][:length]
+
+        self.q_start, self.kv_len = view(raw.q_start, R + 1), view(raw.kv_len, R)
+        self.tok_req, self.tok_pos = view(raw.tok_req, T), view(raw.tok_pos, T)
+        self.slots = view(raw.slots, 2 * layers * n).view(layers, 2, n)[:, :, :T]
+
+
+class KVCache:
+    """A paged key-value cache over a Pool (slora_kv_* of slora.h).
+
+    ``table`` is the block table [layers, 2, max_requests, max_blocks] (int32).
+    Calls run on the pool's compute stream: tensors made on another stream are
+    the caller's to order, as with every call on the pool.
+    """
+
+    def __init__(self, pool: Pool, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
+                 max_blocks: int):
+        import torch
+
+        self.handle = 0
+        if pool.buffer is None:
+            raise ValueError("a KV cache needs a pool with a device buffer")
+        self.pool = pool
+        self.heads_q, self.heads_kv, self.head_dim = heads_q, heads_kv, head_dim
+        self.tokens_per_page = pool.H // max(1, heads_kv * head_dim)
+        cfg = (layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
+        n = slora_kv_array_ints(pool.handle, *cfg)     # also refuses what the cache cannot be
+        i32 = dict(dtype=torch.int32, device=pool.buffer.device)
+        self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
+        self.arrays = torch.empty(n, **i32)
+        self.handle = slora_kv_create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
+
+    def close(self):
+        if self.handle:
+            if not self.pool.handle:
+                raise RuntimeError("the pool was closed before its KV cache")
+            slora_kv_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def set_rotary(self, rot_dim: int, inv_freq, interleaved: bool = False, mscale: float = 1.0) -> None:
+        slora_kv_set_rotary(self.handle, rot_dim, ROTARY_INTERLEAVED if interleaved else ROTARY_HALF, inv_freq, mscale)
+
+    @staticmethod
+    def _i32(name, t):
+        import torch
+
+        if t is None:
+            return 0
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
+        return t.data_ptr() if t.numel() else 0
+
+    def _rows(self, name, t, T, cols):
+        if t.dtype != self.pool.tdtype or not t.is_cuda or t.dim() != 2 or t.shape[1] != cols or t.shape[0] < T or (
+                t.stride(1) != 1 and cols > 1):
+            raise ValueError(f"{name} must be a CUDA {self.pool.dtype} tensor of {T} rows of {cols} contiguous elements")
+        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
+
+    def plan(self, ctx, new, pages, T: int, max_new: int, rows=None) -> KVBatch:
+        """ctx, new, rows: int32 per request; pages: the opened blocks' pages in
+        order (int32, [block][layer][K, V]); T: tokens the batch has room for."""
+        R = int(ctx.numel())
+        if new.numel() != R or (rows is not None and rows.numel() != R):
+            raise ValueError("ctx, new and rows must have one entry per request")
+        raw = slora_kv_plan(self.handle, R, self._i32("rows", rows), self._i32("ctx", ctx), self._i32("new", new),
+                            self._i32("pages", pages), int(pages.numel()) if pages is not None else 0, T, max_new)
+        return KVBatch(raw, self.arrays, self.table.shape[0])
+
+    def append(self, batch: KVBatch, layer: int, q, k, v, q_out=None, q_weight=None, k_weight=None,
+               eps: float = 1e-6) -> None:
+        """q [T, heads_q * head_dim] (rotated into q_out, or in place), k and v
+        [T, heads_kv * head_dim] (stored); q_weight, k_weight [head_dim]."""
+        T, wq, wk = batch.raw.T, self.heads_q * self.head_dim, self.heads_kv * self.head_dim
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dtype != self.pool.tdtype or w.numel() != self.head_dim or not w.is_contiguous()
+                                  or not w.is_cuda):
+                raise ValueError(f"{name} must be a contiguous CUDA {self.pool.dtype} tensor of {self.head_dim}")
+        slora_kv_append(self.handle, batch.raw, layer, *self._rows("q", q, T, wq), *self._rows("k", k, T, wk),
+                        *self._rows("v", v, T, wk), q_weight.data_ptr() if q_weight is not None else 0,
+                        k_weight.data_ptr() if k_weight is not None else 0, eps,
+                        *self._rows("q_out", q if q_out is None else q_out, T, wq))
+
+    def attend(self, batch: KVBatch, layer: int, q, out, scale: Optional[float] = None, softcap: float = 0.0) -> None:
+        """out[t] = attention of token t's heads over its request's stored tokens
+        (scale: 1 / sqrt(head_dim) by default)."""
+        T, wq = batch.raw.T, self.heads_q * self.head_dim
+        slora_kv_attend(self.handle, batch.raw, layer, *self._rows("q", q, T, wq), *self._rows("out", out, T, wq),
+                        self.head_dim ** -0.5 if scale is None else scale, softcap)
