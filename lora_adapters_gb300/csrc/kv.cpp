@@ -29,6 +29,9 @@ struct slora_kv {
   uint64_t* d_freq = nullptr;     // rotary turns a position, [head_dim / 2]
   int32_t rot_dim = 0, interleaved = 0;
   float mscale = 1.f;
+  float* d_part_o = nullptr;      // the attention's parts of split segments
+  float2* d_part_ml = nullptr;
+  FastDiv per_page_div;
   uint64_t generation = 0;
   int32_t R = 0, T = 0, max_new = 0;   // of the planned batch
 };
@@ -60,6 +63,8 @@ int fail(int code, const char* fmt, ...) {
 
 void free_kv(slora_kv* kv) {
   cudaFree(kv->d_freq);
+  cudaFree(kv->d_part_o);
+  cudaFree(kv->d_part_ml);
 }
 
 // A cache's sizes over a pool: checked, and its KvDev without the arrays.
@@ -111,6 +116,7 @@ int64_t place_arrays(KvDev& d, int32_t* base) {
   d.tok_pos = q; q += T;
   d.q_start = q; q += R + 1;
   d.kv_len = q; q += R;
+  d.dec_off = q; q += R + 1;
   d.row = q; q += R;
   return q - base;
 }
@@ -166,9 +172,13 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
   kv->pool = pool;
   kv->pv = pv;
   kv->dev = d;
+  kv->per_page_div.set((uint32_t)d.per_page);
   auto setup = [&]() -> int {
     CUDA_TRY(prepare_kv_kernels());
     CUDA_TRY(cudaMalloc(&kv->d_freq, sizeof(uint64_t) * (size_t)(c->head_dim / 2)));
+    const int64_t parts = kv_attend_parts(pv.num_sms);
+    CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));
+    CUDA_TRY(cudaMalloc(&kv->d_part_ml, sizeof(float2) * (size_t)parts));
     CUDA_TRY(cudaMemsetAsync(d_arrays, 0, sizeof(int32_t) * (size_t)ints, pv.compute));
     CUDA_TRY(cudaMemsetAsync(d_table, 0xff,
                              sizeof(int32_t) * (size_t)2 * c->layers * (size_t)c->max_requests * (size_t)c->max_blocks,
@@ -333,6 +343,9 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.ldo = ldo;
   a.scale = scale;
   a.softcap = softcap;
+  a.part_o = kv->d_part_o;
+  a.part_ml = kv->d_part_ml;
+  a.per_page_div = kv->per_page_div;
   KvTimed tm(kv->pool, kKvTimerAttend);
   CUDA_TRY(launch_kv_attend(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
   tm.done();

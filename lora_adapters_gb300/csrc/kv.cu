@@ -41,7 +41,7 @@ constexpr int kPlanPer = kKvMaxRequests / kPlanThreads;   // requests per thread
 struct PlanSmem {
   int32_t q_start[kKvMaxRequests + 1];
   int32_t open[kKvMaxRequests + 1];    // first block of each request in `pages`
-  int32_t warp_sum[2][kPlanThreads / 32];
+  int32_t warp_sum[3][kPlanThreads / 32];
   int32_t page[kPlanTokens][kPlanPlanes + 1];
   int32_t t_row[kPlanTokens], t_block[kPlanTokens], t_open[kPlanTokens], t_off[kPlanTokens];
   int32_t bad;
@@ -50,6 +50,14 @@ struct PlanSmem {
 // Sums stay below 2^31: what is larger is larger than T or n_blocks anyway.
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) {
   return (int32_t)min((uint32_t)a + (uint32_t)b, 0x7fffffffu);
+}
+
+// Decode units of a request: row tiles of its (token, head of the group) rows
+// times 16-token units of its length.
+__device__ __forceinline__ int32_t plan_units(const KvDev& d, int fresh, int len) {
+  const int64_t rows = (int64_t)fresh * (d.heads_q / d.heads_kv);
+  const int64_t n = (rows + kKvRowTile - 1) / kKvRowTile * ((len + kKvUnit - 1) / kKvUnit);
+  return (int32_t)min(n, (int64_t)0x7fffffff);
 }
 
 struct PlanReq {
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
   // ---- prefix sums over the requests, each thread a run of `per` of them
   const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
-  int32_t n_tok = 0, n_blk = 0;
+  int32_t n_tok = 0, n_blk = 0, n_dec = 0;
   bool bad = false;
   for (int r = r0; r < r1; ++r) {
     const PlanReq q = plan_req(a, r);
@@ -86,45 +94,56 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
     }
     n_tok = sat_add(n_tok, q.fresh);
     n_blk = sat_add(n_blk, (q.ctx + q.fresh + P - 1) / P - (q.ctx + P - 1) / P);
+    n_dec = sat_add(n_dec, plan_units(d, q.fresh, q.ctx + q.fresh));
   }
-  int32_t it = n_tok, ib = n_blk;
+  int32_t it = n_tok, ib = n_blk, id = n_dec;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int32_t t = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ib, o);
+    const int32_t t = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ib, o),
+                  e = __shfl_up_sync(0xffffffffu, id, o);
     if (lane >= o) {
       it = sat_add(it, t);
       ib = sat_add(ib, b);
+      id = sat_add(id, e);
     }
   }
   if (lane == 31) {
     sm.warp_sum[0][warp] = it;
     sm.warp_sum[1][warp] = ib;
+    sm.warp_sum[2][warp] = id;
   }
   __syncthreads();
-  int32_t wt = 0, wb = 0, tot_t = 0, tot_b = 0;
+  int32_t wt = 0, wb = 0, wd = 0, tot_t = 0, tot_b = 0, tot_d = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w == warp) {
       wt = tot_t;
       wb = tot_b;
+      wd = tot_d;
     }
     tot_t = sat_add(tot_t, sm.warp_sum[0][w]);
     tot_b = sat_add(tot_b, sm.warp_sum[1][w]);
+    tot_d = sat_add(tot_d, sm.warp_sum[2][w]);
   }
-  // more tokens than T or more blocks than pages: nobody has a place that can
-  // be relied on, every request is left out
-  const bool none = tot_t > a.T || tot_b > a.n_blocks;
-  if (none) tot_t = 0;
+  // more tokens than T, more blocks than pages, or more work than the
+  // attention can count: nobody has a place that can be relied on, every
+  // request is left out
+  const bool none = tot_t > a.T || tot_b > a.n_blocks || tot_d == 0x7fffffff;
+  if (none) tot_t = tot_d = 0;
   if ((bad || none) && blockIdx.x == 0) report_err(d.error, kErrInvalid);
   // exclusive sums (up to saturation, which `none` covers)
-  const int32_t pt = __shfl_up_sync(0xffffffffu, it, 1), pb = __shfl_up_sync(0xffffffffu, ib, 1);
-  int32_t rt = none ? 0 : wt + (lane ? pt : 0), rb = none ? 0 : wb + (lane ? pb : 0);
+  const int32_t pt = __shfl_up_sync(0xffffffffu, it, 1), pb = __shfl_up_sync(0xffffffffu, ib, 1),
+                pd = __shfl_up_sync(0xffffffffu, id, 1);
+  int32_t rt = none ? 0 : wt + (lane ? pt : 0), rb = none ? 0 : wb + (lane ? pb : 0),
+          rd = none ? 0 : wd + (lane ? pd : 0);
   for (int r = r0; r < r1; ++r) {
     const PlanReq q = plan_req(a, r);
     sm.q_start[r] = rt;
     sm.open[r] = rb;
     const bool in = q.row >= 0 && !none;
+    if (blockIdx.x == 0) d.dec_off[r] = rd;
     if (in) {
+      rd += plan_units(d, q.fresh, q.ctx + q.fresh);
       rt += q.fresh;
       rb += (q.ctx + q.fresh + P - 1) / P - (q.ctx + P - 1) / P;
     }
@@ -136,7 +155,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
   }
   if (tid == 0) {
     sm.q_start[a.R] = tot_t;
-    if (blockIdx.x == 0) d.q_start[a.R] = tot_t;
+    if (blockIdx.x == 0) {
+      d.q_start[a.R] = tot_t;
+      d.dec_off[a.R] = tot_d;
+    }
   }
   __syncthreads();
   // ---- tokens

@@ -12,6 +12,25 @@ namespace slora {
 
 constexpr int kKvMaxRequests = 4096;   // == SLORA_KV_MAX_REQUESTS
 constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
+constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
+constexpr int kKvUnit = 16;            // tokens of one decode unit
+
+// Quotients of 31-bit numbers by a fixed divisor: mul = ceil(2^(32 + shift) / d)
+// with 2^shift >= d, so that n * mul / 2^(32 + shift) is below 1/d too large
+// for every n < 2^32, and the floor is right; mul takes 33 bits, its top bit
+// is the extra addition of n.
+struct FastDiv {
+  uint32_t d = 1, mul = 0, shift = 0;
+  void set(uint32_t div) {
+    d = div;
+    shift = 0;
+    while ((1ull << shift) < div) ++shift;
+    mul = (uint32_t)((((1ull << shift) - div) << 32) / div + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
 
 // What the kernels of one cache share.  The pool's buffer is addressed as a
 // matrix of token rows of heads_kv * head_dim elements: position t of a
@@ -30,6 +49,7 @@ struct KvDev {
   int32_t* row;                  // [R] table row
   int32_t* tok_req;              // [T] request of each token, -1: none
   int32_t* tok_pos;              // [T] position of each token in its request
+  int32_t* dec_off;              // [R + 1] prefix sums of row tiles * units, the decode kernels' work
   int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
   int32_t* error;                // the pool's device error word
 };
@@ -70,7 +90,13 @@ struct KvAttendArgs {
   uint16_t* out;
   int64_t ldo;
   float scale, softcap;
+  float* part_o;                 // parts of split segments: [kv_attend_parts][kv_attend_cols]
+  float2* part_ml;               // [kv_attend_parts] their maximum (in powers of two) and sum
+  int32_t hbw;                   // neighbouring key heads worked on side by side
+  FastDiv per_page_div;
 };
+int64_t kv_attend_parts(int num_sms);
+int32_t kv_attend_cols(int32_t head_dim);
 cudaError_t launch_kv_attend(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).
