@@ -482,7 +482,7 @@ typedef struct slora_kv_config {
   int32_t heads_kv;      /* key (and value) heads */
   int32_t head_dim;      /* a multiple of 16, at most SLORA_KV_MAX_HEAD_DIM */
   int32_t max_requests;  /* rows of the block table, 1 .. SLORA_KV_MAX_REQUESTS */
-  int32_t max_blocks;    /* entries of a row: a request holds at most max_blocks * P tokens */
+  int32_t max_blocks;    /* entries of a row: a request holds at most max_blocks * P tokens (<= 2^30) */
 } slora_kv_config;
 
 /*
@@ -586,7 +586,7 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
  * head h / (heads_q / heads_kv),
  *     out = sum_{j <= p} softmax_j(c(scale * q . k_j)) v_j,
  * c(s) = softcap * tanh(s / softcap), or s itself for softcap 0.  The step's
- * own keys and values must be appended first.  Scores, softmax and sums are
+ * own keys and values must be appended first.  scale > 0.  Scores, softmax and sums are
  * fp32, the result is rounded once.  d_q, d_out: T rows of heads_q * head_dim,
  * strides ldq, ldo; out rows of tokens without a request are not written;
  * d_out must not overlap d_q.  Slots past a request's length are never used,

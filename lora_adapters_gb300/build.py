@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libslora.so")
 # The SLORA_DEBUG build: the same sources with bounds checks in every kernel.
 OBJ_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libslora_debug.so")
-SOURCES = ["pool.cpp", "kernels.cu", "tc_kernels.cu", "noalloc.cu", "bmm.cu", "kv.cpp", "kv.cu", "attend.cu"]
+SOURCES = ["pool.cpp", "kernels.cu", "tc_kernels.cu", "noalloc.cu", "bmm.cu", "kv.cpp", "kv.cu", "attend.cu",
+           "attend_tc.cu"]
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "kv.h"),
            os.path.join(CSRC, "kv.cuh"),
            os.path.join(ROOT, "include", "slora.h")]

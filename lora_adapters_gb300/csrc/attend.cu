@@ -491,7 +491,7 @@ cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st)
 int64_t kv_attend_parts(int num_sms) { return (int64_t)num_sms * kDecCtas * kDecWarps * 2 * kKvRowTile; }
 int32_t kv_attend_cols(int32_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
-cudaError_t launch_kv_attend(const KvAttendArgs& args, int dtype, int num_sms, cudaStream_t st) {
+cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, cudaStream_t st) {
   KvAttendArgs a = args;
   // warps that work on neighbouring heads of the same tokens: the largest of
   // 4, 2, 1 that divides the key heads

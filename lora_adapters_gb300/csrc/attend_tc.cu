@@ -1,0 +1,640 @@
+// slora_kv_attend for chunks: many new tokens of one request over its paged
+// keys and values, on the tensor cores (tcgen05).
+//
+// Rows are (token, query head) pairs that share a key head: a tile of 128 of
+// them is 128 / group tokens of the request with all `group` heads each, so
+// shared key heads fill the tile as well as separate ones do.  Per 128 keys
+//     S = Q K^T        (128 x 128 x head_dim, operands in shared memory)
+//     P = 2^(scale' S - m), m the row's running maximum in powers of two
+//     O <- O 2^(m_old - m) + P V       (P from TMEM, V in shared memory)
+// and O / sum(P) at the end.  S, P and O live in TMEM; S is read once and P,
+// rounded to the storage type (its sum is taken before the rounding), written
+// over it.  The rounding adds at most one unit of the storage type relative to
+// the largest value, the size of the result's own rounding.
+//
+// Bound: the tensor cores where contexts are long (4 head_dim operations per
+// score against a softmax of about ten instructions, the exponentials first),
+// memory for prompts of a few hundred tokens.  What the layout is for:
+//  - two tiles (A, B) of one request and key head share every K and V tile and
+//    take turns: while one tile's softmax runs, the tensor cores work on the
+//    other's products;
+//  - O is rescaled only when a row's maximum has grown by more than 2^8 (P
+//    then stays below 2^8, and fp32 sums lose nothing by it);
+//  - keys and values are gathered from their pages by the TMA engine, four
+//    token rows an instruction, into a ring of tiles;
+//  - the work, (request, key head, pair of tiles) x 128-key tiles laid end to
+//    end, is cut into equal runs, one per CTA; what a run holds of a segment
+//    cut by its ends goes to scratch as (m, l, O), joined in order afterwards.
+// A position past the request's length reads the request's first key instead
+// and gets weight 0, so whatever its slot holds is never touched.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "kv.cuh"
+#include "kv.h"
+#include "ptx.cuh"
+
+namespace slora {
+namespace {
+
+using namespace ptx;
+
+constexpr int kRowBytes = 128;                  // 64 elements, one swizzle row
+constexpr int kAtom = kKvTile * kRowBytes;      // 128 rows x 64 elements: 16 KB
+constexpr int kMaxAtoms = 2;                    // head_dim <= 128
+constexpr int kStages = 5;                      // K and V tiles in flight
+// warps: 0 K and V, 1 MMAs, 2 Q, 3 none; 4-7 softmax of tile A, 8-11 of tile B
+constexpr int kThreads = 12 * 32;
+constexpr int kTmemCols = 512;                  // S_A, S_B, O_A, O_B of 128 columns each
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;                    // O is rescaled when a maximum grew by more (powers of two)
+
+// Polls of a wait before it gives up (SLORA_ERR_TIMEOUT); a wait lasts
+// microseconds when all is well.
+constexpr uint32_t kPolls = 1u << 20;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+struct TcSmem {
+  uint8_t q[2][kMaxAtoms][kAtom];
+  uint8_t kv[kStages][kMaxAtoms][kAtom];
+  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint32_t tmem_slot;
+};
+
+__device__ __forceinline__ void report_err(int32_t* err, int code) {
+  if (err) atomicCAS(err, 0, code);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// D[tmem] (+)= A[tmem] B[smem]: A is 128 lanes of packed 16-bit pairs.
+__device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 3-D tiled tensor copy global -> shared.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// A part of a segment: one request, key head and pair of tiles, key tiles
+// [i0, i1) of n.
+struct Part {
+  int r, hk, pr;           // request, key head, pair of tiles
+  int i0, i1, n;           // key tiles of this part, of the segment
+  int q0, fresh, ctx;      // the request's first token, new tokens, tokens before them
+};
+// Walks a CTA's run of units part by part.  Every role walks it for itself.
+struct Walk {
+  int64_t u, u1;
+  int r, hk, pr;
+  int64_t seg_u;           // unit the segment starts at
+};
+// Key tiles of pair pr: up to the position of its last token.
+__device__ __forceinline__ int pair_tiles(int ctx, int fresh, int tpt, int pr) {
+  return (ctx + min(fresh, (pr + 1) * 2 * tpt) + kKvTile - 1) / kKvTile;
+}
+__device__ __forceinline__ void walk_segment(const KvAttendArgs& a, Walk& w) {
+  // the segment that holds unit w.u, from the request that does
+  const KvDev& d = a.kv;
+  while ((int64_t)__ldg(d.tc_off + w.r + 1) * d.heads_kv <= w.u) ++w.r;
+  const int off = __ldg(d.tc_off + w.r), per = __ldg(d.tc_off + w.r + 1) - off;
+  const int64_t in = w.u - (int64_t)off * d.heads_kv;
+  w.hk = (int)(in / per);
+  int rest = (int)(in - (int64_t)w.hk * per);
+  const int fresh = __ldg(d.q_start + w.r + 1) - __ldg(d.q_start + w.r), ctx = __ldg(d.kv_len + w.r) - fresh;
+  w.pr = 0;
+  for (int n; rest >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)); ++w.pr) rest -= n;
+  w.seg_u = w.u - rest;
+}
+__device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t total, int64_t run) {
+  Walk w;
+  w.u = (int64_t)blockIdx.x * run;
+  w.u1 = min(total, w.u + run);
+  int lo = 0, hi = a.R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)__ldg(a.kv.tc_off + mid) * a.kv.heads_kv <= w.u) lo = mid;
+    else hi = mid - 1;
+  }
+  w.r = lo;
+  return w;
+}
+__device__ __forceinline__ bool walk_next(const KvAttendArgs& a, Walk& w, Part& p) {
+  if (w.u >= w.u1) return false;
+  walk_segment(a, w);
+  p.r = w.r;
+  p.hk = w.hk;
+  p.pr = w.pr;
+  p.q0 = __ldg(a.kv.q_start + w.r);
+  p.fresh = __ldg(a.kv.q_start + w.r + 1) - p.q0;
+  p.ctx = __ldg(a.kv.kv_len + w.r) - p.fresh;
+  p.n = pair_tiles(p.ctx, p.fresh, a.tpt, w.pr);
+  p.i0 = (int)(w.u - w.seg_u);
+  p.i1 = (int)min((int64_t)p.n, p.i0 + (w.u1 - w.u));
+  w.u += p.i1 - p.i0;
+  return true;
+}
+// One past the last key tile of this part that tile x of the pair needs (i0:
+// none), and the tile's tokens.
+__device__ __forceinline__ int tile_end(const Part& p, int tpt, int x, int* tokens) {
+  const int t0 = (p.pr * 2 + x) * tpt;
+  *tokens = max(0, min(tpt, p.fresh - t0));
+  if (*tokens == 0) return p.i0;
+  return max(p.i0, min(p.i1, (p.ctx + t0 + *tokens + kKvTile - 1) / kKvTile));
+}
+
+template <class E, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ KvAttendArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem& sm = *reinterpret_cast<TcSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
+  const KvDev& d = a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
+  const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+  if ((int64_t)blockIdx.x * run >= total) return;
+  if (warp == 1) tmem_alloc(&sm.tmem_slot, kTmemCols);
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_full[x], 4);
+      mbar_init(&sm.o_full[x], 1);
+      mbar_init(&sm.o_empty[x], 4);
+    }
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_slot;
+  const int dim = d.head_dim, group = d.heads_q / d.heads_kv, tpt = a.tpt;
+  const int natoms = (dim + 63) >> 6;
+  bool ok = true;
+  auto wait_lane0 = [&](uint64_t* bar, uint32_t parity) -> bool {
+    bool got = true;
+    if (lane == 0) got = wait_bar(bar, parity);
+    return __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+  };
+  Walk w = walk_start(a, total, run);
+  Part p;
+
+  if (warp == 0) {  // ------------------------------------------------ K and V tiles
+    // Each lane gathers four consecutive positions of the tile; their pages
+    // for the next tile are looked up while this one's copies are issued.
+    const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
+    uint32_t n = 0;      // tiles issued
+    while (ok && walk_next(a, w, p)) {
+      const int len = p.ctx + p.fresh;
+      const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)__ldg(d.row + p.r) * d.max_blocks;
+      auto slot_of = [&](int j, int64_t pl) -> int {
+        const int b = (int)a.per_page_div.div((uint32_t)j);
+        const int page = __ldg(tab + pl + b);
+        // an entry that names no page: row 0, as the request's result is
+        // undefined (its plan reported the entry) but the copy is not
+        return (uint32_t)page < (uint32_t)d.num_pages ? page * d.per_page + (j - b * d.per_page) : 0;
+      };
+      int ks[4], vs[4];
+      auto lookup = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          int j = i * kKvTile + 4 * lane + x;
+          j = j < len ? j : 0;
+          ks[x] = slot_of(j, 0);
+          vs[x] = slot_of(j, plane);
+        }
+      };
+      lookup(p.i0);
+      for (int i = p.i0; i < p.i1 && ok; ++i) {
+        int kc[4], vc[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          kc[x] = ks[x];
+          vc[x] = vs[x];
+        }
+        if (i + 1 < p.i1) lookup(i + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half, ++n) {
+          const uint32_t st = n % kStages;
+          if (!wait_lane0(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_expect_tx(&sm.kv_full[st], (uint32_t)natoms * kAtom);
+          __syncwarp();
+          const int* c = half ? vc : kc;
+          for (int at = 0; at < natoms; ++at)
+            tma_gather4(&sm.kv[st][at][4 * lane * kRowBytes], &a.pool_map, p.hk * dim + at * 64, c[0], c[1], c[2], c[3],
+                        &sm.kv_full[st]);
+        }
+      }
+    }
+    if (!ok) {     // copies in flight land before the CTA goes
+      for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
+        wait_lane0(&sm.kv_full[k % kStages], (k / kStages) & 1);
+    }
+  } else if (warp == 2) {  // ------------------------------------------ Q tiles
+    uint32_t n = 0;
+    while (ok && walk_next(a, w, p)) {
+      if (!wait_lane0(&sm.q_empty, (n & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        const int t0 = p.pr * 2 * tpt;
+        const int tiles = p.fresh - t0 > tpt ? 2 : 1;
+        mbar_expect_tx(&sm.q_full, (uint32_t)(tiles * natoms * tpt * group) * kRowBytes);
+        for (int x = 0; x < tiles; ++x)
+          for (int at = 0; at < natoms; ++at)
+            tma_load_3d(sm.q[x][at], &a.q_map, at * 64, p.hk * group, p.q0 + t0 + x * tpt, &sm.q_full);
+      }
+      __syncwarp();
+      ++n;
+    }
+    if (n > 0) wait_lane0(&sm.q_full, (n - 1) & 1);   // the last copy has landed before the CTA goes
+  } else if (warp == 1) {  // ------------------------------------------ MMAs
+    const uint32_t id_s = umma_idesc_f16(kKvTile, kKvTile, Elem<E>::kBf16, false);
+    const uint32_t id_o = umma_idesc_f16(kKvTile, dim, Elem<E>::kBf16, true);
+    uint32_t n = 0, nq = 0, np[2] = {0, 0}, no[2] = {0, 0};
+    const uint32_t q_addr = smem_addr(sm.q[0][0]), kv_addr = smem_addr(sm.kv[0][0]);
+    auto issue_s = [&](int x, uint32_t st) {
+      const uint32_t qa = q_addr + x * kMaxAtoms * kAtom, ka = kv_addr + st * kMaxAtoms * kAtom;
+      for (int ks = 0; ks < dim / 16; ++ks) {
+        const uint32_t o = (ks >> 2) * kAtom + (ks & 3) * 32;
+        umma_f16(tmem + x * 128, umma_desc_sw128(qa + o, 16, 1024), umma_desc_sw128(ka + o, 16, 1024), id_s, ks ? 1u : 0u);
+      }
+      umma_commit(&sm.s_full[x]);
+    };
+    while (ok && walk_next(a, w, p)) {
+      int tok, end[2];
+      end[0] = tile_end(p, tpt, 0, &tok);
+      end[1] = tile_end(p, tpt, 1, &tok);
+      if (!wait_lane0(&sm.q_full, nq & 1)) {
+        ok = false;
+        break;
+      }
+      ++nq;
+      for (int i = p.i0 - 1; i < p.i1 && ok; ++i) {
+        // K tile i + 1 and V tile i, in the order they were loaded (K i0, V i0, K i0 + 1, ...)
+        const bool has_v = i >= p.i0, has_k = i + 1 < p.i1;
+        const uint32_t vst = n % kStages, vph = (n / kStages) & 1;
+        if (has_v) ++n;
+        const uint32_t kst = n % kStages, kph = (n / kStages) & 1;
+        if (has_k) ++n;
+        if (has_v && !wait_lane0(&sm.kv_full[vst], vph)) ok = false;
+        bool k_in = false;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (has_v && i < end[x]) {
+            if (i == p.i0) {        // O of the tile's previous part has been read
+              if (!wait_lane0(&sm.o_empty[x], (no[x] & 1) ^ 1)) {
+                ok = false;
+                break;
+              }
+              ++no[x];
+            }
+            if (!wait_lane0(&sm.p_full[x], np[x] & 1)) {
+              ok = false;
+              break;
+            }
+            ++np[x];
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t va = kv_addr + vst * kMaxAtoms * kAtom;
+#pragma unroll
+              for (int ks = 0; ks < kKvTile / 16; ++ks)
+                umma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + ks * 8,
+                            umma_desc_sw128(va + ks * 16 * kRowBytes, kAtom, 1024), id_o, (i > p.i0 || ks) ? 1u : 0u);
+              if (i == end[x] - 1) umma_commit(&sm.o_full[x]);
+            }
+            __syncwarp();
+          }
+          if (has_k && i + 1 < end[x]) {
+            if (!k_in && !wait_lane0(&sm.kv_full[kst], kph)) {
+              ok = false;
+              break;
+            }
+            k_in = true;
+            tc_fence_after();
+            if (lane == 0) issue_s(x, kst);
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        // (a K tile no tile needs is waited for all the same: its slot may only
+        // be handed back once it has been filled)
+        if (has_k && !k_in && !wait_lane0(&sm.kv_full[kst], kph)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          if (has_v) umma_commit(&sm.kv_empty[vst]);
+          if (has_k) umma_commit(&sm.kv_empty[kst]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(&sm.q_empty);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {  // ------------------------------------------ softmax
+    const int x = (warp - 4) >> 2, quarter = warp & 3, rho = 32 * quarter + lane;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
+    const float sc = CAP ? 2.f * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
+    const float cap2 = a.softcap * kLog2e;
+    const int my_tok = rho / group, my_head = rho - my_tok * group;
+    uint32_t ns = 0, nf = 0;
+    while (ok && walk_next(a, w, p)) {
+      int tokens;
+      const int end = tile_end(p, tpt, x, &tokens);
+      const int t0 = (p.pr * 2 + x) * tpt;
+      const bool live = my_tok < tokens;
+      const int pos = p.ctx + t0 + min(my_tok, max(tokens - 1, 0));
+      const int pos_first = p.ctx + t0;                       // the tile's earliest position
+      float m = -INFINITY;
+      uint64_t l2a = 0, l2b = 0;                              // pairs of partial sums (+0, +0)
+      for (int i = p.i0; i < end; ++i) {
+        if (!wait_lane0(&sm.s_full[x], ns & 1)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + 32 * c, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+        if (CAP) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              s[c][j] = __float_as_uint(cap2 - 2.f * cap2 * __fdividef(1.f, 1.f + ex2(__uint_as_float(s[c][j]) * sc)));
+        }
+        if ((i + 1) * kKvTile - 1 > pos_first) {              // some row may not see the whole tile
+          const int lim = pos - i * kKvTile;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j > lim) s[c][j] = 0xff800000u;    // -inf
+        }
+        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            mx = max3(mx, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+            my = max3(my, __uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3]));
+          }
+        mx = fmaxf(mx, my);
+        if (!CAP) mx *= sc;                                   // scale > 0; -inf stays
+        if (i == p.i0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + kGrow || (m == -INFINITY && mx > m))) {
+          // the products up to the previous tile are done (S came after them)
+          const float mn = fmaxf(m, mx);
+          const float f = mn == m ? 1.f : ex2(m - mn);
+          m = mn;
+          l2a = fma2(l2a, pair(f, f), 0);
+          l2b = fma2(l2b, pair(f, f), 0);
+          for (int c = 0; c < dim; c += 16) {
+            float v[16];
+            uint32_t r[16];
+            tmem_ld16(t_o + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[j] * f);
+            tmem_st16(t_o + c, r);
+          }
+        }
+        const float z = m == -INFINITY ? 0.f : m;             // a row that sees nothing yet: all weights 0
+        const uint64_t sc2 = CAP ? pair(1.f, 1.f) : pair(sc, sc), z2 = pair(-z, -z);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float2 e0 = unpair(fma2(pair(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), sc2, z2));
+            const float2 e1 = unpair(fma2(pair(__uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3])), sc2, z2));
+            const float p0 = ex2(e0.x), p1 = ex2(e0.y), p2 = ex2(e1.x), p3 = ex2(e1.y);
+            l2a = add2(l2a, pair(p0, p1));
+            l2b = add2(l2b, pair(p2, p3));
+            pk[j / 2] = Elem<E>::from2(p0, p1);
+            pk[j / 2 + 1] = Elem<E>::from2(p2, p3);
+          }
+          tmem_st16(t_s + 16 * c, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[x]);
+      }
+      if (!ok) break;
+      const float2 la = unpair(l2a), lb = unpair(l2b);
+      const float l = (la.x + la.y) + (lb.x + lb.y);
+      const bool whole = p.i0 == 0 && p.i1 == p.n;
+      // slot 0: the segment began in an earlier run; slot 1: it begins here
+      const int64_t part = (((int64_t)blockIdx.x * 2 + (p.i0 == 0 ? 1 : 0)) * 2 + x) * kKvTile + rho;
+      if (end > p.i0) {
+        if (!wait_lane0(&sm.o_full[x], nf & 1)) {
+          ok = false;
+          break;
+        }
+        ++nf;
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint16_t* dst = a.out + (int64_t)(p.q0 + t0 + my_tok) * a.ldo + (int64_t)(p.hk * group + my_head) * dim;
+        for (int c = 0; c < dim; c += 16) {
+          float v[16];
+          tmem_ld16(t_o + c, v);
+          if (live) {
+            if (whole) {
+              float y[8];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = v[8 * h + j] * inv;
+                *reinterpret_cast<uint4*>(dst + c + 8 * h) = pack8<E>(y);
+              }
+            } else {
+              float4* po = reinterpret_cast<float4*>(a.tc_part_o + part * kKvTile + c);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) po[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty[x]);
+      }
+      if (!whole && live) a.tc_part_ml[part] = make_float2(m, l);   // m = -inf: the part has no weight, O unwritten
+    }
+  }
+  if (!ok && lane == 0) report_err(d.error, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// The parts of the split segments, joined in the order of the cache: one warp
+// per row of a segment.  Border b lies between runs b and b + 1; a segment
+// belongs to the first border inside it.
+constexpr int kJoinThreads = 256;
+
+template <class E>
+__global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ KvAttendArgs a,
+                                                                     const int grid) {
+  const KvDev& d = a.kv;
+  const int lane = threadIdx.x & 31;
+  const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
+  const int64_t run = max((int64_t)1, (total + grid - 1) / grid);
+  const int64_t u = (int64_t)(blockIdx.x + 1) * run;      // the border
+  Walk w;
+  if (u < total) {
+    int lo = 0, hi = a.R - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)__ldg(d.tc_off + mid) * d.heads_kv <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    w.r = lo;
+    w.u = u;
+    walk_segment(a, w);
+  }
+  pdl_wait();
+  if (u >= total || w.seg_u == u || u - run > w.seg_u) return;
+  const int group = d.heads_q / d.heads_kv, dim = d.head_dim;
+  const int q0 = __ldg(d.q_start + w.r), fresh = __ldg(d.q_start + w.r + 1) - q0, ctx = __ldg(d.kv_len + w.r) - fresh;
+  const int n = pair_tiles(ctx, fresh, a.tpt, w.pr);
+  const int first = blockIdx.x, last = (int)((w.seg_u + n - 1) / run);
+  for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < 2 * kKvTile;
+       row += gridDim.y * (kJoinThreads / 32)) {
+    const int x = row / kKvTile, rho = row - x * kKvTile, tok = rho / group;
+    const int t = (w.pr * 2 + x) * a.tpt + tok;
+    if (tok >= a.tpt || t >= fresh) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int g = first; g <= last; ++g) {
+      const int64_t part = (((int64_t)g * 2 + (g == first ? 1 : 0)) * 2 + x) * kKvTile + rho;
+      const float2 ml = __ldcg(a.tc_part_ml + part);
+      if (ml.x == -INFINITY) continue;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.tc_part_o + part * kKvTile) + lane);
+      const float mn = fmaxf(m, ml.x), f = ex2(m - mn), e = ex2(ml.x - mn);
+      m = mn;
+      l = l * f + ml.y * e;
+      o.x = o.x * f + v.x * e;
+      o.y = o.y * f + v.y * e;
+      o.z = o.z * f + v.z * e;
+      o.w = o.w * f + v.w * e;
+    }
+    if (lane * 4 < dim) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(a.out + (int64_t)(q0 + t) * a.ldo + (int64_t)(w.hk * group + rho - tok * group) * dim +
+                                lane * 4) = make_uint2(Elem<E>::from2(o.x * inv, o.y * inv),
+                                                       Elem<E>::from2(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+template <class E>
+cudaError_t chunk_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st) {
+  if (a.softcap > 0.f) kv_chunk_kernel<E, true><<<num_sms, kThreads, kSmemBytes, st>>>(a);
+  else kv_chunk_kernel<E, false><<<num_sms, kThreads, kSmemBytes, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // one block row per border between runs, on the GPU before the runs are done
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms, 8);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_chunk_join_kernel<E>, a, num_sms);
+}
+
+}  // namespace
+
+cudaError_t prepare_kv_chunk_kernels() {
+  cudaError_t e;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__half, false>, attr, (int)kSmemBytes))) return e;
+  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__half, true>, attr, (int)kSmemBytes))) return e;
+  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__nv_bfloat16, false>, attr, (int)kSmemBytes))) return e;
+  return cudaFuncSetAttribute(kv_chunk_kernel<__nv_bfloat16, true>, attr, (int)kSmemBytes);
+}
+
+int64_t kv_chunk_part_rows(int num_sms) { return (int64_t)num_sms * 4 * kKvTile; }
+
+cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  return dtype == 0 ? chunk_dispatch<__half>(a, num_sms, st) : chunk_dispatch<__nv_bfloat16>(a, num_sms, st);
+}
+
+}  // namespace slora

@@ -32,6 +32,10 @@ struct slora_kv {
   float* d_part_o = nullptr;      // the attention's parts of split segments
   float2* d_part_ml = nullptr;
   FastDiv per_page_div;
+  int32_t tpt = 0;                // tokens of a chunk tile, 0: the decode kernel takes everything
+  float* d_tc_part_o = nullptr;
+  float2* d_tc_part_ml = nullptr;
+  CUtensorMap pool_map{};
   uint64_t generation = 0;
   int32_t R = 0, T = 0, max_new = 0;   // of the planned batch
 };
@@ -65,6 +69,8 @@ void free_kv(slora_kv* kv) {
   cudaFree(kv->d_freq);
   cudaFree(kv->d_part_o);
   cudaFree(kv->d_part_ml);
+  cudaFree(kv->d_tc_part_o);
+  cudaFree(kv->d_tc_part_ml);
 }
 
 // A cache's sizes over a pool: checked, and its KvDev without the arrays.
@@ -87,8 +93,8 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv,
     return fail(SLORA_ERR_INVALID, "page_elems=%d must be a multiple of heads_kv * head_dim = %lld", pv->H,
                 (long long)width);
   const int64_t P = pv->H / width;
-  if (pv->num_pages * P >= INT32_MAX || c->max_blocks * P >= INT32_MAX)
-    return fail(SLORA_ERR_INVALID, "more than 2^31 - 2 tokens in the pool or in a table row");
+  if (pv->num_pages * P >= INT32_MAX || c->max_blocks * P > (1 << 30))
+    return fail(SLORA_ERR_INVALID, "more than 2^31 - 2 tokens in the pool, or 2^30 in a table row");
   if ((int64_t)c->heads_q * c->head_dim >= INT32_MAX) return fail(SLORA_ERR_INVALID, "heads_q * head_dim too large");
   KvDev& d = *dev;
   d = KvDev{};
@@ -117,6 +123,7 @@ int64_t place_arrays(KvDev& d, int32_t* base) {
   d.q_start = q; q += R + 1;
   d.kv_len = q; q += R;
   d.dec_off = q; q += R + 1;
+  d.tc_off = q; q += R + 1;
   d.row = q; q += R;
   return q - base;
 }
@@ -179,6 +186,17 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
     const int64_t parts = kv_attend_parts(pv.num_sms);
     CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));
     CUDA_TRY(cudaMalloc(&kv->d_part_ml, sizeof(float2) * (size_t)parts));
+    kv->tpt = kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
+    if (kv->tpt > 0) {
+      CUDA_TRY(prepare_kv_chunk_kernels());
+      const int64_t rows = kv_chunk_part_rows(pv.num_sms);
+      CUDA_TRY(cudaMalloc(&kv->d_tc_part_o, sizeof(float) * (size_t)rows * kKvTile));
+      CUDA_TRY(cudaMalloc(&kv->d_tc_part_ml, sizeof(float2) * (size_t)rows));
+      const uint64_t width = (uint64_t)d.heads_kv * d.head_dim;
+      const uint64_t dims[2] = {width, (uint64_t)d.num_rows}, strides[1] = {2 * width};
+      const uint32_t box[2] = {64, 1};
+      if (int rc = encode_map(&kv->pool_map, pv.d_pool, pv.dtype, 2, dims, strides, box)) return rc;
+    }
     CUDA_TRY(cudaMemsetAsync(d_arrays, 0, sizeof(int32_t) * (size_t)ints, pv.compute));
     CUDA_TRY(cudaMemsetAsync(d_table, 0xff,
                              sizeof(int32_t) * (size_t)2 * c->layers * (size_t)c->max_requests * (size_t)c->max_blocks,
@@ -260,6 +278,7 @@ int slora_kv_plan(slora_kv* kv, int32_t R, const int32_t* d_row, const int32_t* 
   a.R = R;
   a.T = T;
   a.max_new = max_new;
+  a.tpt = kv->tpt;
   a.row = d_row;
   a.ctx = d_ctx;
   a.fresh = d_new;
@@ -326,7 +345,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
                     void* d_out, int64_t ldo, float scale, float softcap) {
   SLORA_RANGE("slora_kv_attend");
   if (int rc = check_batch(kv, batch, layer)) return rc;
-  if (!std::isfinite(scale)) return fail(SLORA_ERR_INVALID, "scale is not finite");
+  if (!std::isfinite(scale) || scale <= 0.f) return fail(SLORA_ERR_INVALID, "scale must be finite and > 0");
   if (!std::isfinite(softcap) || softcap < 0.f) return fail(SLORA_ERR_INVALID, "softcap must be finite and >= 0");
   if (kv->T == 0 || kv->R == 0) return SLORA_OK;
   const int64_t wq = (int64_t)kv->dev.heads_q * kv->dev.head_dim;
@@ -346,8 +365,22 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.part_o = kv->d_part_o;
   a.part_ml = kv->d_part_ml;
   a.per_page_div = kv->per_page_div;
+  a.tpt = kv->tpt;
+  a.tc_part_o = kv->d_tc_part_o;
+  a.tc_part_ml = kv->d_tc_part_ml;
+  const int32_t group = kv->dev.heads_q / kv->dev.heads_kv;
+  // chunks are possible where one request may bring more than kKvChunkRows rows
+  const bool chunks = kv->tpt > 0 && (int64_t)std::min(kv->max_new, kv->T) * group > kKvChunkRows;
+  if (chunks) {
+    a.pool_map = kv->pool_map;
+    const uint64_t dims[3] = {(uint64_t)kv->dev.head_dim, (uint64_t)kv->dev.heads_q, (uint64_t)kv->T};
+    const uint64_t strides[2] = {2 * (uint64_t)kv->dev.head_dim, 2 * (uint64_t)ldq};
+    const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)kv->tpt};
+    if (int rc = encode_map(&a.q_map, d_q, kv->pv.dtype, 3, dims, strides, box)) return rc;
+  }
   KvTimed tm(kv->pool, kKvTimerAttend);
-  CUDA_TRY(launch_kv_attend(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  if (chunks) CUDA_TRY(launch_kv_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  CUDA_TRY(launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
   tm.done();
   return SLORA_OK;
 }

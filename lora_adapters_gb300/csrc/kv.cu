@@ -38,10 +38,11 @@ constexpr int kPlanTokens = 32;
 constexpr int kPlanPlanes = 64;      // (layer, K/V) planes per pass
 constexpr int kPlanPer = kKvMaxRequests / kPlanThreads;   // requests per thread at most
 
+constexpr int kPlanSums = 4;
 struct PlanSmem {
   int32_t q_start[kKvMaxRequests + 1];
   int32_t open[kKvMaxRequests + 1];    // first block of each request in `pages`
-  int32_t warp_sum[3][kPlanThreads / 32];
+  int32_t warp_sum[kPlanSums][kPlanThreads / 32];
   int32_t page[kPlanTokens][kPlanPlanes + 1];
   int32_t t_row[kPlanTokens], t_block[kPlanTokens], t_open[kPlanTokens], t_off[kPlanTokens];
   int32_t bad;
@@ -52,26 +53,41 @@ __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) {
   return (int32_t)min((uint32_t)a + (uint32_t)b, 0x7fffffffu);
 }
 
-// Decode units of a request: row tiles of its (token, head of the group) rows
-// times 16-token units of its length.
-__device__ __forceinline__ int32_t plan_units(const KvDev& d, int fresh, int len) {
-  const int64_t rows = (int64_t)fresh * (d.heads_q / d.heads_kv);
-  const int64_t n = (rows + kKvRowTile - 1) / kKvRowTile * ((len + kKvUnit - 1) / kKvUnit);
-  return (int32_t)min(n, (int64_t)0x7fffffff);
+// The attention's work for one request: decode units (row tiles of its (token,
+// head of the group) rows times 16-token units of its length) or, for a chunk,
+// 128-key tiles of every pair of row tiles, up to the pair's last position.
+__device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ctx, int32_t* dec, int32_t* tc) {
+  const int64_t rows = (int64_t)fresh * (a.kv.heads_q / a.kv.heads_kv);
+  const int len = ctx + fresh;
+  *dec = *tc = 0;
+  if (a.tpt > 0 && rows > kKvChunkRows) {
+    int32_t n = 0;
+    for (int t = 0; t < fresh; t += 2 * a.tpt) n = sat_add(n, (ctx + min(fresh, t + 2 * a.tpt) + kKvTile - 1) / kKvTile);
+    *tc = n;
+  } else {
+    *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + kKvUnit - 1) / kKvUnit), (int64_t)0x7fffffff);
+  }
 }
 
+__device__ __forceinline__ int32_t ceil_pages(int32_t tokens, int32_t P) {
+  return tokens / P + (tokens % P != 0);
+}
 struct PlanReq {
   int32_t row, ctx, fresh;   // row -1: left out
+  int32_t opened;            // blocks the step opens
 };
 __device__ __forceinline__ PlanReq plan_req(const KvPlanArgs& a, int r) {
   PlanReq q;
   q.row = a.row ? __ldg(a.row + r) : r;
   q.ctx = __ldg(a.ctx + r);
   q.fresh = __ldg(a.fresh + r);
+  q.opened = 0;
   const int64_t room = (int64_t)a.kv.max_blocks * a.kv.per_page;
   if (q.row < 0 || q.row >= a.kv.max_rows || q.ctx < 0 || q.fresh < 0 || q.fresh > a.max_new ||
       (int64_t)q.ctx + q.fresh > room)
     q.row = -1;
+  else
+    q.opened = ceil_pages(q.ctx + q.fresh, a.kv.per_page) - ceil_pages(q.ctx, a.kv.per_page);
   return q;
 }
 
@@ -81,10 +97,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
   const KvDev& d = a.kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = d.per_page;
-  // ---- prefix sums over the requests, each thread a run of `per` of them
+  // ---- prefix sums over the requests, each thread a run of `per` of them:
+  // new tokens, opened blocks and (the first CTA alone) the attention's work
   const int per = (a.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
-  int32_t n_tok = 0, n_blk = 0, n_dec = 0;
+  const bool lead = blockIdx.x == 0;
+  int32_t own[kPlanSums] = {}, inc[kPlanSums], at[kPlanSums] = {}, tot[kPlanSums] = {};
   bool bad = false;
   for (int r = r0; r < r1; ++r) {
     const PlanReq q = plan_req(a, r);
@@ -92,72 +110,73 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
       bad = true;
       continue;
     }
-    n_tok = sat_add(n_tok, q.fresh);
-    n_blk = sat_add(n_blk, (q.ctx + q.fresh + P - 1) / P - (q.ctx + P - 1) / P);
-    n_dec = sat_add(n_dec, plan_units(d, q.fresh, q.ctx + q.fresh));
-  }
-  int32_t it = n_tok, ib = n_blk, id = n_dec;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t t = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ib, o),
-                  e = __shfl_up_sync(0xffffffffu, id, o);
-    if (lane >= o) {
-      it = sat_add(it, t);
-      ib = sat_add(ib, b);
-      id = sat_add(id, e);
+    own[0] = sat_add(own[0], q.fresh);
+    own[1] = sat_add(own[1], q.opened);
+    if (lead) {
+      int32_t dec, tc;
+      plan_work(a, q.fresh, q.ctx, &dec, &tc);
+      own[2] = sat_add(own[2], dec);
+      own[3] = sat_add(own[3], tc);
     }
   }
-  if (lane == 31) {
-    sm.warp_sum[0][warp] = it;
-    sm.warp_sum[1][warp] = ib;
-    sm.warp_sum[2][warp] = id;
+#pragma unroll
+  for (int k = 0; k < kPlanSums; ++k) {
+    inc[k] = own[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, inc[k], o);
+      if (lane >= o) inc[k] = sat_add(inc[k], v);
+    }
+    if (lane == 31) sm.warp_sum[k][warp] = inc[k];
   }
   __syncthreads();
-  int32_t wt = 0, wb = 0, wd = 0, tot_t = 0, tot_b = 0, tot_d = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w == warp) {
-      wt = tot_t;
-      wb = tot_b;
-      wd = tot_d;
+  for (int k = 0; k < kPlanSums; ++k) {
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w == warp) at[k] = tot[k];
+      tot[k] = sat_add(tot[k], sm.warp_sum[k][w]);
     }
-    tot_t = sat_add(tot_t, sm.warp_sum[0][w]);
-    tot_b = sat_add(tot_b, sm.warp_sum[1][w]);
-    tot_d = sat_add(tot_d, sm.warp_sum[2][w]);
+    const int32_t before = __shfl_up_sync(0xffffffffu, inc[k], 1);
+    if (lane) at[k] = sat_add(at[k], before);
   }
-  // more tokens than T, more blocks than pages, or more work than the
-  // attention can count: nobody has a place that can be relied on, every
-  // request is left out
-  const bool none = tot_t > a.T || tot_b > a.n_blocks || tot_d == 0x7fffffff;
-  if (none) tot_t = tot_d = 0;
-  if ((bad || none) && blockIdx.x == 0) report_err(d.error, kErrInvalid);
-  // exclusive sums (up to saturation, which `none` covers)
-  const int32_t pt = __shfl_up_sync(0xffffffffu, it, 1), pb = __shfl_up_sync(0xffffffffu, ib, 1),
-                pd = __shfl_up_sync(0xffffffffu, id, 1);
-  int32_t rt = none ? 0 : wt + (lane ? pt : 0), rb = none ? 0 : wb + (lane ? pb : 0),
-          rd = none ? 0 : wd + (lane ? pd : 0);
+  // more tokens than T or more blocks than pages: nobody has a place that can
+  // be relied on, every request is left out
+  const bool none = tot[0] > a.T || tot[1] > a.n_blocks;
+  // more work than 31 bits count: no attention
+  const bool idle = none || tot[2] == 0x7fffffff || tot[3] == 0x7fffffff;
+  if (none) at[0] = at[1] = tot[0] = 0;
+  if (idle) at[2] = at[3] = tot[2] = tot[3] = 0;
+  if ((bad || idle) && lead) report_err(d.error, kErrInvalid);
+  const int32_t tot_t = tot[0];
   for (int r = r0; r < r1; ++r) {
     const PlanReq q = plan_req(a, r);
-    sm.q_start[r] = rt;
-    sm.open[r] = rb;
     const bool in = q.row >= 0 && !none;
-    if (blockIdx.x == 0) d.dec_off[r] = rd;
-    if (in) {
-      rd += plan_units(d, q.fresh, q.ctx + q.fresh);
-      rt += q.fresh;
-      rb += (q.ctx + q.fresh + P - 1) / P - (q.ctx + P - 1) / P;
-    }
-    if (blockIdx.x == 0) {
-      d.q_start[r] = sm.q_start[r];
+    sm.q_start[r] = at[0];
+    sm.open[r] = at[1];
+    if (lead) {
+      d.q_start[r] = at[0];
+      d.dec_off[r] = at[2];
+      d.tc_off[r] = at[3];
       d.kv_len[r] = in ? q.ctx + q.fresh : 0;
       d.row[r] = in ? q.row : 0;
+      if (in && !idle) {
+        int32_t dec, tc;
+        plan_work(a, q.fresh, q.ctx, &dec, &tc);
+        at[2] += dec;
+        at[3] += tc;
+      }
+    }
+    if (in) {
+      at[0] += q.fresh;
+      at[1] += q.opened;
     }
   }
   if (tid == 0) {
     sm.q_start[a.R] = tot_t;
-    if (blockIdx.x == 0) {
+    if (lead) {
       d.q_start[a.R] = tot_t;
-      d.dec_off[a.R] = tot_d;
+      d.dec_off[a.R] = tot[2];
+      d.tc_off[a.R] = tot[3];
     }
   }
   __syncthreads();
@@ -179,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
         pos = q.ctx + t - sm.q_start[lo];
         row = q.row;
         block = pos / P;
-        const int first = (q.ctx + P - 1) / P;
+        const int first = ceil_pages(q.ctx, P);
         if (block >= first) open = sm.open[lo] + block - first;
       }
       if (t < a.T) {

@@ -3,6 +3,7 @@
 // include/slora.h.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -14,6 +15,19 @@ constexpr int kKvMaxRequests = 4096;   // == SLORA_KV_MAX_REQUESTS
 constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
 constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
 constexpr int kKvUnit = 16;            // tokens of one decode unit
+constexpr int kKvTile = 128;           // rows and keys of one chunk tile
+// A request whose new tokens make more rows than this (per key head) is a
+// chunk: two row tiles at most read the cache in the decode kernel.
+constexpr int kKvChunkRows = 16;
+// Query heads per key head the chunk kernel takes: a 128-row tile then holds
+// four tokens at least, and a request's tiles stay few enough to be counted
+// one by one.
+constexpr int kKvChunkGroup = 32;
+// Tokens of one row tile of the chunk kernel, 0: this shape runs in the decode
+// kernel (head_dim whole 16-element steps of one or two 64-element atoms).
+inline int32_t kv_chunk_tokens(int32_t group, int32_t head_dim) {
+  return head_dim < 64 || head_dim > 128 || group > kKvChunkGroup ? 0 : kKvTile / group;
+}
 
 // Quotients of 31-bit numbers by a fixed divisor: mul = ceil(2^(32 + shift) / d)
 // with 2^shift >= d, so that n * mul / 2^(32 + shift) is below 1/d too large
@@ -50,6 +64,7 @@ struct KvDev {
   int32_t* tok_req;              // [T] request of each token, -1: none
   int32_t* tok_pos;              // [T] position of each token in its request
   int32_t* dec_off;              // [R + 1] prefix sums of row tiles * units, the decode kernels' work
+  int32_t* tc_off;               // [R + 1] prefix sums of 128-key tiles, the chunk kernel's work per key head
   int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
   int32_t* error;                // the pool's device error word
 };
@@ -57,6 +72,7 @@ struct KvDev {
 struct KvPlanArgs {
   KvDev kv;
   int32_t R, T, max_new;
+  int32_t tpt;                   // kv_chunk_tokens
   const int32_t* row;            // NULL: request r has row r
   const int32_t* ctx;
   const int32_t* fresh;          // new tokens per request
@@ -94,10 +110,19 @@ struct KvAttendArgs {
   float2* part_ml;               // [kv_attend_parts] their maximum (in powers of two) and sum
   int32_t hbw;                   // neighbouring key heads worked on side by side
   FastDiv per_page_div;
+  // chunk kernel
+  int32_t tpt;                   // kv_chunk_tokens
+  float* tc_part_o;              // [kv_chunk_part_rows][kKvTile]
+  float2* tc_part_ml;
+  CUtensorMap pool_map;          // token rows of the pool, box {64, 1}
+  CUtensorMap q_map;             // q as [T][heads_q][head_dim], box {64, group, tpt}
 };
+int64_t kv_chunk_part_rows(int num_sms);
+cudaError_t prepare_kv_chunk_kernels();
+cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 int64_t kv_attend_parts(int num_sms);
 int32_t kv_attend_cols(int32_t head_dim);
-cudaError_t launch_kv_attend(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).
 struct PoolView {
@@ -109,6 +134,11 @@ struct PoolView {
   bool planning;
 };
 PoolView pool_view(const slora_pool* p);
+// A tensor map of 16-bit elements, 128-byte swizzle (rank 2 or 3; row strides
+// in bytes for the dimensions after the first); the reason is in
+// slora_last_error_string().
+int encode_map(CUtensorMap* m, const void* base, int dtype, int rank, const uint64_t* dims, const uint64_t* strides,
+               const uint32_t* box);
 enum KvTimer { kKvTimerPlan = 0, kKvTimerAppend, kKvTimerAttend };
 // Brackets a launch with the pool's timing events when timing is on.
 struct KvTimed {

@@ -410,6 +410,19 @@ slora::PoolView slora::pool_view(const slora_pool* p) {
                   p->planning};
 }
 
+int slora::encode_map(CUtensorMap* m, const void* base, int dtype, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return fail(SLORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, dtype == SLORA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                  const_cast<void*>(base), reinterpret_cast<const cuuint64_t*>(dims),
+                  reinterpret_cast<const cuuint64_t*>(strides), box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SLORA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return SLORA_OK;
+}
+
 slora::KvTimed::KvTimed(slora_pool* p, KvTimer which) : pool(p), kind(kTKvPlan + which), start(nullptr) {
   if (p->timing) {
     start = get_event(p);
