@@ -20,8 +20,8 @@
 //    other's products;
 //  - O is rescaled only when a row's maximum has grown by more than 2^8 (P
 //    then stays below 2^8, and fp32 sums lose nothing by it);
-//  - keys and values are gathered from their pages by the TMA engine, four
-//    token rows an instruction, into a ring of tiles;
+//  - keys and values are gathered from their pages by four warps with 16-byte
+//    asynchronous copies into a ring of tiles;
 //  - the work, (request, key head, pair of tiles) x 128-key tiles laid end to
 //    end, is cut into equal runs, one per CTA; what a run holds of a segment
 //    cut by its ends goes to scratch as (m, l, O), joined in order afterwards.
@@ -46,8 +46,14 @@ constexpr int kRowBytes = 128;                  // 64 elements, one swizzle row
 constexpr int kAtom = kKvTile * kRowBytes;      // 128 rows x 64 elements: 16 KB
 constexpr int kMaxAtoms = 2;                    // head_dim <= 128
 constexpr int kStages = 5;                      // K and V tiles in flight
-// warps: 0 K and V, 1 MMAs, 2 Q, 3 none; 4-7 softmax of tile A, 8-11 of tile B
-constexpr int kThreads = 12 * 32;
+// warps: 0-3 K and V, 4-7 softmax of tile A, 8-11 of tile B, 12 MMAs, 13 Q
+constexpr int kThreads = 16 * 32;
+constexpr int kLoaders = 4 * 32;
+constexpr int kWarpMma = 12, kWarpQ = 13;
+// Registers a thread of each warp group (setmaxnreg): the launch gives each of
+// the four groups 128, and the shares add up to the same 512.
+constexpr int kRegsLoad = 48, kRegsSoftmax = 192, kRegsOther = 80;
+static_assert(kRegsLoad + 2 * kRegsSoftmax + kRegsOther <= 4 * 128, "the shares come out of the launch's registers");
 constexpr int kTmemCols = 512;                  // S_A, S_B, O_A, O_B of 128 columns each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                    // O is rescaled when a maximum grew by more (powers of two)
@@ -103,13 +109,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// D[tmem] (+)= A[tmem] B[smem]: A is 128 lanes of packed 16-bit pairs.
-__device__ __forceinline__ void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Matrix descriptors as their low words (start address and leading offset in
+// 16-byte units): the high word, stride offset 1024 and 128-byte swizzle, is
+// the same for all of them.
+constexpr uint32_t kDescHi = (uint32_t)((uint64_t)(1024 >> 4) | (1u << 14) | (2u << 29));
+__device__ __forceinline__ uint32_t desc_lo(const void* p, uint32_t lbo_bytes) {
+  return ((smem_addr(p) >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+// D[tmem] (+)= A[smem] B[smem].
+template <bool ADD>
+__device__ __forceinline__ void umma_ss(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "n"(ADD ? 1 : 0));
+}
+// D[tmem] (+)= A[tmem] B[smem]: A is 128 lanes of packed 16-bit pairs.
+__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(add));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -118,7 +138,32 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
+// 16 bytes global -> shared, not kept in L1.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on the barrier when all copies of this thread so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// True in one lane of a converged warp, always the same one.  The MMA role runs
+// in that lane alone, waits and all: with the whole warp in the loop and one
+// lane of it issuing, every step took four times as long (741 us instead of
+// 319 for a 1024-token chunk over 16 K tokens).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
+  return y != 0;
+}
 // 3-D tiled tensor copy global -> shared.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -128,6 +173,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// S = Q K^T of STEPS 16-element steps; q, k: descriptors of the tiles.
+template <int STEPS>
+__device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint32_t q, uint32_t k, uint32_t idesc) {
+  umma_ss<false>(tmem_s, q, k, idesc);
+#pragma unroll
+  for (int ks = 1; ks < STEPS; ++ks) {
+    const uint32_t o = (ks >> 2) * (kAtom / 16) + (ks & 3) * 2;
+    umma_ss<true>(tmem_s, q + o, k + o, idesc);
+  }
+}
+
 // A part of a segment: one request, key head and pair of tiles, key tiles
 // [i0, i1) of n.
 struct Part {
@@ -135,55 +191,60 @@ struct Part {
   int i0, i1, n;           // key tiles of this part, of the segment
   int q0, fresh, ctx;      // the request's first token, new tokens, tokens before them
 };
-// Walks a CTA's run of units part by part.  Every role walks it for itself.
+// Walks a CTA's run of units part by part; every role walks it for itself.
 struct Walk {
-  int64_t u, u1;
-  int r, hk, pr;
-  int64_t seg_u;           // unit the segment starts at
+  int left;                // units of the run not yet walked
+  int r, hk, pr, i0;       // where the next part starts
 };
 // Key tiles of pair pr: up to the position of its last token.
 __device__ __forceinline__ int pair_tiles(int ctx, int fresh, int tpt, int pr) {
   return (ctx + min(fresh, (pr + 1) * 2 * tpt) + kKvTile - 1) / kKvTile;
 }
-__device__ __forceinline__ void walk_segment(const KvAttendArgs& a, Walk& w) {
-  // the segment that holds unit w.u, from the request that does
+// The walk from unit u on.
+__device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t u, int64_t end) {
   const KvDev& d = a.kv;
-  while ((int64_t)__ldg(d.tc_off + w.r + 1) * d.heads_kv <= w.u) ++w.r;
-  const int off = __ldg(d.tc_off + w.r), per = __ldg(d.tc_off + w.r + 1) - off;
-  const int64_t in = w.u - (int64_t)off * d.heads_kv;
-  w.hk = (int)(in / per);
-  int rest = (int)(in - (int64_t)w.hk * per);
-  const int fresh = __ldg(d.q_start + w.r + 1) - __ldg(d.q_start + w.r), ctx = __ldg(d.kv_len + w.r) - fresh;
-  w.pr = 0;
-  for (int n; rest >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)); ++w.pr) rest -= n;
-  w.seg_u = w.u - rest;
-}
-__device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t total, int64_t run) {
-  Walk w;
-  w.u = (int64_t)blockIdx.x * run;
-  w.u1 = min(total, w.u + run);
-  int lo = 0, hi = a.R - 1;
+  int lo = 0, hi = a.R - 1;         // the last request that starts at or before u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)__ldg(a.kv.tc_off + mid) * a.kv.heads_kv <= w.u) lo = mid;
+    if ((int64_t)__ldg(d.tc_off + mid) * d.heads_kv <= u) lo = mid;
     else hi = mid - 1;
   }
+  const int off = __ldg(d.tc_off + lo), per = max(1, __ldg(d.tc_off + lo + 1) - off);
+  const int64_t in = u - (int64_t)off * d.heads_kv;
+  Walk w;
+  w.left = (int)(end - u);
   w.r = lo;
+  w.hk = (int)(in / per);
+  w.i0 = (int)(in - (int64_t)w.hk * per);
+  w.pr = 0;
+  const int fresh = __ldg(d.q_start + lo + 1) - __ldg(d.q_start + lo), ctx = __ldg(d.kv_len + lo) - fresh;
+  for (int n; w.i0 >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)) && n > 0; ++w.pr) w.i0 -= n;
   return w;
 }
 __device__ __forceinline__ bool walk_next(const KvAttendArgs& a, Walk& w, Part& p) {
-  if (w.u >= w.u1) return false;
-  walk_segment(a, w);
+  if (w.left <= 0) return false;
+  const KvDev& d = a.kv;
   p.r = w.r;
   p.hk = w.hk;
   p.pr = w.pr;
-  p.q0 = __ldg(a.kv.q_start + w.r);
-  p.fresh = __ldg(a.kv.q_start + w.r + 1) - p.q0;
-  p.ctx = __ldg(a.kv.kv_len + w.r) - p.fresh;
+  p.q0 = __ldg(d.q_start + w.r);
+  p.fresh = __ldg(d.q_start + w.r + 1) - p.q0;
+  p.ctx = __ldg(d.kv_len + w.r) - p.fresh;
   p.n = pair_tiles(p.ctx, p.fresh, a.tpt, w.pr);
-  p.i0 = (int)(w.u - w.seg_u);
-  p.i1 = (int)min((int64_t)p.n, p.i0 + (w.u1 - w.u));
-  w.u += p.i1 - p.i0;
+  p.i0 = w.i0;
+  p.i1 = min(p.n, p.i0 + w.left);
+  w.left -= p.i1 - p.i0;
+  w.i0 = 0;
+  if (w.left > 0) {                 // the next pair, key head or request with tiles
+    if (++w.pr * 2 * a.tpt >= p.fresh) {
+      w.pr = 0;
+      if (++w.hk == d.heads_kv) {
+        w.hk = 0;
+        do ++w.r;
+        while (__ldg(d.tc_off + w.r + 1) == __ldg(d.tc_off + w.r));
+      }
+    }
+  }
   return true;
 }
 // One past the last key tile of this part that tile x of the pair needs (i0:
@@ -195,7 +256,9 @@ __device__ __forceinline__ int tile_end(const Part& p, int tpt, int x, int* toke
   return max(p.i0, min(p.i1, (p.ctx + t0 + *tokens + kKvTile - 1) / kKvTile));
 }
 
-template <class E, bool CAP>
+// STEPS: 16-element steps of a head, 8 or 4; 0: head_dim 80, 96 or 112 (a
+// branch to the right run of MMAs costs 7 % of the kernel).
+template <class E, bool CAP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ KvAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   TcSmem& sm = *reinterpret_cast<TcSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
@@ -204,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
   const int64_t run = (total + gridDim.x - 1) / gridDim.x;
   if ((int64_t)blockIdx.x * run >= total) return;
-  if (warp == 1) tmem_alloc(&sm.tmem_slot, kTmemCols);
+  if (warp == kWarpMma) tmem_alloc(&sm.tmem_slot, kTmemCols);
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_full[s], kLoaders);
       mbar_init(&sm.kv_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -232,167 +295,173 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     if (lane == 0) got = wait_bar(bar, parity);
     return __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
   };
-  Walk w = walk_start(a, total, run);
+  Walk w = walk_start(a, (int64_t)blockIdx.x * run, min(total, (int64_t)(blockIdx.x + 1) * run));
   Part p;
 
-  if (warp == 0) {  // ------------------------------------------------ K and V tiles
-    // Each lane gathers four consecutive positions of the tile; their pages
-    // for the next tile are looked up while this one's copies are issued.
+  if (warp < 4) {  // -------------------------------------------------- K and V tiles
+    // Warp w copies rows 32 w .. 32 w + 31 of a tile, a lane 16 bytes of every
+    // fourth row, straight to their swizzled places; each lane looks one
+    // position's page up, for the next tile while this one's copies run.  The
+    // copies arrive on the tile's barrier when they land, so a warp runs the
+    // whole ring ahead.
+    regs_down<kRegsLoad>();
     const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
+    const int64_t row_bytes = (int64_t)d.heads_kv * dim * 2;
+    const int ch = lane & 7, sub = lane >> 3;
+    const bool ch1 = 64 + ch * 8 < dim;              // this lane's piece of the second atom exists
     uint32_t n = 0;      // tiles issued
     while (ok && walk_next(a, w, p)) {
       const int len = p.ctx + p.fresh;
       const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)__ldg(d.row + p.r) * d.max_blocks;
-      auto slot_of = [&](int j, int64_t pl) -> int {
-        const int b = (int)a.per_page_div.div((uint32_t)j);
-        const int page = __ldg(tab + pl + b);
+      const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)p.hk * dim * 2 + ch * 16;
+      int kslot, vslot;
+      auto lookup = [&](int i) {
+        int j = i * kKvTile + 32 * warp + lane;
+        j = j < len ? j : 0;
+        const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
+        const int kp = __ldg(tab + b), vp = __ldg(tab + plane + b);
         // an entry that names no page: row 0, as the request's result is
         // undefined (its plan reported the entry) but the copy is not
-        return (uint32_t)page < (uint32_t)d.num_pages ? page * d.per_page + (j - b * d.per_page) : 0;
-      };
-      int ks[4], vs[4];
-      auto lookup = [&](int i) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          int j = i * kKvTile + 4 * lane + x;
-          j = j < len ? j : 0;
-          ks[x] = slot_of(j, 0);
-          vs[x] = slot_of(j, plane);
-        }
+        kslot = (uint32_t)kp < (uint32_t)d.num_pages ? kp * d.per_page + off : 0;
+        vslot = (uint32_t)vp < (uint32_t)d.num_pages ? vp * d.per_page + off : 0;
       };
       lookup(p.i0);
       for (int i = p.i0; i < p.i1 && ok; ++i) {
-        int kc[4], vc[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          kc[x] = ks[x];
-          vc[x] = vs[x];
-        }
+        const int kc = kslot, vc = vslot;
         if (i + 1 < p.i1) lookup(i + 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half, ++n) {
           const uint32_t st = n % kStages;
-          if (!wait_lane0(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) {
+          if (!wait_bar(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) ok = false;
+          if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
-          if (lane == 0) mbar_expect_tx(&sm.kv_full[st], (uint32_t)natoms * kAtom);
-          __syncwarp();
-          const int* c = half ? vc : kc;
-          for (int at = 0; at < natoms; ++at)
-            tma_gather4(&sm.kv[st][at][4 * lane * kRowBytes], &a.pool_map, p.hk * dim + at * 64, c[0], c[1], c[2], c[3],
-                        &sm.kv_full[st]);
-        }
-      }
-    }
-    if (!ok) {     // copies in flight land before the CTA goes
-      for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
-        wait_lane0(&sm.kv_full[k % kStages], (k / kStages) & 1);
-    }
-  } else if (warp == 2) {  // ------------------------------------------ Q tiles
-    uint32_t n = 0;
-    while (ok && walk_next(a, w, p)) {
-      if (!wait_lane0(&sm.q_empty, (n & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        const int t0 = p.pr * 2 * tpt;
-        const int tiles = p.fresh - t0 > tpt ? 2 : 1;
-        mbar_expect_tx(&sm.q_full, (uint32_t)(tiles * natoms * tpt * group) * kRowBytes);
-        for (int x = 0; x < tiles; ++x)
-          for (int at = 0; at < natoms; ++at)
-            tma_load_3d(sm.q[x][at], &a.q_map, at * 64, p.hk * group, p.q0 + t0 + x * tpt, &sm.q_full);
-      }
-      __syncwarp();
-      ++n;
-    }
-    if (n > 0) wait_lane0(&sm.q_full, (n - 1) & 1);   // the last copy has landed before the CTA goes
-  } else if (warp == 1) {  // ------------------------------------------ MMAs
-    const uint32_t id_s = umma_idesc_f16(kKvTile, kKvTile, Elem<E>::kBf16, false);
-    const uint32_t id_o = umma_idesc_f16(kKvTile, dim, Elem<E>::kBf16, true);
-    uint32_t n = 0, nq = 0, np[2] = {0, 0}, no[2] = {0, 0};
-    const uint32_t q_addr = smem_addr(sm.q[0][0]), kv_addr = smem_addr(sm.kv[0][0]);
-    auto issue_s = [&](int x, uint32_t st) {
-      const uint32_t qa = q_addr + x * kMaxAtoms * kAtom, ka = kv_addr + st * kMaxAtoms * kAtom;
-      for (int ks = 0; ks < dim / 16; ++ks) {
-        const uint32_t o = (ks >> 2) * kAtom + (ks & 3) * 32;
-        umma_f16(tmem + x * 128, umma_desc_sw128(qa + o, 16, 1024), umma_desc_sw128(ka + o, 16, 1024), id_s, ks ? 1u : 0u);
-      }
-      umma_commit(&sm.s_full[x]);
-    };
-    while (ok && walk_next(a, w, p)) {
-      int tok, end[2];
-      end[0] = tile_end(p, tpt, 0, &tok);
-      end[1] = tile_end(p, tpt, 1, &tok);
-      if (!wait_lane0(&sm.q_full, nq & 1)) {
-        ok = false;
-        break;
-      }
-      ++nq;
-      for (int i = p.i0 - 1; i < p.i1 && ok; ++i) {
-        // K tile i + 1 and V tile i, in the order they were loaded (K i0, V i0, K i0 + 1, ...)
-        const bool has_v = i >= p.i0, has_k = i + 1 < p.i1;
-        const uint32_t vst = n % kStages, vph = (n / kStages) & 1;
-        if (has_v) ++n;
-        const uint32_t kst = n % kStages, kph = (n / kStages) & 1;
-        if (has_k) ++n;
-        if (has_v && !wait_lane0(&sm.kv_full[vst], vph)) ok = false;
-        bool k_in = false;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (has_v && i < end[x]) {
-            if (i == p.i0) {        // O of the tile's previous part has been read
-              if (!wait_lane0(&sm.o_empty[x], (no[x] & 1) ^ 1)) {
-                ok = false;
-                break;
-              }
-              ++no[x];
-            }
-            if (!wait_lane0(&sm.p_full[x], np[x] & 1)) {
-              ok = false;
-              break;
-            }
-            ++np[x];
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t va = kv_addr + vst * kMaxAtoms * kAtom;
+          const uint32_t dst = smem_addr(sm.kv[st][0]) + (32 * warp + sub) * kRowBytes;
 #pragma unroll
-              for (int ks = 0; ks < kKvTile / 16; ++ks)
-                umma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + ks * 8,
-                            umma_desc_sw128(va + ks * 16 * kRowBytes, kAtom, 1024), id_o, (i > p.i0 || ks) ? 1u : 0u);
-              if (i == end[x] - 1) umma_commit(&sm.o_full[x]);
-            }
-            __syncwarp();
+          for (int j = 0; j < 8; ++j) {
+            const int row = __shfl_sync(0xffffffffu, half ? vc : kc, 4 * j + sub);
+            const uint8_t* src = base + row * row_bytes;
+            // row 32 w + 4 j + sub of the tile; its chunk ch goes to ch ^ (row & 7)
+            const uint32_t to = dst + 4 * j * kRowBytes + ((ch ^ ((4 * j + sub) & 7)) << 4);
+            cp16(to, src);
+            if (ch1) cp16(to + kAtom, src + 128);
           }
-          if (has_k && i + 1 < end[x]) {
-            if (!k_in && !wait_lane0(&sm.kv_full[kst], kph)) {
-              ok = false;
-              break;
-            }
-            k_in = true;
-            tc_fence_after();
-            if (lane == 0) issue_s(x, kst);
-            __syncwarp();
-          }
+          cp_arrive(&sm.kv_full[st]);
         }
-        if (!ok) break;
-        // (a K tile no tile needs is waited for all the same: its slot may only
-        // be handed back once it has been filled)
-        if (has_k && !k_in && !wait_lane0(&sm.kv_full[kst], kph)) {
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 12) {
+    regs_down<kRegsOther>();
+    if (warp == kWarpQ) {  // ----------------------------------------------- Q tiles
+      uint32_t n = 0;
+      while (ok && walk_next(a, w, p)) {
+        if (!wait_lane0(&sm.q_empty, (n & 1) ^ 1)) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          if (has_v) umma_commit(&sm.kv_empty[vst]);
-          if (has_k) umma_commit(&sm.kv_empty[kst]);
+          const int t0 = p.pr * 2 * tpt;
+          const int tiles = p.fresh - t0 > tpt ? 2 : 1;
+          mbar_expect_tx(&sm.q_full, (uint32_t)(tiles * natoms * tpt * group) * kRowBytes);
+          for (int x = 0; x < tiles; ++x)
+            for (int at = 0; at < natoms; ++at)
+              tma_load_3d(sm.q[x][at], &a.q_map, at * 64, p.hk * group, p.q0 + t0 + x * tpt, &sm.q_full);
         }
         __syncwarp();
+        ++n;
       }
-      if (!ok) break;
-      if (lane == 0) umma_commit(&sm.q_empty);
-      __syncwarp();
+      if (n > 0) wait_lane0(&sm.q_full, (n - 1) & 1);   // the last copy has landed before the CTA goes
+    } else if (warp == kWarpMma && elect_one()) {  // ----------------------- MMAs, by one thread
+      const uint32_t id_s = umma_idesc_f16(kKvTile, kKvTile, Elem<E>::kBf16, false);
+      const uint32_t id_o = umma_idesc_f16(kKvTile, dim, Elem<E>::kBf16, true);
+      // descriptors of the first tiles; others by adding to the address field
+      // (16-byte units), one addition an instruction
+      const uint32_t q_desc = desc_lo(sm.q[0][0], 16), k_desc = desc_lo(sm.kv[0][0], 16),
+                     v_desc = desc_lo(sm.kv[0][0], kAtom);
+      constexpr uint32_t kTileUnits = kMaxAtoms * kAtom / 16;
+      uint32_t st = 0, ph = 0, q_ph = 0;        // the ring's next tile; Q's phase
+      uint32_t p_ph = 0, o_ph = 3;              // a bit per tile: the phase to wait for
+      auto issue_s = [&](int x, uint32_t kst) {
+        const uint32_t qd = q_desc + x * kTileUnits, kd = k_desc + kst * kTileUnits;
+        const uint32_t ts = tmem + x * 128;
+        if constexpr (STEPS > 0) {
+          issue_qk<STEPS>(ts, qd, kd, id_s);
+        } else {
+          switch (dim) {
+            case 80: issue_qk<5>(ts, qd, kd, id_s); break;
+            case 96: issue_qk<6>(ts, qd, kd, id_s); break;
+            default: issue_qk<7>(ts, qd, kd, id_s); break;
+          }
+        }
+        umma_commit(&sm.s_full[x]);
+      };
+      auto issue_o = [&](int x, uint32_t vst, uint32_t add) {
+        const uint32_t vd = v_desc + vst * kTileUnits;
+#pragma unroll
+        for (int ks = 0; ks < kKvTile / 16; ++ks)
+          umma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + ks * (16 * kRowBytes / 16), id_o, ks ? 1u : add);
+      };
+      while (ok && walk_next(a, w, p)) {
+        int tok;
+        const int end0 = tile_end(p, tpt, 0, &tok), end1 = tile_end(p, tpt, 1, &tok);
+        ok = wait_bar(&sm.q_full, q_ph);
+        q_ph ^= 1;
+        // K tile i + 1 and V tile i, in the order they were loaded (K i0, V i0, K i0 + 1, ...)
+        for (int i = p.i0 - 1; i < p.i1 && ok; ++i) {
+          const bool has_v = i >= p.i0, has_k = i + 1 < p.i1;
+          const uint32_t vst = st;
+          if (has_v) {
+            ok = wait_bar(&sm.kv_full[st], ph);
+            if (++st == kStages) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          const uint32_t kst = st;
+          // (a K tile that no tile needs is waited for all the same: its slot
+          // may only be handed back once it has been filled)
+          bool k_in = !has_k;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int end = x ? end1 : end0;
+            if (ok && has_v && i < end) {
+              if (i == p.i0) {        // O of the tile's previous part has been read
+                ok = wait_bar(&sm.o_empty[x], (o_ph >> x) & 1);
+                o_ph ^= 1u << x;
+              }
+              ok = ok && wait_bar(&sm.p_full[x], (p_ph >> x) & 1);
+              p_ph ^= 1u << x;
+              tc_fence_after();
+              fence_async_shared();   // the tile's copies (generic proxy), for the MMAs' reads
+              if (ok) {
+                issue_o(x, vst, i > p.i0 ? 1u : 0u);
+                if (i == end - 1) umma_commit(&sm.o_full[x]);
+              }
+            }
+            if (ok && !k_in) {
+              ok = wait_bar(&sm.kv_full[kst], ph);
+              k_in = true;
+              tc_fence_after();
+              fence_async_shared();
+            }
+            if (ok && i + 1 < end) issue_s(x, kst);
+          }
+          if (!ok) break;
+          if (has_v) umma_commit(&sm.kv_empty[vst]);
+          if (has_k) umma_commit(&sm.kv_empty[kst]);
+          if (has_k && ++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit(&sm.q_empty);
+      }
     }
-  } else if (warp >= 4) {  // ------------------------------------------ softmax
+    __syncwarp();
+  } else {  // --------------------------------------------------------- softmax
+    regs_up<kRegsSoftmax>();
     const int x = (warp - 4) >> 2, quarter = warp & 3, rho = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
@@ -528,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       if (!whole && live) a.tc_part_ml[part] = make_float2(m, l);   // m = -inf: the part has no weight, O unwritten
     }
   }
-  if (!ok && lane == 0) report_err(d.error, kErrTimeout);
+  if (!ok) report_err(d.error, kErrTimeout);
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -550,24 +619,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
   const int64_t run = max((int64_t)1, (total + grid - 1) / grid);
   const int64_t u = (int64_t)(blockIdx.x + 1) * run;      // the border
-  Walk w;
-  if (u < total) {
-    int lo = 0, hi = a.R - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)__ldg(d.tc_off + mid) * d.heads_kv <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    w.r = lo;
-    w.u = u;
-    walk_segment(a, w);
-  }
+  Walk w{};
+  if (u < total) w = walk_start(a, u, total);
   pdl_wait();
-  if (u >= total || w.seg_u == u || u - run > w.seg_u) return;
+  // w.i0: the segment's tiles before the border
+  if (u >= total || w.i0 == 0 || w.i0 > run) return;
   const int group = d.heads_q / d.heads_kv, dim = d.head_dim;
   const int q0 = __ldg(d.q_start + w.r), fresh = __ldg(d.q_start + w.r + 1) - q0, ctx = __ldg(d.kv_len + w.r) - fresh;
   const int n = pair_tiles(ctx, fresh, a.tpt, w.pr);
-  const int first = blockIdx.x, last = (int)((w.seg_u + n - 1) / run);
+  const int first = blockIdx.x, last = (int)((u - w.i0 + n - 1) / run);
   for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < 2 * kKvTile;
        row += gridDim.y * (kJoinThreads / 32)) {
     const int x = row / kKvTile, rho = row - x * kKvTile, tok = rho / group;
@@ -601,10 +661,19 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
 constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
+template <class E, bool CAP>
+void (*chunk_kernel(int head_dim))(const KvAttendArgs) {
+  return head_dim == 128 ? kv_chunk_kernel<E, CAP, 8> : head_dim == 64 ? kv_chunk_kernel<E, CAP, 4>
+                                                                       : kv_chunk_kernel<E, CAP, 0>;
+}
+void (*chunk_kernel(int dtype, bool cap, int head_dim))(const KvAttendArgs) {
+  if (dtype == 0) return cap ? chunk_kernel<__half, true>(head_dim) : chunk_kernel<__half, false>(head_dim);
+  return cap ? chunk_kernel<__nv_bfloat16, true>(head_dim) : chunk_kernel<__nv_bfloat16, false>(head_dim);
+}
+
 template <class E>
-cudaError_t chunk_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st) {
-  if (a.softcap > 0.f) kv_chunk_kernel<E, true><<<num_sms, kThreads, kSmemBytes, st>>>(a);
-  else kv_chunk_kernel<E, false><<<num_sms, kThreads, kSmemBytes, st>>>(a);
+cudaError_t chunk_dispatch(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  chunk_kernel(dtype, a.softcap > 0.f, a.kv.head_dim)<<<num_sms, kThreads, kSmemBytes, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // one block row per border between runs, on the GPU before the runs are done
@@ -623,18 +692,19 @@ cudaError_t chunk_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st) 
 }  // namespace
 
 cudaError_t prepare_kv_chunk_kernels() {
-  cudaError_t e;
-  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__half, false>, attr, (int)kSmemBytes))) return e;
-  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__half, true>, attr, (int)kSmemBytes))) return e;
-  if ((e = cudaFuncSetAttribute(kv_chunk_kernel<__nv_bfloat16, false>, attr, (int)kSmemBytes))) return e;
-  return cudaFuncSetAttribute(kv_chunk_kernel<__nv_bfloat16, true>, attr, (int)kSmemBytes);
+  for (int i = 0; i < 12; ++i) {
+    const int dims[3] = {64, 80, 128};
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel(i & 1, i & 2, dims[i >> 2]),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 int64_t kv_chunk_part_rows(int num_sms) { return (int64_t)num_sms * 4 * kKvTile; }
 
 cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
-  return dtype == 0 ? chunk_dispatch<__half>(a, num_sms, st) : chunk_dispatch<__nv_bfloat16>(a, num_sms, st);
+  return dtype == 0 ? chunk_dispatch<__half>(a, dtype, num_sms, st) : chunk_dispatch<__nv_bfloat16>(a, dtype, num_sms, st);
 }
 
 }  // namespace slora

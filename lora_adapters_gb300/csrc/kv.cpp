@@ -35,7 +35,6 @@ struct slora_kv {
   int32_t tpt = 0;                // tokens of a chunk tile, 0: the decode kernel takes everything
   float* d_tc_part_o = nullptr;
   float2* d_tc_part_ml = nullptr;
-  CUtensorMap pool_map{};
   uint64_t generation = 0;
   int32_t R = 0, T = 0, max_new = 0;   // of the planned batch
 };
@@ -192,10 +191,6 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
       const int64_t rows = kv_chunk_part_rows(pv.num_sms);
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_o, sizeof(float) * (size_t)rows * kKvTile));
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_ml, sizeof(float2) * (size_t)rows));
-      const uint64_t width = (uint64_t)d.heads_kv * d.head_dim;
-      const uint64_t dims[2] = {width, (uint64_t)d.num_rows}, strides[1] = {2 * width};
-      const uint32_t box[2] = {64, 1};
-      if (int rc = encode_map(&kv->pool_map, pv.d_pool, pv.dtype, 2, dims, strides, box)) return rc;
     }
     CUDA_TRY(cudaMemsetAsync(d_arrays, 0, sizeof(int32_t) * (size_t)ints, pv.compute));
     CUDA_TRY(cudaMemsetAsync(d_table, 0xff,
@@ -372,7 +367,6 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   // chunks are possible where one request may bring more than kKvChunkRows rows
   const bool chunks = kv->tpt > 0 && (int64_t)std::min(kv->max_new, kv->T) * group > kKvChunkRows;
   if (chunks) {
-    a.pool_map = kv->pool_map;
     const uint64_t dims[3] = {(uint64_t)kv->dev.head_dim, (uint64_t)kv->dev.heads_q, (uint64_t)kv->T};
     const uint64_t strides[2] = {2 * (uint64_t)kv->dev.head_dim, 2 * (uint64_t)ldq};
     const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)kv->tpt};

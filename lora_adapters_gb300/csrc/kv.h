@@ -114,7 +114,6 @@ struct KvAttendArgs {
   int32_t tpt;                   // kv_chunk_tokens
   float* tc_part_o;              // [kv_chunk_part_rows][kKvTile]
   float2* tc_part_ml;
-  CUtensorMap pool_map;          // token rows of the pool, box {64, 1}
   CUtensorMap q_map;             // q as [T][heads_q][head_dim], box {64, group, tpt}
 };
 int64_t kv_chunk_part_rows(int num_sms);
