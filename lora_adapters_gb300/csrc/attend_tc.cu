@@ -45,11 +45,15 @@ using namespace ptx;
 constexpr int kRowBytes = 128;                  // 64 elements, one swizzle row
 constexpr int kAtom = kKvTile * kRowBytes;      // 128 rows x 64 elements: 16 KB
 constexpr int kMaxAtoms = 2;                    // head_dim <= 128
-constexpr int kStages = 5;                      // K and V tiles in flight
-// warps: 0-3 K and V, 4-7 softmax of tile A, 8-11 of tile B, 12 MMAs, 13 Q
+constexpr int kStages = 4;                      // K and V tiles in flight
+constexpr int kQTiles = 3;                      // Q tiles: two in use, one for the next part
+// warps: 0-3 K and V, 4-7 softmax of tile A, 8-11 of tile B, 12 MMAs, 13 Q,
+// 14 the walk
 constexpr int kThreads = 16 * 32;
 constexpr int kLoaders = 4 * 32;
-constexpr int kWarpMma = 12, kWarpQ = 13;
+constexpr int kWarpMma = 12, kWarpQ = 13, kWarpWalk = 14;
+constexpr int kParts = 4;                       // parts handed out ahead
+constexpr int kPartReaders = 4 + 8 + 2;         // warps that read them
 // Registers a thread of each warp group (setmaxnreg): the launch gives each of
 // the four groups 128, and the shares add up to the same 512.
 constexpr int kRegsLoad = 48, kRegsSoftmax = 192, kRegsOther = 80;
@@ -62,18 +66,11 @@ constexpr float kGrow = 8.f;                    // O is rescaled when a maximum 
 // microseconds when all is well.
 constexpr uint32_t kPolls = 1u << 20;
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kPolls; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
-
-struct TcSmem {
-  uint8_t q[2][kMaxAtoms][kAtom];
-  uint8_t kv[kStages][kMaxAtoms][kAtom];
-  uint64_t q_full, q_empty, kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint32_t tmem_slot;
-};
 
 __device__ __forceinline__ void report_err(int32_t* err, int code) {
   if (err) atomicCAS(err, 0, code);
@@ -185,13 +182,16 @@ __device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint32_t q, uint32_t k
 }
 
 // A part of a segment: one request, key head and pair of tiles, key tiles
-// [i0, i1) of n.
-struct Part {
-  int r, hk, pr;           // request, key head, pair of tiles
-  int i0, i1, n;           // key tiles of this part, of the segment
-  int q0, fresh, ctx;      // the request's first token, new tokens, tokens before them
+// [i0, i1) of n.  One warp walks the CTA's run and hands the parts to the other
+// roles through shared memory, a few ahead.
+struct alignas(16) Part {
+  int i0, i1;              // key tiles of this part (i1 = 0: the run is over)
+  int end[2];              // one past the last key tile that tile A (B) of the pair needs, i0: none
+  int tok, pos, tokens[2]; // the pair's first token and its position; tokens of tile A, of tile B
+  int hk, row, len, whole; // key head; table row; tokens held; the segment lies in this part as a whole
 };
-// Walks a CTA's run of units part by part; every role walks it for itself.
+static_assert(sizeof(Part) == 48, "three 16-byte pieces");
+// Walks a CTA's run of units part by part.
 struct Walk {
   int left;                // units of the run not yet walked
   int r, hk, pr, i0;       // where the next part starts
@@ -221,22 +221,30 @@ __device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t u, int
   for (int n; w.i0 >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)) && n > 0; ++w.pr) w.i0 -= n;
   return w;
 }
-__device__ __forceinline__ bool walk_next(const KvAttendArgs& a, Walk& w, Part& p) {
-  if (w.left <= 0) return false;
+__device__ __forceinline__ Part walk_next(const KvAttendArgs& a, Walk& w) {
+  Part p{};
+  if (w.left <= 0) return p;
   const KvDev& d = a.kv;
-  p.r = w.r;
-  p.hk = w.hk;
-  p.pr = w.pr;
-  p.q0 = __ldg(d.q_start + w.r);
-  p.fresh = __ldg(d.q_start + w.r + 1) - p.q0;
-  p.ctx = __ldg(d.kv_len + w.r) - p.fresh;
-  p.n = pair_tiles(p.ctx, p.fresh, a.tpt, w.pr);
+  const int q0 = __ldg(d.q_start + w.r), fresh = __ldg(d.q_start + w.r + 1) - q0;
+  p.len = __ldg(d.kv_len + w.r);
+  p.row = __ldg(d.row + w.r);
+  const int ctx = p.len - fresh, t0 = w.pr * 2 * a.tpt, n = pair_tiles(ctx, fresh, a.tpt, w.pr);
   p.i0 = w.i0;
-  p.i1 = min(p.n, p.i0 + w.left);
+  p.i1 = min(n, p.i0 + w.left);
+  p.tok = q0 + t0;
+  p.pos = ctx + t0;
+  p.hk = w.hk;
+  p.whole = p.i0 == 0 && p.i1 == n;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    p.tokens[x] = max(0, min(a.tpt, fresh - t0 - x * a.tpt));
+    p.end[x] = p.tokens[x] == 0 ? p.i0
+                                : max(p.i0, min(p.i1, (p.pos + x * a.tpt + p.tokens[x] + kKvTile - 1) / kKvTile));
+  }
   w.left -= p.i1 - p.i0;
   w.i0 = 0;
   if (w.left > 0) {                 // the next pair, key head or request with tiles
-    if (++w.pr * 2 * a.tpt >= p.fresh) {
+    if (++w.pr * 2 * a.tpt >= fresh) {
       w.pr = 0;
       if (++w.hk == d.heads_kv) {
         w.hk = 0;
@@ -245,16 +253,18 @@ __device__ __forceinline__ bool walk_next(const KvAttendArgs& a, Walk& w, Part& 
       }
     }
   }
-  return true;
+  return p;
 }
-// One past the last key tile of this part that tile x of the pair needs (i0:
-// none), and the tile's tokens.
-__device__ __forceinline__ int tile_end(const Part& p, int tpt, int x, int* tokens) {
-  const int t0 = (p.pr * 2 + x) * tpt;
-  *tokens = max(0, min(tpt, p.fresh - t0));
-  if (*tokens == 0) return p.i0;
-  return max(p.i0, min(p.i1, (p.ctx + t0 + *tokens + kKvTile - 1) / kKvTile));
-}
+
+struct TcSmem {
+  uint8_t q[kQTiles][kMaxAtoms][kAtom];
+  uint8_t kv[kStages][kMaxAtoms][kAtom];
+  uint64_t q_full[kQTiles], q_empty[kQTiles], kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t part_full[kParts], part_empty[kParts];
+  Part part[kParts];
+  uint32_t tmem_slot;
+};
 
 // STEPS: 16-element steps of a head, 8 or 4; 0: head_dim 80, 96 or 112 (a
 // branch to the right run of MMAs costs 7 % of the kernel).
@@ -269,11 +279,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   if ((int64_t)blockIdx.x * run >= total) return;
   if (warp == kWarpMma) tmem_alloc(&sm.tmem_slot, kTmemCols);
   if (threadIdx.x == 0) {
-    mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.kv_full[s], kLoaders);
       mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int k = 0; k < kParts; ++k) {
+      mbar_init(&sm.part_full[k], 1);
+      mbar_init(&sm.part_empty[k], kPartReaders);
+    }
+    for (int b = 0; b < kQTiles; ++b) {
+      mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.q_empty[b], 4);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.s_full[x], 1);
@@ -290,12 +306,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   const int dim = d.head_dim, group = d.heads_q / d.heads_kv, tpt = a.tpt;
   const int natoms = (dim + 63) >> 6;
   bool ok = true;
-  auto wait_lane0 = [&](uint64_t* bar, uint32_t parity) -> bool {
-    bool got = true;
-    if (lane == 0) got = wait_bar(bar, parity);
-    return __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+  // by a whole warp: every lane polls (one lane polling and a shuffle that
+  // tells the others cost 6 % of the kernel)
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
   };
-  Walk w = walk_start(a, (int64_t)blockIdx.x * run, min(total, (int64_t)(blockIdx.x + 1) * run));
+  // the reader's next part (false: no more, or a wait gave up): copied out of
+  // the ring by every lane, handed back by one
+  uint32_t n_part = 0;
+  auto next_part = [&](Part& p, bool whole_warp) -> bool {
+    const uint32_t k = n_part % kParts, ph = (n_part / kParts) & 1;
+    if (!ok || !(whole_warp ? wait_warp(&sm.part_full[k], ph) : wait_bar(&sm.part_full[k], ph))) {
+      ok = false;
+      return false;
+    }
+    ++n_part;
+    p = sm.part[k];
+    return true;
+  };
+  auto part_read = [&]() { mbar_arrive(&sm.part_empty[(n_part - 1) % kParts]); };
   Part p;
 
   if (warp < 4) {  // -------------------------------------------------- K and V tiles
@@ -310,14 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const int ch = lane & 7, sub = lane >> 3;
     const bool ch1 = 64 + ch * 8 < dim;              // this lane's piece of the second atom exists
     uint32_t n = 0;      // tiles issued
-    while (ok && walk_next(a, w, p)) {
-      const int len = p.ctx + p.fresh;
-      const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)__ldg(d.row + p.r) * d.max_blocks;
+    for (;;) {
+      if (!next_part(p, true)) break;
+      __syncwarp();
+      if (lane == 0) part_read();
+      if (p.i1 == 0) break;
+      const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)p.row * d.max_blocks;
       const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)p.hk * dim * 2 + ch * 16;
       int kslot, vslot;
       auto lookup = [&](int i) {
         int j = i * kKvTile + 32 * warp + lane;
-        j = j < len ? j : 0;
+        j = j < p.len ? j : 0;
         const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
         const int kp = __ldg(tab + b), vp = __ldg(tab + plane + b);
         // an entry that names no page: row 0, as the request's result is
@@ -332,8 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
 #pragma unroll
         for (int half = 0; half < 2; ++half, ++n) {
           const uint32_t st = n % kStages;
-          if (!wait_bar(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) ok = false;
-          if (!__all_sync(0xffffffffu, ok)) {
+          if (!wait_warp(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -350,29 +381,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
           cp_arrive(&sm.kv_full[st]);
         }
       }
+      if (!ok) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 12) {
     regs_down<kRegsOther>();
     if (warp == kWarpQ) {  // ----------------------------------------------- Q tiles
-      uint32_t n = 0;
-      while (ok && walk_next(a, w, p)) {
-        if (!wait_lane0(&sm.q_empty, (n & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const int t0 = p.pr * 2 * tpt;
-          const int tiles = p.fresh - t0 > tpt ? 2 : 1;
-          mbar_expect_tx(&sm.q_full, (uint32_t)(tiles * natoms * tpt * group) * kRowBytes);
-          for (int x = 0; x < tiles; ++x)
+      if (elect_one()) {
+        uint32_t n = 0;      // tiles loaded
+        while (next_part(p, false)) {
+          part_read();
+          if (p.i1 == 0) break;
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (p.end[x] == p.i0) continue;      // no keys for this tile here
+            const uint32_t b = n % kQTiles;
+            ok = wait_bar(&sm.q_empty[b], ((n / kQTiles) & 1) ^ 1);
+            if (!ok) break;
+            mbar_expect_tx(&sm.q_full[b], (uint32_t)(natoms * tpt * group) * kRowBytes);
             for (int at = 0; at < natoms; ++at)
-              tma_load_3d(sm.q[x][at], &a.q_map, at * 64, p.hk * group, p.q0 + t0 + x * tpt, &sm.q_full);
+              tma_load_3d(sm.q[b][at], &a.q_map, at * 64, p.hk * group, p.tok + x * tpt, &sm.q_full[b]);
+            ++n;
+          }
         }
-        __syncwarp();
-        ++n;
+        for (uint32_t k = n > kQTiles ? n - kQTiles : 0; k < n; ++k)   // copies land before the CTA goes
+          wait_bar(&sm.q_full[k % kQTiles], (k / kQTiles) & 1);
       }
-      if (n > 0) wait_lane0(&sm.q_full, (n - 1) & 1);   // the last copy has landed before the CTA goes
+    } else if (warp == kWarpWalk) {  // ------------------------------------- the walk, by one thread
+      if (elect_one()) {
+        Walk w = walk_start(a, (int64_t)blockIdx.x * run, min(total, (int64_t)(blockIdx.x + 1) * run));
+        for (uint32_t k = 0;; ++k) {
+          const Part q = walk_next(a, w);
+          ok = wait_bar(&sm.part_empty[k % kParts], ((k / kParts) & 1) ^ 1);
+          if (!ok) break;
+          sm.part[k % kParts] = q;
+          mbar_arrive(&sm.part_full[k % kParts]);
+          if (q.i1 == 0) break;
+        }
+      }
     } else if (warp == kWarpMma && elect_one()) {  // ----------------------- MMAs, by one thread
       const uint32_t id_s = umma_idesc_f16(kKvTile, kKvTile, Elem<E>::kBf16, false);
       const uint32_t id_o = umma_idesc_f16(kKvTile, dim, Elem<E>::kBf16, true);
@@ -381,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       const uint32_t q_desc = desc_lo(sm.q[0][0], 16), k_desc = desc_lo(sm.kv[0][0], 16),
                      v_desc = desc_lo(sm.kv[0][0], kAtom);
       constexpr uint32_t kTileUnits = kMaxAtoms * kAtom / 16;
-      uint32_t st = 0, ph = 0, q_ph = 0;        // the ring's next tile; Q's phase
+      uint32_t st = 0, ph = 0;                  // the ring's next tile
       uint32_t p_ph = 0, o_ph = 3;              // a bit per tile: the phase to wait for
-      auto issue_s = [&](int x, uint32_t kst) {
-        const uint32_t qd = q_desc + x * kTileUnits, kd = k_desc + kst * kTileUnits;
+      uint32_t nq = 0;                          // Q tiles used
+      auto issue_s = [&](int x, uint32_t qb, uint32_t kst) {
+        const uint32_t qd = q_desc + qb * kTileUnits, kd = k_desc + kst * kTileUnits;
         const uint32_t ts = tmem + x * 128;
         if constexpr (STEPS > 0) {
           issue_qk<STEPS>(ts, qd, kd, id_s);
@@ -403,11 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         for (int ks = 0; ks < kKvTile / 16; ++ks)
           umma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + ks * (16 * kRowBytes / 16), id_o, ks ? 1u : add);
       };
-      while (ok && walk_next(a, w, p)) {
-        int tok;
-        const int end0 = tile_end(p, tpt, 0, &tok), end1 = tile_end(p, tpt, 1, &tok);
-        ok = wait_bar(&sm.q_full, q_ph);
-        q_ph ^= 1;
+      while (next_part(p, false)) {
+        part_read();
+        if (p.i1 == 0) break;
+        const int end0 = p.end[0], end1 = p.end[1];
+        const uint32_t n0 = nq, n1 = nq + (end0 > p.i0);    // the tiles' places in the order of loads
+        nq = n1 + (end1 > p.i0);
+        const uint32_t qb0 = n0 % kQTiles, qb1 = n1 % kQTiles;
         // K tile i + 1 and V tile i, in the order they were loaded (K i0, V i0, K i0 + 1, ...)
         for (int i = p.i0 - 1; i < p.i1 && ok; ++i) {
           const bool has_v = i >= p.i0, has_k = i + 1 < p.i1;
@@ -432,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
                 o_ph ^= 1u << x;
               }
               ok = ok && wait_bar(&sm.p_full[x], (p_ph >> x) & 1);
-              p_ph ^= 1u << x;
               tc_fence_after();
               fence_async_shared();   // the tile's copies (generic proxy), for the MMAs' reads
+              p_ph ^= 1u << x;
               if (ok) {
                 issue_o(x, vst, i > p.i0 ? 1u : 0u);
                 if (i == end - 1) umma_commit(&sm.o_full[x]);
@@ -446,7 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
               tc_fence_after();
               fence_async_shared();
             }
-            if (ok && i + 1 < end) issue_s(x, kst);
+            if (ok && i + 1 < end) {
+              if (!has_v) {             // the part's first: this tile's queries
+                ok = wait_bar(&sm.q_full[x ? qb1 : qb0], ((x ? n1 : n0) / kQTiles) & 1);
+              }
+              if (ok) issue_s(x, x ? qb1 : qb0, kst);
+            }
           }
           if (!ok) break;
           if (has_v) umma_commit(&sm.kv_empty[vst]);
@@ -456,7 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
             ph ^= 1;
           }
         }
-        if (ok) umma_commit(&sm.q_empty);
       }
     }
     __syncwarp();
@@ -468,51 +520,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const float sc = CAP ? 2.f * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
     const float cap2 = a.softcap * kLog2e;
     const int my_tok = rho / group, my_head = rho - my_tok * group;
-    uint32_t ns = 0, nf = 0;
-    while (ok && walk_next(a, w, p)) {
-      int tokens;
-      const int end = tile_end(p, tpt, x, &tokens);
-      const int t0 = (p.pr * 2 + x) * tpt;
+    uint32_t ns = 0, nf = 0, nq = 0;
+    for (;;) {
+      if (!next_part(p, true)) break;
+      __syncwarp();
+      if (lane == 0) part_read();
+      if (p.i1 == 0) break;
+      const int end = x ? p.end[1] : p.end[0], tokens = x ? p.tokens[1] : p.tokens[0];
+      const uint32_t has0 = p.end[0] > p.i0, has1 = p.end[1] > p.i0, qb = (nq + (x ? has0 : 0)) % kQTiles;
+      nq += has0 + has1;
       const bool live = my_tok < tokens;
-      const int pos = p.ctx + t0 + min(my_tok, max(tokens - 1, 0));
-      const int pos_first = p.ctx + t0;                       // the tile's earliest position
+      const int pos_first = p.pos + x * tpt;                  // the tile's earliest position
+      const int pos = pos_first + min(my_tok, max(tokens - 1, 0));
       float m = -INFINITY;
       uint64_t l2a = 0, l2b = 0;                              // pairs of partial sums (+0, +0)
       for (int i = p.i0; i < end; ++i) {
-        if (!wait_lane0(&sm.s_full[x], ns & 1)) {
+        if (!wait_warp(&sm.s_full[x], ns & 1)) {
           ok = false;
           break;
         }
         ++ns;
         tc_fence_after();
+        // S, 32 columns at a time: the next ones on their way while these are
+        // capped, masked and searched for the maximum
         uint32_t s[4][32];
+        const int lim = pos - i * kKvTile;
+        const bool edge = (i + 1) * kKvTile - 1 > pos_first;  // some row may not see the whole tile
+        float mx = -INFINITY, my = -INFINITY;
+        tmem_ld32_nowait(t_s, s[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + 32 * c, s[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-        if (CAP) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c]);
+          if (c < 3) tmem_ld32_nowait(t_s + 32 * (c + 1), s[c + 1]);
+          if (CAP) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               s[c][j] = __float_as_uint(cap2 - 2.f * cap2 * __fdividef(1.f, 1.f + ex2(__uint_as_float(s[c][j]) * sc)));
-        }
-        if ((i + 1) * kKvTile - 1 > pos_first) {              // some row may not see the whole tile
-          const int lim = pos - i * kKvTile;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+          }
+          if (edge) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (32 * c + j > lim) s[c][j] = 0xff800000u;    // -inf
-        }
-        float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+          }
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             mx = max3(mx, __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
             my = max3(my, __uint_as_float(s[c][j + 2]), __uint_as_float(s[c][j + 3]));
           }
+        }
         mx = fmaxf(mx, my);
         if (!CAP) mx *= sc;                                   // scale > 0; -inf stays
         if (i == p.i0) {
@@ -524,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
           m = mn;
           l2a = fma2(l2a, pair(f, f), 0);
           l2b = fma2(l2b, pair(f, f), 0);
+#pragma unroll 1
           for (int c = 0; c < dim; c += 16) {
             float v[16];
             uint32_t r[16];
@@ -558,41 +614,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       if (!ok) break;
       const float2 la = unpair(l2a), lb = unpair(l2b);
       const float l = (la.x + la.y) + (lb.x + lb.y);
-      const bool whole = p.i0 == 0 && p.i1 == p.n;
+      const bool whole = p.whole != 0;
       // slot 0: the segment began in an earlier run; slot 1: it begins here
       const int64_t part = (((int64_t)blockIdx.x * 2 + (p.i0 == 0 ? 1 : 0)) * 2 + x) * kKvTile + rho;
       if (end > p.i0) {
-        if (!wait_lane0(&sm.o_full[x], nf & 1)) {
+        if (!wait_warp(&sm.o_full[x], nf & 1)) {
           ok = false;
           break;
         }
         ++nf;
         tc_fence_after();
+        // The tile's rows leave through its queries' place in shared memory
+        // (their last product is done), 256 bytes a row in 16-byte pieces, the
+        // piece's place exchanged by the row's low bits: each warp writes its
+        // own 32 rows one row a lane and reads them back row by row, so that
+        // global memory sees whole rows.
+        uint8_t* stage = sm.q[qb][0] + 32 * quarter * 256;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint16_t* dst = a.out + (int64_t)(p.q0 + t0 + my_tok) * a.ldo + (int64_t)(p.hk * group + my_head) * dim;
-        for (int c = 0; c < dim; c += 16) {
-          float v[16];
-          tmem_ld16(t_o + c, v);
-          if (live) {
-            if (whole) {
-              float y[8];
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.tok + x * tpt + my_tok) * a.ldo +
+                                                          (int64_t)(p.hk * group + my_head) * dim)
+                             : reinterpret_cast<uint8_t*>(a.tc_part_o + part * kKvTile);
+        const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
+        const int piece = lane & 15;
+        uint8_t* mine = stage + lane * 256;
+        // (loops kept rolled: code run once per part is fetched as it runs)
+        auto store_rows = [&](int byte0, int bytes) {
+          __syncwarp();
+#pragma unroll 1
+          for (int r0 = lane >> 4; r0 < 32; r0 += 8) {
+            uint4 v[4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+            for (int k = 0; k < 4; ++k) {
+              const int rr = r0 + 2 * k;
+              v[k] = *reinterpret_cast<const uint4*>(stage + rr * 256 + (piece ^ (rr & 7)) * 16);
+            }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = v[8 * h + j] * inv;
-                *reinterpret_cast<uint4*>(dst + c + 8 * h) = pack8<E>(y);
-              }
-            } else {
-              float4* po = reinterpret_cast<float4*>(a.tc_part_o + part * kKvTile + c);
-#pragma unroll
-              for (int h = 0; h < 4; ++h) po[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            for (int k = 0; k < 4; ++k) {
+              const int rr = r0 + 2 * k;
+              uint8_t* to = reinterpret_cast<uint8_t*>(
+                  __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+              if (((rows_live >> rr) & 1) && piece * 16 < bytes) *reinterpret_cast<uint4*>(to + byte0 + piece * 16) = v[k];
             }
           }
           __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {      // 32 columns (beyond head_dim: whatever is there, not stored)
+          uint32_t o[32];
+          tmem_ld32_nowait(t_o + 32 * c, o);
+          tmem_wait_ld(o);
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float y[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(o[k * 8 + j]) * inv;
+              *reinterpret_cast<uint4*>(mine + ((4 * c + k) ^ (lane & 7)) * 16) = pack8<E>(y);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(mine + ((8 * (c & 1) + k) ^ (lane & 7)) * 16) =
+                  make_uint4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
+            if (c & 1) store_rows(128 * (c - 1), dim * 4 - 128 * (c - 1));
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_empty[x]);
+        if (lane == 0) mbar_arrive(&sm.o_empty[x]);        // the next part's products may start
+        if (whole) store_rows(0, dim * 2);
+        fence_async_shared();      // the next queries come through the TMA engine
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
       }
       if (!whole && live) a.tc_part_ml[part] = make_float2(m, l);   // m = -inf: the part has no weight, O unwritten
     }
