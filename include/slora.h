@@ -512,7 +512,8 @@ typedef struct slora_kv_batch {
  * stream: a row that starts with another row's entries shares that prefix.
  * page_elems must be a multiple of heads_kv * head_dim.  Batches are of at
  * most the pool's max_tokens tokens.  d_arrays: caller-owned device memory,
- * int32, as many as slora_kv_array_ints says, zeroed here; the batch arrays.
+ * int32, 16-byte aligned, as many as slora_kv_array_ints says, zeroed here; the
+ * batch arrays.
  * Both must outlive the cache.  Allocates the rotary table and the
  * attention's scratch with cudaMalloc.
  */

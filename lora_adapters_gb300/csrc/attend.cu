@@ -43,9 +43,7 @@ namespace {
 constexpr int kDecWarps = 4;             // per CTA
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecCtas = 3;              // per SM: 170 registers a thread
-constexpr int kDecMinUnits = 2;          // shortest run: 32 tokens
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kDecMinUnits = 1;          // shortest run (one 640-token request: 12.5 us with 1, 13.0 with 2, 15.6 with 4)
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -94,13 +92,17 @@ __device__ __forceinline__ DecSplit dec_split(int units, int blocks, int64_t gro
   s.run = max((int64_t)kDecMinUnits, (s.total + groups - 1) / groups);
   return s;
 }
-// Largest r with off[r] <= x.
+// Largest r with off[r] * blocks <= x, by a whole warp: the lanes look at 32
+// places of what is left at a time.
 __device__ __forceinline__ int find_request(const int32_t* off, int R, int64_t x, int blocks) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)off[mid] * blocks <= x) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = R;               // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = lane * step;
+    const bool le = i < n && (int64_t)__ldg(off + lo + i) * blocks <= x;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);   // off[lo] <= x always
+    n = min(step, n - k * step);
+    lo += k * step;
   }
   return lo;
 }
@@ -111,19 +113,15 @@ __global__ void __launch_bounds__(kDecThreads, D <= 128 ? kDecCtas : 2)
 kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int NB = D / 64;        // 64-element blocks of a head (V)
   constexpr int NC = D / 32;        // 32-element chunks of a head (K, Q)
-  __shared__ int32_t off[kKvMaxRequests + 1];
   const KvDev& d = a.kv;
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int i = tid; i <= a.R; i += kDecThreads) off[i] = d.dec_off[i];
-  __syncthreads();
   const int hbw = a.hbw, blocks = d.heads_kv / hbw;
   const int64_t gw = (int64_t)blockIdx.x * kDecWarps + (tid >> 5);
   const int64_t groups = (int64_t)gridDim.x * kDecWarps / hbw;
-  const DecSplit sp = dec_split(off[a.R], blocks, groups);
+  const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, groups);
   const int64_t g = gw / hbw;
   int64_t u = g * sp.run;
   const int64_t u1 = min(sp.total, u + sp.run);
-  if (u >= u1) return;
   const int hsub = (int)(gw - g * hbw);
 
   const int dim = d.head_dim, P = d.per_page, group = d.heads_q / d.heads_kv;
@@ -132,18 +130,25 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
   const float sc = CAP ? 2.f * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
   const float cap2 = a.softcap * kLog2e;
-  int r = find_request(off, a.R, u, blocks);
+  int r = u < u1 ? find_request(d.dec_off, a.R, u, blocks) : 0;
 
   while (u < u1) {
-    while ((int64_t)off[r + 1] * blocks <= u) ++r;      // requests without units are passed over
-    const int len = d.kv_len[r], q0 = d.q_start[r], rows = (d.q_start[r + 1] - q0) * group;
+    int off = __ldg(d.dec_off + r), off_next = __ldg(d.dec_off + r + 1);
+    int4 rq = __ldg(d.req + r);
+    while ((int64_t)off_next * blocks <= u) {           // requests without units are passed over
+      ++r;
+      off = off_next;
+      off_next = __ldg(d.dec_off + r + 1);
+      rq = __ldg(d.req + r);
+    }
+    const int len = rq.z, q0 = rq.x, rows = rq.y * group;
     const int nchunk = (len + 15) >> 4, tiles = (rows + kKvRowTile - 1) / kKvRowTile;
-    const int64_t in_req = u - (int64_t)off[r] * blocks;
+    const int64_t in_req = u - (int64_t)off * blocks;
     const int seg = (int)(in_req / nchunk), c0 = (int)(in_req - (int64_t)seg * nchunk);
     const int hb = seg / tiles, rt = seg - hb * tiles;
     const int c1 = (int)min((int64_t)nchunk, c0 + (u1 - u));
     const int hk = hb * hbw + hsub;
-    const int ctx = len - rows / group;
+    const int ctx = len - rq.y;
     // ---- this tile's queries: row n of the tile is (token, head of the group)
     uint32_t qf[NC][4];
     {
@@ -172,7 +177,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     // lanes 0-15 look up the K rows of a unit's tokens, lanes 16-31 the V rows
-    const int32_t* tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)d.row[r] * d.max_blocks;
+    const int32_t* tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)rq.w * d.max_blocks;
     auto lookup = [&](int c) -> int {
       const int j = c * 16 + (lane & 15);
       if (c >= c1 || j >= len) return -1;
@@ -317,173 +322,223 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     }
     u += c1 - c0;
   }
+  // after chunks: their kernel may still run, and this grid ends after it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// The parts of every split segment added up, in the order of the cache.  Every
-// CTA lists the split segments for itself (each thread looks at some of the
-// borders between runs), then takes (segment, head, row) items; its warps take
-// every kJoinWarps-th part, and the warps' sums are added in warp order.
-struct JoinItem {
-  int32_t r, seg;        // request; block of heads * tiles + row tile
-  int32_t first, last;   // groups of warps that hold its parts
-};
-constexpr int kJoinList = 512;      // borders looked at per round
+// The parts of the split segments, joined in the order of the cache.  Decode:
+// an item is one row (request, token, query head); where it was split follows
+// from the same sums the decode kernel divides its work by.  A warp per item;
+// with few requests, whose segments have many parts each, a block per item,
+// its warps taking every so-many-th part.  Chunks: a warp per row.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWideWarps = 16;
 
-template <class E, int D>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvAttendArgs a,
-                                                               const int64_t groups) {
+template <int V>
+struct JoinSum {
+  float m = -INFINITY, l = 0.f, o[V] = {};
+  // (a part with m = -inf has no weight, and its sums may not have been written)
+  __device__ __forceinline__ void add(float2 ml, const float (&y)[V]) {
+    if (ml.x == -INFINITY) return;
+    const float mn = fmaxf(m, ml.x), f = ex2(m - mn), w = ex2(ml.x - mn);
+    m = mn;
+    l = l * f + ml.y * w;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = o[j] * f + y[j] * w;
+  }
+};
+// A lane's elements of a row of `cols` floats: 4 consecutive ones of every 128
+// (2 of 64), as floats j of y.
+template <int V>
+__device__ __forceinline__ void load_row(const float* row, int lane, float (&y)[V]) {
+  if constexpr (V == 2) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(row) + lane);
+    y[0] = v.x; y[1] = v.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(row + j * 128) + lane);
+      y[4 * j] = v.x; y[4 * j + 1] = v.y; y[4 * j + 2] = v.z; y[4 * j + 3] = v.w;
+    }
+  }
+}
+template <class E, int V>
+__device__ __forceinline__ void store_row(uint16_t* row, int lane, int dim, const float (&o)[V], float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if constexpr (V == 2) {
+    if (lane * 2 < dim) *reinterpret_cast<uint32_t*>(row + lane * 2) = Elem<E>::from2(o[0] * inv, o[1] * inv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j)
+      if (j * 128 + lane * 4 < dim)
+        *reinterpret_cast<uint2*>(row + j * 128 + lane * 4) =
+            make_uint2(Elem<E>::from2(o[4 * j] * inv, o[4 * j + 1] * inv),
+                       Elem<E>::from2(o[4 * j + 2] * inv, o[4 * j + 3] * inv));
+  }
+}
+
+template <class E, int D, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kJoinWideWarps * 32 : kJoinThreads)
+kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
   constexpr int V = D / 32;      // elements per lane
-  __shared__ int32_t off[kKvMaxRequests + 1];
-  __shared__ JoinItem items[kJoinList];
-  __shared__ int32_t start[kJoinList + 1];     // first (head, row) item of each listed segment
-  __shared__ int32_t warp_n[kJoinWarps];
-  __shared__ __align__(16) float s_o[kJoinWarps][D];
-  __shared__ float2 s_ml[kJoinWarps];
+  constexpr int W = WIDE ? kJoinWideWarps : 1;
+  __shared__ float s_o[W][D];
+  __shared__ float s_f[W], s_m[W], s_l[W];
   const KvDev& d = a.kv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i <= a.R; i += kJoinThreads) off[i] = d.dec_off[i];
-  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hbw = a.hbw, blocks = d.heads_kv / hbw, group = d.heads_q / d.heads_kv, dim = d.head_dim;
-  const DecSplit sp = dec_split(off[a.R], blocks, groups);
+  const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, groups);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t borders = (sp.total + sp.run - 1) / sp.run - 1;    // run g + 1 starts at (g + 1) * sp.run
-  for (int64_t b0 = 0; b0 < borders; b0 += kJoinList) {
-    // ---- list: a segment is listed by the first border inside it
-    __syncthreads();
-    for (int i = tid; i < kJoinList; i += kJoinThreads) {
-      JoinItem it{-1, 0, 0, 0};
-      const int64_t g = b0 + i + 1;
-      if (g <= borders) {
-        const int64_t u = g * sp.run;
-        int r = find_request(off, a.R, u, blocks);
-        while ((int64_t)off[r + 1] * blocks <= u) ++r;
-        const int nchunk = (d.kv_len[r] + 15) >> 4;
-        const int64_t in_req = u - (int64_t)off[r] * blocks;
-        const int seg = (int)(in_req / nchunk);
-        const int64_t us = (int64_t)off[r] * blocks + (int64_t)seg * nchunk;
-        if (us < u && (g - 1) * sp.run <= us)
-          it = JoinItem{r, seg, (int32_t)(g - 1), (int32_t)((us + nchunk - 1) / sp.run)};
+  // items: request, row, key head (fastest)
+  const int per_req = a.rows * d.heads_kv;
+  const int64_t items = (int64_t)a.R * per_req, stride = (int64_t)gridDim.x * (WIDE ? 1 : blockDim.x / 32);
+  for (int64_t it = WIDE ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / 32) + warp; it < items; it += stride) {
+    const int r = (int)(it / per_req), in = (int)(it - (int64_t)r * per_req), row = in / d.heads_kv,
+              hk = in - row * d.heads_kv;
+    const int4 rq = __ldg(d.req + r);
+    const int off = __ldg(d.dec_off + r), off_next = __ldg(d.dec_off + r + 1);
+    const int rows = rq.y * group;
+    if (row >= rows || off == off_next) continue;         // no such row, or a chunk
+    const int nchunk = (rq.z + 15) >> 4, tiles = (rows + kKvRowTile - 1) / kKvRowTile, n = row % kKvRowTile;
+    const int hb = hk / hbw, hsub = hk - hb * hbw;
+    const int64_t us = (int64_t)off * blocks + (int64_t)(hb * tiles + row / kKvRowTile) * nchunk;
+    const int64_t g0 = us / sp.run, g1 = (us + nchunk - 1) / sp.run;
+    if (g0 == g1) continue;                               // the decode kernel wrote it
+    JoinSum<V> s;
+    for (int64_t g = g0 + (WIDE ? warp : 0); g <= g1; g += 4 * W) {   // four parts on their way at a time
+      float2 ml[4];
+      float y[4][V];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        const int64_t gk = g + k * W;
+        if (gk <= g1) {
+          const int64_t part = ((gk * hbw + hsub) * 2 + (gk == g0 ? 1 : 0)) * kKvRowTile + n;
+          ml[k] = __ldcg(a.part_ml + part);
+          load_row<V>(a.part_o + part * D, lane, y[k]);
+        }
       }
-      items[i] = it;
-      int n = 0;
-      if (it.r >= 0) {
-        const int rows = (d.q_start[it.r + 1] - d.q_start[it.r]) * group;
-        const int tiles = (rows + kKvRowTile - 1) / kKvRowTile;
-        n = hbw * min(kKvRowTile, rows - (it.seg % tiles) * kKvRowTile);
-      }
-      start[i] = n;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s.add(ml[k], y[k]);
     }
-    __syncthreads();
-    if (warp == 0) {       // exclusive sums of the item counts
-      int run = 0;
-      for (int i = lane; i < kJoinList; i += 32) {
-        const int n = start[i];
-        int inc = n;
+    uint16_t* dst = a.out + (int64_t)(rq.x + row / group) * a.ldo + (int64_t)(hk * group + row % group) * dim;
+    if constexpr (!WIDE) {
+      store_row<E, V>(dst, lane, dim, s.o, s.l);
+    } else {                                              // the warps' sums, in their order
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        start[i] = run + inc - n;
-        run += __shfl_sync(0xffffffffu, inc, 31);
+      for (int j = 0; j < V; ++j) s_o[warp][j * 32 + lane] = s.o[j];
+      if (lane == 0) {
+        s_m[warp] = s.m;
+        s_l[warp] = s.l;
       }
-      if (lane == 0) start[kJoinList] = run;
-    }
-    __syncthreads();
-    const int total = start[kJoinList];
-    for (int x = blockIdx.x; x < total; x += gridDim.x) {
-      int lo = 0, hi = kJoinList - 1;          // the last segment that starts at or before x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= x) lo = mid;
-        else hi = mid - 1;
-      }
-      const JoinItem it = items[lo];
-      const int q0 = d.q_start[it.r], rows = (d.q_start[it.r + 1] - q0) * group;
-      const int tiles = (rows + kKvRowTile - 1) / kKvRowTile;
-      const int rt = it.seg % tiles, hsub = (x - start[lo]) % hbw, n = (x - start[lo]) / hbw;
-      const int hk = (it.seg / tiles) * hbw + hsub, row = rt * kKvRowTile + n;
-      float m = -INFINITY, l = 0.f;
-      alignas(16) float o[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = 0.f;
-#pragma unroll 4
-      for (int g = it.first + warp; g <= it.last; g += kJoinWarps) {
-        const int64_t part = (((int64_t)g * hbw + hsub) * 2 + (g == it.first ? 1 : 0)) * kKvRowTile + n;
-        const float2 ml = __ldcg(a.part_ml + part);
-        alignas(16) float y[V];
-        if constexpr (V >= 4) {
-#pragma unroll
-          for (int j = 0; j < V / 4; ++j)
-            *reinterpret_cast<float4*>(y + 4 * j) = __ldcg(reinterpret_cast<const float4*>(a.part_o + part * D + j * 128) + lane);
-        } else {
-          *reinterpret_cast<float2*>(y) = __ldcg(reinterpret_cast<const float2*>(a.part_o + part * D) + lane);
-        }
-        const float mn = fmaxf(m, ml.x);
-        if (mn > -INFINITY) {
-          const float f = ex2(m - mn), w = ex2(ml.x - mn);
-          l = l * f + ml.y * w;
-#pragma unroll
-          for (int j = 0; j < V; ++j) o[j] = o[j] * f + y[j] * w;
-          m = mn;
-        }
-      }
-      __syncthreads();          // the previous item's sums are no longer read
-      if constexpr (V >= 4) {
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j)
-          *(reinterpret_cast<float4*>(&s_o[warp][j * 128]) + lane) = *reinterpret_cast<float4*>(o + 4 * j);
-      } else {
-        *(reinterpret_cast<float2*>(s_o[warp]) + lane) = *reinterpret_cast<float2*>(o);
-      }
-      if (lane == 0) s_ml[warp] = make_float2(m, l);
       __syncthreads();
-      for (int e = 2 * tid; e < dim; e += 2 * kJoinThreads) {
-        float M = -INFINITY;
+      if (warp == 0) {
+        float m = lane < W ? s_m[lane] : -INFINITY;
+        const float own = m;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
-        float L = 0.f, y0 = 0.f, y1 = 0.f;
-        if (M > -INFINITY) {
+        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (lane < W) s_f[lane] = own == -INFINITY ? 0.f : ex2(own - m);
+        __syncwarp();
+        float l = 0.f, y[V] = {};
+#pragma unroll 4
+        for (int k = 0; k < W; ++k) {
+          const float f = s_f[k];
+          if (f == 0.f) continue;
+          l += s_l[k] * f;
 #pragma unroll
-          for (int w = 0; w < kJoinWarps; ++w) {
-            const float f = ex2(s_ml[w].x - M);
-            L += s_ml[w].y * f;
-            y0 += s_o[w][e] * f;
-            y1 += s_o[w][e + 1] * f;
-          }
+          for (int j = 0; j < V; ++j) y[j] += s_o[k][j * 32 + lane] * f;
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        *reinterpret_cast<uint32_t*>(a.out + (int64_t)(q0 + row / group) * a.ldo +
-                                     (int64_t)(hk * group + row % group) * dim + e) = Elem<E>::from2(y0 * inv, y1 * inv);
+        store_row<E, V>(dst, lane, dim, y, l);
       }
+      __syncthreads();
     }
   }
 }
 
-template <class E, int D>
-cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, cudaStream_t st) {
-  const int grid = num_sms * (D <= 128 ? kDecCtas : 2);
-  if (a.softcap > 0.f) kv_decode_kernel<E, D, true><<<grid, kDecThreads, 0, st>>>(a);
-  else kv_decode_kernel<E, D, false><<<grid, kDecThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+// Rows are spread over gridDim.y blocks of every CTA's split segment.
+constexpr int kChunkJoinThreads = 256;
+template <class E>
+__global__ void __launch_bounds__(kChunkJoinThreads) kv_chunk_join_kernel(const __grid_constant__ KvAttendArgs a) {
+  const KvDev& d = a.kv;
+  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int first = blockIdx.x;
+  const int4 sg = __ldcg(a.tc_split + first);
+  if (sg.x < 0) return;
+  const int group = d.heads_q / d.heads_kv, dim = d.head_dim, rows_a = (sg.y >> 16) * group,
+            rows = rows_a + (sg.y & 0xffff) * group;
+  for (int row = blockIdx.y * (kChunkJoinThreads / 32) + (threadIdx.x >> 5); row < rows;
+       row += gridDim.y * (kChunkJoinThreads / 32)) {
+    const int x = row >= rows_a, rho = row - (x ? rows_a : 0), tok = rho / group;
+    JoinSum<4> s;
+    for (int g = first; g <= sg.w; g += 4) {
+      float2 ml[4];
+      float y[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (g + k <= sg.w) {
+          const int64_t part = (((int64_t)(g + k) * 2 + (g + k == first ? 1 : 0)) * 2 + x) * kKvTile + rho;
+          ml[k] = __ldcg(a.tc_part_ml + part);
+          load_row<4>(a.tc_part_o + part * kKvTile, lane, y[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s.add(ml[k], y[k]);
+    }
+    store_row<E, 4>(a.out + (int64_t)(sg.x + x * a.tpt + tok) * a.ldo + (int64_t)(sg.z * group + rho - tok * group) * dim,
+                    lane, dim, s.o, s.l);
+  }
+}
+
+// A launch that may begin before the one ahead of it in the stream has ended.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * num_sms);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<E, D>, a, (int64_t)grid * kDecWarps / a.hbw);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class E, int D>
+cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
+  const int grid = num_sms * (D <= 128 ? kDecCtas : 2);
+  auto kernel = a.softcap > 0.f ? kv_decode_kernel<E, D, true> : kv_decode_kernel<E, D, false>;
+  cudaError_t e;
+  if (after_chunks) {
+    e = launch_early(kernel, dim3(grid), kDecThreads, st, a);
+  } else {
+    kernel<<<grid, kDecThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  if (after_chunks) {
+    e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t groups = (int64_t)grid * kDecWarps / a.hbw, items = (int64_t)a.R * a.rows * a.kv.heads_kv;
+  // segments of 16 parts or more on average: a block each (a 131072-token
+  // context, 228 parts a row: 24 us with a warp each, 8 with a block)
+  const int64_t segments = (int64_t)a.R * ((a.rows + kKvRowTile - 1) / kKvRowTile) * (a.kv.heads_kv / a.hbw);
+  if (segments * 16 <= groups)
+    return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
+                        kJoinWideWarps * 32, st, a, groups);
+  const int64_t ctas = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, st,
+                      a, groups);
 }
 
 template <class E>
-cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st) {
-  if (a.kv.head_dim <= 64) return launch_decode<E, 64>(a, num_sms, st);
-  if (a.kv.head_dim <= 128) return launch_decode<E, 128>(a, num_sms, st);
-  return launch_decode<E, 256>(a, num_sms, st);
+cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
+  if (a.kv.head_dim <= 64) return launch_decode<E, 64>(a, num_sms, after_chunks, st);
+  if (a.kv.head_dim <= 128) return launch_decode<E, 128>(a, num_sms, after_chunks, st);
+  return launch_decode<E, 256>(a, num_sms, after_chunks, st);
 }
 
 }  // namespace
@@ -491,12 +546,33 @@ cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, cudaStream_t st)
 int64_t kv_attend_parts(int num_sms) { return (int64_t)num_sms * kDecCtas * kDecWarps * 2 * kKvRowTile; }
 int32_t kv_attend_cols(int32_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
-cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, cudaStream_t st) {
+template <class E, int D>
+cudaError_t prepare_decode() {
+  // all of the SM's memory as first-level cache, which holds the loads in flight
+  // (left to itself the kernel inherits the chunk kernel's split on its SMs)
+  for (auto k : {kv_decode_kernel<E, D, false>, kv_decode_kernel<E, D, true>})
+    if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1))
+      return e;
+  return cudaSuccess;
+}
+cudaError_t prepare_kv_decode_kernels() {
+  for (auto f : {prepare_decode<__half, 64>, prepare_decode<__half, 128>, prepare_decode<__half, 256>,
+                 prepare_decode<__nv_bfloat16, 64>, prepare_decode<__nv_bfloat16, 128>, prepare_decode<__nv_bfloat16, 256>})
+    if (cudaError_t e = f()) return e;
+  return cudaSuccess;
+}
+
+cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
   KvAttendArgs a = args;
-  // warps that work on neighbouring heads of the same tokens: the largest of
-  // 4, 2, 1 that divides the key heads
-  a.hbw = a.kv.heads_kv % 4 == 0 ? 4 : a.kv.heads_kv % 2 == 0 ? 2 : 1;
-  return dtype == 0 ? decode_dispatch<__half>(a, num_sms, st) : decode_dispatch<__nv_bfloat16>(a, num_sms, st);
+  // Warps that work side by side on neighbouring heads of the same tokens, so
+  // that what they read of a page at about the same time is long: the largest
+  // power of two up to 16 that divides the key heads (256 requests, 32 key
+  // heads of 128: 334 us with 1, 257 with 4, 247 with 8, 243 with 16, 247
+  // with 32; 8 key heads: 367, 352 and 350 us with 1, 4 and 8).
+  a.hbw = 1;
+  while (a.hbw < 16 && a.kv.heads_kv % (2 * a.hbw) == 0) a.hbw *= 2;
+  return dtype == 0 ? decode_dispatch<__half>(a, num_sms, after_chunks, st)
+                    : decode_dispatch<__nv_bfloat16>(a, num_sms, after_chunks, st);
 }
 
 }  // namespace slora

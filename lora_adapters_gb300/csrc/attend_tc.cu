@@ -189,8 +189,9 @@ struct alignas(16) Part {
   int end[2];              // one past the last key tile that tile A (B) of the pair needs, i0: none
   int tok, pos, tokens[2]; // the pair's first token and its position; tokens of tile A, of tile B
   int hk, row, len, whole; // key head; table row; tokens held; the segment lies in this part as a whole
+  int n, pad[3];           // key tiles of the segment
 };
-static_assert(sizeof(Part) == 48, "three 16-byte pieces");
+static_assert(sizeof(Part) == 64, "four 16-byte pieces");
 // Walks a CTA's run of units part by part.
 struct Walk {
   int left;                // units of the run not yet walked
@@ -217,7 +218,8 @@ __device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t u, int
   w.hk = (int)(in / per);
   w.i0 = (int)(in - (int64_t)w.hk * per);
   w.pr = 0;
-  const int fresh = __ldg(d.q_start + lo + 1) - __ldg(d.q_start + lo), ctx = __ldg(d.kv_len + lo) - fresh;
+  const int4 rq = __ldg(d.req + lo);
+  const int fresh = rq.y, ctx = rq.z - fresh;
   for (int n; w.i0 >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)) && n > 0; ++w.pr) w.i0 -= n;
   return w;
 }
@@ -225,10 +227,12 @@ __device__ __forceinline__ Part walk_next(const KvAttendArgs& a, Walk& w) {
   Part p{};
   if (w.left <= 0) return p;
   const KvDev& d = a.kv;
-  const int q0 = __ldg(d.q_start + w.r), fresh = __ldg(d.q_start + w.r + 1) - q0;
-  p.len = __ldg(d.kv_len + w.r);
-  p.row = __ldg(d.row + w.r);
+  const int4 rq = __ldg(d.req + w.r);
+  const int q0 = rq.x, fresh = rq.y;
+  p.len = rq.z;
+  p.row = rq.w;
   const int ctx = p.len - fresh, t0 = w.pr * 2 * a.tpt, n = pair_tiles(ctx, fresh, a.tpt, w.pr);
+  p.n = n;
   p.i0 = w.i0;
   p.i1 = min(n, p.i0 + w.left);
   p.tok = q0 + t0;
@@ -276,7 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
   const int64_t run = (total + gridDim.x - 1) / gridDim.x;
-  if ((int64_t)blockIdx.x * run >= total) return;
+  pdl_trigger();        // the decode kernel's CTAs take the SMs that become free
+  if ((int64_t)blockIdx.x * run >= total) {
+    if (threadIdx.x == 0) a.tc_split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
   if (warp == kWarpMma) tmem_alloc(&sm.tmem_slot, kTmemCols);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -408,15 +416,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       }
     } else if (warp == kWarpWalk) {  // ------------------------------------- the walk, by one thread
       if (elect_one()) {
-        Walk w = walk_start(a, (int64_t)blockIdx.x * run, min(total, (int64_t)(blockIdx.x + 1) * run));
+        const int64_t u0 = (int64_t)blockIdx.x * run;
+        Walk w = walk_start(a, u0, min(total, u0 + run));
+        const int units = w.left;
+        int4 split = make_int4(-1, 0, 0, 0);
         for (uint32_t k = 0;; ++k) {
+          const int64_t u = u0 + units - w.left;
           const Part q = walk_next(a, w);
+          if (q.i1 > 0 && q.i0 == 0 && !q.whole)      // a split segment begins here
+            split = make_int4(q.tok, q.tokens[0] << 16 | q.tokens[1], q.hk, (int)((u + q.n - 1) / run));
           ok = wait_bar(&sm.part_empty[k % kParts], ((k / kParts) & 1) ^ 1);
           if (!ok) break;
           sm.part[k % kParts] = q;
           mbar_arrive(&sm.part_full[k % kParts]);
           if (q.i1 == 0) break;
         }
+        a.tc_split[blockIdx.x] = split;
       }
     } else if (warp == kWarpMma && elect_one()) {  // ----------------------- MMAs, by one thread
       const uint32_t id_s = umma_idesc_f16(kKvTile, kKvTile, Elem<E>::kBf16, false);
@@ -699,58 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   }
 }
 
-// The parts of the split segments, joined in the order of the cache: one warp
-// per row of a segment.  Border b lies between runs b and b + 1; a segment
-// belongs to the first border inside it.
-constexpr int kJoinThreads = 256;
-
-template <class E>
-__global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ KvAttendArgs a,
-                                                                     const int grid) {
-  const KvDev& d = a.kv;
-  const int lane = threadIdx.x & 31;
-  const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
-  const int64_t run = max((int64_t)1, (total + grid - 1) / grid);
-  const int64_t u = (int64_t)(blockIdx.x + 1) * run;      // the border
-  Walk w{};
-  if (u < total) w = walk_start(a, u, total);
-  pdl_wait();
-  // w.i0: the segment's tiles before the border
-  if (u >= total || w.i0 == 0 || w.i0 > run) return;
-  const int group = d.heads_q / d.heads_kv, dim = d.head_dim;
-  const int q0 = __ldg(d.q_start + w.r), fresh = __ldg(d.q_start + w.r + 1) - q0, ctx = __ldg(d.kv_len + w.r) - fresh;
-  const int n = pair_tiles(ctx, fresh, a.tpt, w.pr);
-  const int first = blockIdx.x, last = (int)((u - w.i0 + n - 1) / run);
-  for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < 2 * kKvTile;
-       row += gridDim.y * (kJoinThreads / 32)) {
-    const int x = row / kKvTile, rho = row - x * kKvTile, tok = rho / group;
-    const int t = (w.pr * 2 + x) * a.tpt + tok;
-    if (tok >= a.tpt || t >= fresh) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int g = first; g <= last; ++g) {
-      const int64_t part = (((int64_t)g * 2 + (g == first ? 1 : 0)) * 2 + x) * kKvTile + rho;
-      const float2 ml = __ldcg(a.tc_part_ml + part);
-      if (ml.x == -INFINITY) continue;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.tc_part_o + part * kKvTile) + lane);
-      const float mn = fmaxf(m, ml.x), f = ex2(m - mn), e = ex2(ml.x - mn);
-      m = mn;
-      l = l * f + ml.y * e;
-      o.x = o.x * f + v.x * e;
-      o.y = o.y * f + v.y * e;
-      o.z = o.z * f + v.z * e;
-      o.w = o.w * f + v.w * e;
-    }
-    if (lane * 4 < dim) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      *reinterpret_cast<uint2*>(a.out + (int64_t)(q0 + t) * a.ldo + (int64_t)(w.hk * group + rho - tok * group) * dim +
-                                lane * 4) = make_uint2(Elem<E>::from2(o.x * inv, o.y * inv),
-                                                       Elem<E>::from2(o.z * inv, o.w * inv));
-    }
-  }
-}
-
 constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -762,24 +725,6 @@ void (*chunk_kernel(int head_dim))(const KvAttendArgs) {
 void (*chunk_kernel(int dtype, bool cap, int head_dim))(const KvAttendArgs) {
   if (dtype == 0) return cap ? chunk_kernel<__half, true>(head_dim) : chunk_kernel<__half, false>(head_dim);
   return cap ? chunk_kernel<__nv_bfloat16, true>(head_dim) : chunk_kernel<__nv_bfloat16, false>(head_dim);
-}
-
-template <class E>
-cudaError_t chunk_dispatch(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
-  chunk_kernel(dtype, a.softcap > 0.f, a.kv.head_dim)<<<num_sms, kThreads, kSmemBytes, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // one block row per border between runs, on the GPU before the runs are done
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms, 8);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_chunk_join_kernel<E>, a, num_sms);
 }
 
 }  // namespace
@@ -797,7 +742,8 @@ cudaError_t prepare_kv_chunk_kernels() {
 int64_t kv_chunk_part_rows(int num_sms) { return (int64_t)num_sms * 4 * kKvTile; }
 
 cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
-  return dtype == 0 ? chunk_dispatch<__half>(a, dtype, num_sms, st) : chunk_dispatch<__nv_bfloat16>(a, dtype, num_sms, st);
+  chunk_kernel(dtype, a.softcap > 0.f, a.kv.head_dim)<<<num_sms, kThreads, kSmemBytes, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace slora

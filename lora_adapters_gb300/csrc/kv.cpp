@@ -35,6 +35,7 @@ struct slora_kv {
   int32_t tpt = 0;                // tokens of a chunk tile, 0: the decode kernel takes everything
   float* d_tc_part_o = nullptr;
   float2* d_tc_part_ml = nullptr;
+  int4* d_tc_split = nullptr;
   uint64_t generation = 0;
   int32_t R = 0, T = 0, max_new = 0;   // of the planned batch
 };
@@ -68,6 +69,7 @@ void free_kv(slora_kv* kv) {
   cudaFree(kv->d_freq);
   cudaFree(kv->d_part_o);
   cudaFree(kv->d_part_ml);
+  cudaFree(kv->d_tc_split);
   cudaFree(kv->d_tc_part_o);
   cudaFree(kv->d_tc_part_ml);
 }
@@ -116,6 +118,7 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv,
 int64_t place_arrays(KvDev& d, int32_t* base) {
   int32_t* q = base;
   const int64_t T = d.max_tokens, R = d.max_rows;
+  d.req = reinterpret_cast<int4*>(q); q += 4 * R;      // first: 16-byte aligned
   d.slots = q; q += (int64_t)2 * d.layers * T;
   d.tok_req = q; q += T;
   d.tok_pos = q; q += T;
@@ -168,8 +171,8 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
   PoolView pv;
   KvDev d;
   if (int rc = check_config(pool, c, &pv, &d)) return rc;
-  if (!d_table || !d_arrays || (reinterpret_cast<uintptr_t>(d_table) | reinterpret_cast<uintptr_t>(d_arrays)) & 3)
-    return fail(SLORA_ERR_INVALID, "d_table and d_arrays must be device pointers to int32");
+  if (!d_table || !d_arrays || reinterpret_cast<uintptr_t>(d_table) & 3 || reinterpret_cast<uintptr_t>(d_arrays) & 15)
+    return fail(SLORA_ERR_INVALID, "d_table and d_arrays must be device pointers to int32, d_arrays 16-byte aligned");
 
   slora_kv* kv = new (std::nothrow) slora_kv();
   if (!kv) return fail(SLORA_ERR_OOM, "host allocation failed");
@@ -181,6 +184,7 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
   kv->per_page_div.set((uint32_t)d.per_page);
   auto setup = [&]() -> int {
     CUDA_TRY(prepare_kv_kernels());
+    CUDA_TRY(prepare_kv_decode_kernels());
     CUDA_TRY(cudaMalloc(&kv->d_freq, sizeof(uint64_t) * (size_t)(c->head_dim / 2)));
     const int64_t parts = kv_attend_parts(pv.num_sms);
     CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));
@@ -191,6 +195,7 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
       const int64_t rows = kv_chunk_part_rows(pv.num_sms);
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_o, sizeof(float) * (size_t)rows * kKvTile));
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_ml, sizeof(float2) * (size_t)rows));
+      CUDA_TRY(cudaMalloc(&kv->d_tc_split, sizeof(int4) * (size_t)pv.num_sms));
     }
     CUDA_TRY(cudaMemsetAsync(d_arrays, 0, sizeof(int32_t) * (size_t)ints, pv.compute));
     CUDA_TRY(cudaMemsetAsync(d_table, 0xff,
@@ -359,6 +364,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.softcap = softcap;
   a.part_o = kv->d_part_o;
   a.part_ml = kv->d_part_ml;
+  a.tc_split = kv->d_tc_split;
   a.per_page_div = kv->per_page_div;
   a.tpt = kv->tpt;
   a.tc_part_o = kv->d_tc_part_o;
@@ -366,6 +372,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   const int32_t group = kv->dev.heads_q / kv->dev.heads_kv;
   // chunks are possible where one request may bring more than kKvChunkRows rows
   const bool chunks = kv->tpt > 0 && (int64_t)std::min(kv->max_new, kv->T) * group > kKvChunkRows;
+  a.rows = chunks ? kKvChunkRows : (int32_t)((int64_t)std::min(kv->max_new, kv->T) * group);
   if (chunks) {
     const uint64_t dims[3] = {(uint64_t)kv->dev.head_dim, (uint64_t)kv->dev.heads_q, (uint64_t)kv->T};
     const uint64_t strides[2] = {2 * (uint64_t)kv->dev.head_dim, 2 * (uint64_t)ldq};
@@ -374,7 +381,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   }
   KvTimed tm(kv->pool, kKvTimerAttend);
   if (chunks) CUDA_TRY(launch_kv_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
-  CUDA_TRY(launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  CUDA_TRY(launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute));
   tm.done();
   return SLORA_OK;
 }

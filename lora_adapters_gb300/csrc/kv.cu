@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
       d.tc_off[r] = at[3];
       d.kv_len[r] = in ? q.ctx + q.fresh : 0;
       d.row[r] = in ? q.row : 0;
+      d.req[r] = in ? make_int4(at[0], q.fresh, q.ctx + q.fresh, q.row) : make_int4(at[0], 0, 0, 0);
       if (in && !idle) {
         int32_t dec, tc;
         plan_work(a, q.fresh, q.ctx, &dec, &tc);

@@ -63,6 +63,7 @@ struct KvDev {
   int32_t* row;                  // [R] table row
   int32_t* tok_req;              // [T] request of each token, -1: none
   int32_t* tok_pos;              // [T] position of each token in its request
+  int4* req;                     // [R] {first token, new tokens, tokens held, table row}, 16-byte aligned
   int32_t* dec_off;              // [R + 1] prefix sums of row tiles * units, the decode kernels' work
   int32_t* tc_off;               // [R + 1] prefix sums of 128-key tiles, the chunk kernel's work per key head
   int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
@@ -109,19 +110,25 @@ struct KvAttendArgs {
   float* part_o;                 // parts of split segments: [kv_attend_parts][kv_attend_cols]
   float2* part_ml;               // [kv_attend_parts] their maximum (in powers of two) and sum
   int32_t hbw;                   // neighbouring key heads worked on side by side
+  int32_t rows;                  // rows (token, head of the group) a request has at most in the decode kernel
   FastDiv per_page_div;
   // chunk kernel
   int32_t tpt;                   // kv_chunk_tokens
   float* tc_part_o;              // [kv_chunk_part_rows][kKvTile]
   float2* tc_part_ml;
+  int4* tc_split;                // per CTA: the split segment that begins in its run
+                                 // {first token (-1: none), tokens of tile A << 16 | of tile B, key head, last CTA}
   CUtensorMap q_map;             // q as [T][heads_q][head_dim], box {64, group, tpt}
 };
 int64_t kv_chunk_part_rows(int num_sms);
+cudaError_t prepare_kv_decode_kernels();
 cudaError_t prepare_kv_chunk_kernels();
 cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 int64_t kv_attend_parts(int num_sms);
 int32_t kv_attend_cols(int32_t head_dim);
-cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
+// The decode kernel (after_chunks: while the chunk kernel launched before it
+// still runs), and the joins of what either kernel split.
+cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).
 struct PoolView {
