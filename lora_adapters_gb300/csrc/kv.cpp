@@ -279,6 +279,7 @@ int slora_kv_plan(slora_kv* kv, int32_t R, const int32_t* d_row, const int32_t* 
   a.T = T;
   a.max_new = max_new;
   a.tpt = kv->tpt;
+  a.per_page_div = kv->per_page_div;
   a.row = d_row;
   a.ctx = d_ctx;
   a.fresh = d_new;

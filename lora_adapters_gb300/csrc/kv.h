@@ -74,6 +74,8 @@ struct KvPlanArgs {
   KvDev kv;
   int32_t R, T, max_new;
   int32_t tpt;                   // kv_chunk_tokens
+  int32_t tile;                  // tokens a CTA takes at a time (set by the launcher)
+  FastDiv per_page_div;
   const int32_t* row;            // NULL: request r has row r
   const int32_t* ctx;
   const int32_t* fresh;          // new tokens per request
@@ -96,6 +98,7 @@ struct KvAppendArgs {
   int32_t rot_dim;
   int32_t interleaved;
   float mscale;
+  int32_t parts;                 // warps per token (set by the launcher)
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, int num_sms, cudaStream_t st);
 

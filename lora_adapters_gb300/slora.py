@@ -521,17 +521,11 @@ class KVBatch:
     """A planned step: the arrays of slora_kv_batch as views of the cache's
     ``arrays`` tensor (the cache's next plan overwrites them)."""
 
-    def __init__(self, raw: slora_kv_batch, arrays, layers: int):
-        self.raw = raw
-        R, T, n = raw.R, raw.T, raw.slot_stride
-        base = arrays.data_ptr()
+    __slots__ = ("raw", "ref", "q_start", "kv_len", "tok_req", "tok_pos", "slots")
 
-        def view(ptr, length):
-            return arrays[(ptr - base) // 4:][:length]
-
-        self.q_start, self.kv_len = view(raw.q_start, R + 1), view(raw.kv_len, R)
-        self.tok_req, self.tok_pos = view(raw.tok_req, T), view(raw.tok_pos, T)
-        self.slots = view(raw.slots, 2 * layers * n).view(layers, 2, n)[:, :, :T]
+    def __init__(self, raw: slora_kv_batch, views):
+        self.raw, self.ref = raw, ctypes.byref(raw)
+        self.q_start, self.kv_len, self.tok_req, self.tok_pos, self.slots = views
 
 
 class KVCache:
@@ -558,6 +552,8 @@ class KVCache:
         self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
         self.arrays = torch.empty(n, **i32)
         self.handle = slora_kv_create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
+        self._lib, self._int32, self._views = lib(), torch.int32, {}
+        self._wq, self._wk = heads_q * head_dim, heads_kv * head_dim
 
     def close(self):
         if self.handle:
@@ -575,49 +571,76 @@ class KVCache:
     def set_rotary(self, rot_dim: int, inv_freq, interleaved: bool = False, mscale: float = 1.0) -> None:
         slora_kv_set_rotary(self.handle, rot_dim, ROTARY_INTERLEAVED if interleaved else ROTARY_HALF, inv_freq, mscale)
 
-    @staticmethod
-    def _i32(name, t):
-        import torch
-
+    def _i32(self, name, t):
         if t is None:
-            return 0
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            return None
+        if t.dtype is not self._int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
-        return t.data_ptr() if t.numel() else 0
+        return t.data_ptr() or None
 
     def _rows(self, name, t, T, cols):
-        if t.dtype != self.pool.tdtype or not t.is_cuda or t.dim() != 2 or t.shape[1] != cols or t.shape[0] < T or (
-                t.stride(1) != 1 and cols > 1):
+        """(address, row stride) of at least T rows of `cols` contiguous elements."""
+        shape, stride = t.shape, t.stride()
+        if t.dtype is not self.pool.tdtype or len(shape) != 2 or shape[1] != cols or shape[0] < T or stride[1] != 1 or (
+                not t.is_cuda):
             raise ValueError(f"{name} must be a CUDA {self.pool.dtype} tensor of {T} rows of {cols} contiguous elements")
-        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
+        return t.data_ptr(), stride[0] if shape[0] > 1 else max(cols, stride[0])
+
+    def _weight(self, name, t):
+        if t is None:
+            return None
+        if t.dtype is not self.pool.tdtype or t.numel() != self.head_dim or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous CUDA {self.pool.dtype} tensor of {self.head_dim}")
+        return t.data_ptr()
+
+    def _batch_views(self, raw):
+        layers, R, T, n = self.table.shape[0], raw.R, raw.T, raw.slot_stride
+        base = self.arrays.data_ptr()
+
+        def view(ptr, length):
+            at = (ptr - base) // 4
+            return self.arrays[at:at + length]
+
+        return (view(raw.q_start, R + 1), view(raw.kv_len, R), view(raw.tok_req, T), view(raw.tok_pos, T),
+                view(raw.slots, 2 * layers * n).view(layers, 2, n)[:, :, :T])
 
     def plan(self, ctx, new, pages, T: int, max_new: int, rows=None) -> KVBatch:
         """ctx, new, rows: int32 per request; pages: the opened blocks' pages in
         order (int32, [block][layer][K, V]); T: tokens the batch has room for."""
-        R = int(ctx.numel())
+        R = ctx.numel()
         if new.numel() != R or (rows is not None and rows.numel() != R):
             raise ValueError("ctx, new and rows must have one entry per request")
-        raw = slora_kv_plan(self.handle, R, self._i32("rows", rows), self._i32("ctx", ctx), self._i32("new", new),
-                            self._i32("pages", pages), int(pages.numel()) if pages is not None else 0, T, max_new)
-        return KVBatch(raw, self.arrays, self.table.shape[0])
+        raw = slora_kv_batch()
+        _check(self._lib.slora_kv_plan(self.handle, R, self._i32("rows", rows), self._i32("ctx", ctx),
+                                       self._i32("new", new), self._i32("pages", pages),
+                                       pages.numel() if pages is not None else 0, T, max_new, ctypes.byref(raw)),
+               "slora_kv_plan")
+        # the arrays stay where they are: the views of a batch of these sizes serve the next one too
+        views = self._views.get((R, T))
+        if views is None:
+            if len(self._views) >= 256:
+                self._views.clear()
+            views = self._views[(R, T)] = self._batch_views(raw)
+        return KVBatch(raw, views)
 
     def append(self, batch: KVBatch, layer: int, q, k, v, q_out=None, q_weight=None, k_weight=None,
                eps: float = 1e-6) -> None:
         """q [T, heads_q * head_dim] (rotated into q_out, or in place), k and v
         [T, heads_kv * head_dim] (stored); q_weight, k_weight [head_dim]."""
-        T, wq, wk = batch.raw.T, self.heads_q * self.head_dim, self.heads_kv * self.head_dim
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None and (w.dtype != self.pool.tdtype or w.numel() != self.head_dim or not w.is_contiguous()
-                                  or not w.is_cuda):
-                raise ValueError(f"{name} must be a contiguous CUDA {self.pool.dtype} tensor of {self.head_dim}")
-        slora_kv_append(self.handle, batch.raw, layer, *self._rows("q", q, T, wq), *self._rows("k", k, T, wk),
-                        *self._rows("v", v, T, wk), q_weight.data_ptr() if q_weight is not None else 0,
-                        k_weight.data_ptr() if k_weight is not None else 0, eps,
-                        *self._rows("q_out", q if q_out is None else q_out, T, wq))
+        T, wq, wk = batch.raw.T, self._wq, self._wk
+        pq, ldq = self._rows("q", q, T, wq)
+        pk, ldk = self._rows("k", k, T, wk)
+        pv, ldv = self._rows("v", v, T, wk)
+        po, ldo = (pq, ldq) if q_out is None else self._rows("q_out", q_out, T, wq)
+        _check(self._lib.slora_kv_append(self.handle, batch.ref, layer, pq, ldq, pk, ldk, pv, ldv,
+                                         self._weight("q_weight", q_weight), self._weight("k_weight", k_weight), eps,
+                                         po, ldo), "slora_kv_append")
 
     def attend(self, batch: KVBatch, layer: int, q, out, scale: Optional[float] = None, softcap: float = 0.0) -> None:
         """out[t] = attention of token t's heads over its request's stored tokens
         (scale: 1 / sqrt(head_dim) by default)."""
-        T, wq = batch.raw.T, self.heads_q * self.head_dim
-        slora_kv_attend(self.handle, batch.raw, layer, *self._rows("q", q, T, wq), *self._rows("out", out, T, wq),
-                        self.head_dim ** -0.5 if scale is None else scale, softcap)
+        T = batch.raw.T
+        pq, ldq = self._rows("q", q, T, self._wq)
+        po, ldo = self._rows("out", out, T, self._wq)
+        _check(self._lib.slora_kv_attend(self.handle, batch.ref, layer, pq, ldq, po, ldo,
+                                         self.head_dim ** -0.5 if scale is None else scale, softcap), "slora_kv_attend")
