@@ -28,6 +28,13 @@ through such a trace for a whole decoder of ``layers`` layers:
 * each step groups its tokens by adapter once and applies the LoRA delta of
   every layer's q, k, v, o (one multi-projection apply per layer, AUTO mode).
 
+With ``attention`` in the spec every step also does what stands between the
+projections (slora_kv_*): the step's block-table entries and slots are planned
+once, and in every layer the new tokens' queries and keys are rotated, keys and
+values stored in the request's KV pages, and the attention over everything the
+request holds becomes the input of the o projection.  Its time is reported
+apart from the LoRA path's.
+
 Every pool call is logged (``TraceResult.ops``) in the form the oracle's
 allocator replays, so a test can rebuild the pool state independently and
 check a step's outputs.  With ``device=None`` the trace runs on a planning
@@ -42,7 +49,10 @@ from typing import Dict, List, Optional, Tuple
 
 import numpy as np
 
-from . import slora, workloads
+from . import rotary, slora, workloads
+
+
+KV_KERNELS = ("kv_plan", "kv_append", "kv_attend")     # timer names of slora_timing_read
 
 
 @dataclasses.dataclass(frozen=True)
@@ -71,6 +81,8 @@ class TraceSpec:
     steps: int = 1000
     s: float = 0.01                          # y accumulates one delta per layer and step
     seed: int = 0
+    attention: bool = False                  # append and attend between q, k, v and o
+    head_dim: int = 128                      # with attention: H / head_dim query and key heads
 
     @property
     def pool_pages(self) -> int:
@@ -94,6 +106,7 @@ class Request:
     kv_handles: List[str] = dataclasses.field(default_factory=list)
     admitted_step: int = -1
     arrived_step: int = 0
+    row: int = -1                # with attention: its row of the block table
     missed: bool = False         # its adapter was not resident (or still loading) when it arrived
 
 
@@ -123,9 +136,12 @@ class TraceResult:
     ranks: np.ndarray
     wall_s: float
     layers: int = 1
+    attention_ms: Optional[Dict[str, float]] = None   # with attention: kernel time of plan, append, attend
 
     def summary(self) -> dict:
         d = {k: v for k, v in dataclasses.asdict(self).items() if k not in ("ops", "ranks")}
+        if d["attention_ms"] is None:
+            del d["attention_ms"]
         # every token passes through every layer: layer-token products per
         # second of the path's kernel time
         d["tokens_per_s_per_layer"] = (self.tokens * self.layers / (self.gpu_ms * 1e-3)
@@ -243,6 +259,24 @@ class Trace:
                 x.copy_(torch.from_numpy(bits.view(np.int16)).view(tdt))
             self.ta_dev = torch.empty(T, dtype=torch.int32, device=device)
             self.n = n
+        self.cache = None
+        self.free_rows = list(range(spec.max_running))[::-1]
+        if spec.attention:
+            if [p.name for p in spec.layer_projections] != ["q", "k", "v", "o"] or spec.H % spec.head_dim or any(
+                    p.h_in != spec.H or p.h_out != spec.H for p in spec.layer_projections):
+                raise ValueError("attention needs q, k, v, o projections of H x H and H a multiple of head_dim")
+            if spec.kv_pages_per_token != 2 * spec.layers:
+                raise ValueError("attention needs a K and a V page per token and layer")
+            if device is not None:
+                heads = spec.H // spec.head_dim
+                self.cache = slora.KVCache(self.pool, spec.layers, heads, heads, spec.head_dim, spec.max_running,
+                                           spec.prompt_len[1] + spec.output_len[1])
+                freq, mscale = rotary.inv_freq(spec.head_dim)
+                self.cache.set_rotary(spec.head_dim, freq, mscale=mscale)
+                i32 = dict(dtype=torch.int32, device=device)
+                self.plan_dev = torch.empty(3 * spec.max_running, **i32)       # ctx, new, row of each request
+                self.pages_dev = torch.empty(T * spec.kv_pages_per_token, **i32)
+                self.q_rot = torch.empty((T, spec.H), dtype=tdt, device=device)
 
     # ------------------------------------------------------------------ pool calls
     def _kv_alloc(self, n: int) -> Optional[str]:
@@ -305,6 +339,7 @@ class Trace:
         running_sum = 0
         peak_kv = 0
         gpu_ms = step_ms = load_ms = stall_ms = copy_ms = 0.0
+        attention_ms = None
         events = []
         copy_pairs = []      # copy-stream events around each step's loads
         if self.device is not None:
@@ -343,6 +378,8 @@ class Trace:
                             self.resident.move_to_end(rq.adapter)
                             rq.kv_handles.append(h)
                             rq.admitted_step = step
+                            if sp.attention:
+                                rq.row = self.free_rows.pop()
                             self.running.append(rq)
                             (waits_miss if rq.missed else waits_hit).append(step - rq.arrived_step)
                             continue
@@ -385,6 +422,7 @@ class Trace:
                     seg = slora.slora_build_segments_for(self.pool.handle, self.ta_dev.data_ptr(), T,
                                                          np.asarray(ids, dtype=np.int32))
                     npl = self.n
+                    batch = self._plan_step(plan, T) if sp.attention else None
                     for layer in range(sp.layers):
                         if probe and layer == self.probe_layer:
                             rng = np.random.default_rng(np.random.SeedSequence(sp.seed, spawn_key=(24, step)))
@@ -394,9 +432,15 @@ class Trace:
                                   for p in sp.layer_projections]
                             for d_, h_ in zip(self.xs + self.ys, xb + yb):
                                 d_[:T].copy_(torch.from_numpy(h_.view(np.int16)).view(self.pool.tdtype))
-                        self.pool.apply_multi(seg, list(range(layer * npl, (layer + 1) * npl)),
-                                              [x[:T] for x in self.xs], [y[:T] for y in self.ys], sp.s,
-                                              slora.MODE_AUTO)
+                        n_first = npl - 1 if sp.attention else npl       # with attention o comes after it
+                        self.pool.apply_multi(seg, list(range(layer * npl, layer * npl + n_first)),
+                                              [x[:T] for x in self.xs[:n_first]], [y[:T] for y in self.ys[:n_first]],
+                                              sp.s, slora.MODE_AUTO)
+                        if sp.attention:
+                            q, k, v, o = (y[:T] for y in self.ys)
+                            self.cache.append(batch, layer, q, k, v, q_out=self.q_rot[:T])
+                            self.cache.attend(batch, layer, self.q_rot[:T], self.xs[3][:T])
+                            self.pool.apply(seg, layer * npl + 3, self.xs[3][:T], o, sp.s, slora.MODE_AUTO)
                         if probe and layer == self.probe_layer:
                             torch.cuda.synchronize()
                             self.probe = {"step": step, "layer": layer, "ids": np.asarray(ids, dtype=np.int32),
@@ -404,6 +448,11 @@ class Trace:
                                           "y": [y[:T].cpu().view(torch.int16).numpy().view(np.uint16).copy()
                                                 for y in self.ys],
                                           "ops": len(self.ops), "evictions_before": self.evictions}
+                            if sp.attention:
+                                self.probe.update(
+                                    x_o=self.xs[3][:T].cpu(), q_rot=self.q_rot[:T].cpu(), step_plan=[
+                                        (rq.row, rq.prefilled + rq.generated, n) for rq, n, _ in plan],
+                                    table=self.cache.table[layer].cpu().numpy(), pages=self.pool.buffer.cpu())
                     e1.record(st)
                     events.append((e0, e1))
             # loads for the adapters of the first waiting requests that miss
@@ -440,6 +489,8 @@ class Trace:
                 for h in rq.kv_handles:
                     self._kv_free(h)
                 self.refs[rq.adapter] -= 1
+                if sp.attention:
+                    self.free_rows.append(rq.row)
                 finished += 1
             self.running = [rq for rq in self.running if rq.generated < rq.output]
             running_sum += len(self.running)
@@ -451,7 +502,9 @@ class Trace:
             copy_ms = sum(a.elapsed_time(b) for a, b in copy_pairs)
             tm = slora.slora_timing_read(self.pool.handle)
             slora.slora_timing_enable(self.pool.handle, False)
-            gpu_ms = sum(ms for k, (ms, _) in tm.items() if k not in ("scatter", "load_wait"))
+            gpu_ms = sum(ms for k, (ms, _) in tm.items() if k not in ("scatter", "load_wait", *KV_KERNELS))
+            if sp.attention:
+                attention_ms = {k: tm[k][0] for k in KV_KERNELS}
             load_ms = tm.get("scatter", (0.0, 0))[0]
             stall_ms = tm.get("load_wait", (0.0, 0))[0]   # the compute stream's waits for copies
             st = self.pool.status()
@@ -463,9 +516,27 @@ class Trace:
                            float(np.mean(waits_hit)) if waits_hit else 0.0,
                            float(np.mean(waits_miss)) if waits_miss else 0.0,
                            finished, running_sum / max(1, steps), peak_kv,
-                           list(self.ops), self.ranks.copy(), time.perf_counter() - t0, sp.layers)
+                           list(self.ops), self.ranks.copy(), time.perf_counter() - t0, sp.layers, attention_ms)
+
+    def _plan_step(self, plan, T: int):
+        """The step's block-table entries and slots: its requests' lengths and
+        rows, and the pages of the tokens it adds (each request's own list,
+        taken at admission, in order)."""
+        import torch
+
+        R, per = len(plan), self.spec.kv_pages_per_token
+        ctx = np.array([rq.prefilled + rq.generated for rq, _, _ in plan], dtype=np.int32)
+        new = np.array([n for _, n, _ in plan], dtype=np.int32)
+        rows = np.array([rq.row for rq, _, _ in plan], dtype=np.int32)
+        pages = np.concatenate([self.kv[rq.kv_handles[0]][c * per:(c + n) * per] for (rq, n, _), c in zip(plan, ctx)])
+        self.plan_dev[:3 * R].copy_(torch.from_numpy(np.concatenate([ctx, new, rows])), non_blocking=True)
+        self.pages_dev[:pages.shape[0]].copy_(torch.from_numpy(pages), non_blocking=True)
+        return self.cache.plan(self.plan_dev[:R], self.plan_dev[R:2 * R], self.pages_dev[:pages.shape[0]], T,
+                               int(new.max()), rows=self.plan_dev[2 * R:3 * R])
 
     def close(self):
+        if self.cache is not None:
+            self.cache.close()
         self.pool.close()
 
 
@@ -481,12 +552,14 @@ def main():
     ap.add_argument("--layers", type=int, default=32)
     ap.add_argument("--arrivals", type=float, default=4.0)
     ap.add_argument("--pool-gb", type=float, default=80.0)
+    ap.add_argument("--attention", action="store_true",
+                    help="rotate, store and attend between the q, k, v and o projections of every layer")
     args = ap.parse_args()
     from . import build
 
     build.build()
     spec = dataclasses.replace(TraceSpec(), steps=args.steps, layers=args.layers, arrivals_per_step=args.arrivals,
-                               pool_bytes=int(args.pool_gb * 1e9), kv_pages_per_token=2 * args.layers)
+                               pool_bytes=int(args.pool_gb * 1e9), kv_pages_per_token=2 * args.layers, attention=args.attention)
     tr = Trace(spec, device=torch.device("cuda", 0))
     res = tr.run()
     s = res.summary()
@@ -497,7 +570,8 @@ def main():
                        "adapters": spec.num_adapters, "ranks": list(spec.rank_set),
                        "popularity": f"zipf(alpha={spec.zipf_alpha:g})", "pool_gb": spec.pool_bytes / 1e9,
                        "kv_pages_per_token": spec.kv_pages_per_token, "token_budget": spec.token_budget,
-                       "arrivals_per_step": spec.arrivals_per_step, "mode": "auto"},
+                       "arrivals_per_step": spec.arrivals_per_step, "mode": "auto",
+                       **({"attention": True, "head_dim": spec.head_dim} if spec.attention else {})},
             "trace": s}
     print(json.dumps(line))
     tr.close()

@@ -69,3 +69,23 @@ def test_oracle_attention_invariants():
     same = okv.attend(q, np.ones_like(k), v, 6, 0.25, 0.0)
     assert np.allclose(same[1, 0], v[:8, 0].mean(0))
     assert np.allclose(okv.attend(q, k, v, 6, 0.25, 1e6), out, atol=1e-6)
+
+
+def test_rotary_frequencies_of_each_scaling():
+    from lora_adapters_gb300 import rotary
+
+    plain, m = rotary.inv_freq(64)
+    assert m == 1.0 and np.allclose(plain, 10000.0 ** (-np.arange(0, 64, 2) / 64))
+    assert np.allclose(rotary.inv_freq(64, scaling="linear", factor=4.0)[0], np.array(plain) / 4)
+    f, m = rotary.inv_freq(64, scaling="base", factor=8.0)
+    assert m == 1.0 and np.isclose(f[0], 1.0) and np.isclose(f[-1], plain[-1] / 8)
+    f, m = rotary.inv_freq(64, scaling="parts", factor=8.0, trained_len=4096)
+    r = np.array(f) / np.array(plain)
+    assert np.isclose(m, 0.1 * np.log(8.0) + 1) and np.isclose(r[0], 1) and np.isclose(r[-1], 1 / 8)
+    assert (np.diff(r) <= 1e-12).all()
+    turns = 4096 * np.array(plain) / (2 * np.pi)
+    assert np.allclose(r[turns > 33], 1) and np.allclose(r[turns < 0.8], 1 / 8)
+    for bad in (dict(rot_dim=3), dict(rot_dim=64, factor=0.5), dict(rot_dim=64, scaling="parts"),
+                dict(rot_dim=64, scaling="other"), dict(rot_dim=64, base=1.0), dict(rot_dim=2, scaling="base")):
+        with pytest.raises(ValueError):
+            rotary.inv_freq(**bad)
