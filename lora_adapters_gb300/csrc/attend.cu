@@ -131,23 +131,105 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
   const float sc = CAP ? 2.f * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
   const float cap2 = a.softcap * kLog2e;
-  int r = u < u1 ? find_request(d.dec_off, a.R, u, blocks) : 0;
+  if (u >= u1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  int left = (int)min(u1 - u, (int64_t)0x7fffffff);     // units to do (a run of more than 2^31 units has no cache to be in)
 
-  while (u < u1) {
-    int off = __ldg(d.dec_off + r), off_next = __ldg(d.dec_off + r + 1);
-    int4 rq = __ldg(d.req + r);
-    while ((int64_t)off_next * blocks <= u) {           // requests without units are passed over
-      ++r;
-      off = off_next;
-      off_next = __ldg(d.dec_off + r + 1);
-      rq = __ldg(d.req + r);
+  // The units to do are fetched two ahead of the one that is multiplied, from
+  // one segment into the next: `f` is where that is.
+  struct {
+    int left, r, hb, rt, c;        // units left; request, head block, row tile, unit of the segment
+    int n, tiles, len;             // units of a segment, row tiles, tokens of the request
+    int at;                        // byte of a pool row at which the head block's head of this warp starts
+    const int32_t* tab;            // lanes 0-15 the request's K pages, 16-31 its V pages
+  } f;
+  auto f_open = [&](const int4& rq) {
+    f.len = rq.z;
+    f.n = (rq.z + kKvUnit - 1) / kKvUnit;
+    f.tiles = (rq.y * group + kKvRowTile - 1) / kKvRowTile;
+    f.tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)rq.w * d.max_blocks;
+  };
+  // requests without units here: no new tokens, or a chunk
+  auto no_units = [&](const int4& rq) {
+    return rq.y == 0 || (a.tpt > 0 && (int64_t)rq.y * group > kKvChunkRows);
+  };
+  {
+    f.left = left;
+    f.r = find_request(d.dec_off, a.R, u, blocks);
+    const int4 rq = __ldg(d.req + f.r);
+    f_open(rq);
+    const int64_t in_req = u - (int64_t)__ldg(d.dec_off + f.r) * blocks;
+    const int seg = (int)(in_req / f.n);
+    f.c = (int)(in_req - (int64_t)seg * f.n);
+    f.hb = seg / f.tiles;
+    f.rt = seg - f.hb * f.tiles;
+    f.at = (f.hb * hbw + hsub) * dim * 2;
+  }
+  int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
+  // The next unit's pool rows, one a lane, and where its head starts in them.
+  auto fetch = [&](int& at) -> int {
+    if (f.left == 0) return -1;
+    --f.left;
+    if (f.c == f.n) {
+      f.c = 0;
+      if (++f.rt == f.tiles) {
+        f.rt = 0;
+        if (++f.hb == blocks) {
+          f.hb = 0;
+          int4 rq;
+          do rq = __ldg(d.req + ++f.r);
+          while (no_units(rq));
+          f_open(rq);
+        }
+        f.at = (f.hb * hbw + hsub) * dim * 2;
+      }
     }
+    at = f.at;
+    const int j = f.c++ * kKvUnit + (lane & 15);
+    if (j >= f.len) return -1;
+    const int b = (int)a.per_page_div.div((uint32_t)j);
+    const int page = __ldg(f.tab + b);
+    return (uint32_t)page < (uint32_t)d.num_pages ? page * P + (j - b * P) : -1;
+  };
+  uint4 kf[NC][2], vf[NB][4];
+  auto load_k = [&](int slot, int at) {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (at + kk * 16);
+    const int s0 = __shfl_sync(0xffffffffu, slot, nn), s1 = __shfl_sync(0xffffffffu, slot, nn + 8);
+    const uint8_t* p0 = base + s0 * row_bytes;
+    const uint8_t* p1 = base + s1 * row_bytes;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const bool in = D == dim || (i * 4 + kk) * 8 < dim;
+      kf[i][0] = in && s0 >= 0 ? load_stream(p0 + i * 64) : make_uint4(0, 0, 0, 0);
+      kf[i][1] = in && s1 >= 0 ? load_stream(p1 + i * 64) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load_v = [&](int slot, int at) {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (at + nn * 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int s = __shfl_sync(0xffffffffu, slot, 16 + 2 * kk + (x & 1) + (x & 2) * 4);
+      const uint8_t* p = base + s * row_bytes;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const bool in = D == dim || b * 64 + nn * 8 < dim;
+        vf[b][x] = in && s >= 0 ? load_stream(p + b * 128) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  int at = 0, at_next = 0;
+  int slot = fetch(at), slot_next = fetch(at_next);
+  load_k(slot, at);
+  load_v(slot, at);
+
+  while (left > 0) {
+    int4 rq = __ldg(d.req + r);
+    while (no_units(rq)) rq = __ldg(d.req + ++r);
     const int len = rq.z, q0 = rq.x, rows = rq.y * group;
-    const int nchunk = (len + 15) >> 4, tiles = (rows + kKvRowTile - 1) / kKvRowTile;
-    const int64_t in_req = u - (int64_t)off * blocks;
-    const int seg = (int)(in_req / nchunk), c0 = (int)(in_req - (int64_t)seg * nchunk);
-    const int hb = seg / tiles, rt = seg - hb * tiles;
-    const int c1 = (int)min((int64_t)nchunk, c0 + (u1 - u));
+    const int nchunk = (len + kKvUnit - 1) / kKvUnit, tiles = (rows + kKvRowTile - 1) / kKvRowTile;
+    const int c1 = min(nchunk, c0 + left);
     const int hk = hb * hbw + hsub;
     const int ctx = len - rq.y;
     // ---- this tile's queries: row n of the tile is (token, head of the group)
@@ -177,44 +259,6 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    // lanes 0-15 look up the K rows of a unit's tokens, lanes 16-31 the V rows
-    const int32_t* tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)rq.w * d.max_blocks;
-    auto lookup = [&](int c) -> int {
-      const int j = c * 16 + (lane & 15);
-      if (c >= c1 || j >= len) return -1;
-      const int b = (int)a.per_page_div.div((uint32_t)j);
-      const int page = __ldg(tab + b);
-      return (uint32_t)page < (uint32_t)d.num_pages ? page * P + (j - b * P) : -1;
-    };
-    const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)hk * dim * 2;
-    uint4 kf[NC][2], vf[NB][4];
-    auto load_k = [&](int slot) {
-      const int s0 = __shfl_sync(0xffffffffu, slot, nn), s1 = __shfl_sync(0xffffffffu, slot, nn + 8);
-      const uint8_t* p0 = base + s0 * row_bytes + kk * 16;
-      const uint8_t* p1 = base + s1 * row_bytes + kk * 16;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const bool in = D == dim || (i * 4 + kk) * 8 < dim;
-        kf[i][0] = in && s0 >= 0 ? load_stream(p0 + i * 64) : make_uint4(0, 0, 0, 0);
-        kf[i][1] = in && s1 >= 0 ? load_stream(p1 + i * 64) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto load_v = [&](int slot) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int s = __shfl_sync(0xffffffffu, slot, 16 + 2 * kk + (x & 1) + (x & 2) * 4);
-        const uint8_t* p = base + s * row_bytes + nn * 16;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const bool in = D == dim || b * 64 + nn * 8 < dim;
-          vf[b][x] = in && s >= 0 ? load_stream(p + b * 128) : make_uint4(0, 0, 0, 0);
-        }
-      }
-    };
-
-    int slot = lookup(c0), slot_next = lookup(c0 + 1);
-    load_k(slot);
-    load_v(slot);
     for (int c = c0; c < c1; ++c) {
       // S^T: tokens nn and nn + 8, rows 2 kk and 2 kk + 1
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -225,8 +269,9 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
       const int held = slot;
       slot = slot_next;
-      slot_next = lookup(c + 2);
-      load_k(slot);
+      at = at_next;
+      slot_next = fetch(at_next);
+      load_k(slot, at);
       const bool v0 = __shfl_sync(0xffffffffu, held, nn) >= 0, v1 = __shfl_sync(0xffffffffu, held, nn + 8) >= 0;
       const int j0 = c * 16 + nn, j1 = j0 + 8;
 #pragma unroll
@@ -280,7 +325,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           mma16816<E>(o[b * 4 + j], a0, a1, a2, a3, e0, e1);
         }
       }
-      load_v(slot);
+      load_v(slot, at);
     }
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
@@ -321,7 +366,15 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         if (nn == 0) a.part_ml[part] = make_float2(x ? m1 : m0, l);
       }
     }
-    u += c1 - c0;
+    left -= c1 - c0;
+    c0 = 0;                        // the next segment, if any is left
+    if (++rt == tiles) {
+      rt = 0;
+      if (++hb == blocks) {
+        hb = 0;
+        ++r;
+      }
+    }
   }
   // after chunks: their kernel may still run, and this grid ends after it
   asm volatile("griddepcontrol.wait;" ::: "memory");
