@@ -189,13 +189,16 @@ struct alignas(16) Part {
   int end[2];              // one past the last key tile that tile A (B) of the pair needs, i0: none
   int tok, pos, tokens[2]; // the pair's first token and its position; tokens of tile A, of tile B
   int hk, row, len, whole; // key head; table row; tokens held; the segment lies in this part as a whole
-  int n, pad[3];           // key tiles of the segment
+  int last, pad[3];        // the CTA whose run ends the segment
 };
 static_assert(sizeof(Part) == 64, "four 16-byte pieces");
 // Walks a CTA's run of units part by part.
+// A pair of tiles with n key tiles is kKvPairUnits + n units, the first ones its
+// own cost; a run that ends within those leaves the pair to the next CTA.
 struct Walk {
+  int64_t u;               // the next part's first unit
   int left;                // units of the run not yet walked
-  int r, hk, pr, i0;       // where the next part starts
+  int r, hk, pr, v0;       // where the next part starts: request, key head, pair, unit of the pair
 };
 // Key tiles of pair pr: up to the position of its last token.
 __device__ __forceinline__ int pair_tiles(int ctx, int fresh, int tpt, int pr) {
@@ -213,47 +216,51 @@ __device__ __forceinline__ Walk walk_start(const KvAttendArgs& a, int64_t u, int
   const int off = __ldg(d.tc_off + lo), per = max(1, __ldg(d.tc_off + lo + 1) - off);
   const int64_t in = u - (int64_t)off * d.heads_kv;
   Walk w;
+  w.u = u;
   w.left = (int)(end - u);
   w.r = lo;
   w.hk = (int)(in / per);
-  w.i0 = (int)(in - (int64_t)w.hk * per);
+  w.v0 = (int)(in - (int64_t)w.hk * per);
   w.pr = 0;
   const int4 rq = __ldg(d.req + lo);
   const int fresh = rq.y, ctx = rq.z - fresh;
-  for (int n; w.i0 >= (n = pair_tiles(ctx, fresh, a.tpt, w.pr)) && n > 0; ++w.pr) w.i0 -= n;
+  for (int n; w.v0 >= (n = kKvPairUnits + pair_tiles(ctx, fresh, a.tpt, w.pr)); ++w.pr) w.v0 -= n;
   return w;
 }
-__device__ __forceinline__ Part walk_next(const KvAttendArgs& a, Walk& w) {
+__device__ __forceinline__ Part walk_next(const KvAttendArgs& a, Walk& w, int64_t run) {
   Part p{};
-  if (w.left <= 0) return p;
   const KvDev& d = a.kv;
-  const int4 rq = __ldg(d.req + w.r);
-  const int q0 = rq.x, fresh = rq.y;
-  p.len = rq.z;
-  p.row = rq.w;
-  const int ctx = p.len - fresh, t0 = w.pr * 2 * a.tpt, n = pair_tiles(ctx, fresh, a.tpt, w.pr);
-  p.n = n;
-  p.i0 = w.i0;
-  p.i1 = min(n, p.i0 + w.left);
-  p.tok = q0 + t0;
-  p.pos = ctx + t0;
-  p.hk = w.hk;
-  p.whole = p.i0 == 0 && p.i1 == n;
+  while (w.left > 0 && p.i1 == 0) {
+    const int4 rq = __ldg(d.req + w.r);
+    const int q0 = rq.x, fresh = rq.y;
+    p.len = rq.z;
+    p.row = rq.w;
+    const int ctx = p.len - fresh, t0 = w.pr * 2 * a.tpt, n = pair_tiles(ctx, fresh, a.tpt, w.pr);
+    const int v1 = min(kKvPairUnits + n, w.v0 + w.left);
+    p.i0 = max(0, w.v0 - kKvPairUnits);
+    p.i1 = max(0, v1 - kKvPairUnits);
+    p.tok = q0 + t0;
+    p.pos = ctx + t0;
+    p.hk = w.hk;
+    p.whole = p.i0 == 0 && p.i1 == n;
+    p.last = (int)((w.u - w.v0 + kKvPairUnits + n - 1) / run);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    p.tokens[x] = max(0, min(a.tpt, fresh - t0 - x * a.tpt));
-    p.end[x] = p.tokens[x] == 0 ? p.i0
-                                : max(p.i0, min(p.i1, (p.pos + x * a.tpt + p.tokens[x] + kKvTile - 1) / kKvTile));
-  }
-  w.left -= p.i1 - p.i0;
-  w.i0 = 0;
-  if (w.left > 0) {                 // the next pair, key head or request with tiles
-    if (++w.pr * 2 * a.tpt >= fresh) {
-      w.pr = 0;
-      if (++w.hk == d.heads_kv) {
-        w.hk = 0;
-        do ++w.r;
-        while (__ldg(d.tc_off + w.r + 1) == __ldg(d.tc_off + w.r));
+    for (int x = 0; x < 2; ++x) {
+      p.tokens[x] = max(0, min(a.tpt, fresh - t0 - x * a.tpt));
+      p.end[x] = p.tokens[x] == 0 ? p.i0
+                                  : max(p.i0, min(p.i1, (p.pos + x * a.tpt + p.tokens[x] + kKvTile - 1) / kKvTile));
+    }
+    w.left -= v1 - w.v0;
+    w.u += v1 - w.v0;
+    w.v0 = 0;
+    if (w.left > 0) {                 // the next pair, key head or request with tiles
+      if (++w.pr * 2 * a.tpt >= fresh) {
+        w.pr = 0;
+        if (++w.hk == d.heads_kv) {
+          w.hk = 0;
+          do ++w.r;
+          while (__ldg(d.tc_off + w.r + 1) == __ldg(d.tc_off + w.r));
+        }
       }
     }
   }
@@ -418,13 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       if (elect_one()) {
         const int64_t u0 = (int64_t)blockIdx.x * run;
         Walk w = walk_start(a, u0, min(total, u0 + run));
-        const int units = w.left;
         int4 split = make_int4(-1, 0, 0, 0);
         for (uint32_t k = 0;; ++k) {
-          const int64_t u = u0 + units - w.left;
-          const Part q = walk_next(a, w);
+          const Part q = walk_next(a, w, run);
           if (q.i1 > 0 && q.i0 == 0 && !q.whole)      // a split segment begins here
-            split = make_int4(q.tok, q.tokens[0] << 16 | q.tokens[1], q.hk, (int)((u + q.n - 1) / run));
+            split = make_int4(q.tok, q.tokens[0] << 16 | q.tokens[1], q.hk, q.last);
           ok = wait_bar(&sm.part_empty[k % kParts], ((k / kParts) & 1) ^ 1);
           if (!ok) break;
           sm.part[k % kParts] = q;

@@ -54,14 +54,15 @@ __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) {
 
 // The attention's work for one request: decode units (row tiles of its (token,
 // head of the group) rows times 16-token units of its length) or, for a chunk,
-// 128-key tiles of every pair of row tiles, up to the pair's last position.
+// 128-key tiles of every pair of row tiles, up to the pair's last position, and
+// the pair's own cost.
 __device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ctx, int32_t* dec, int32_t* tc) {
   const int64_t rows = (int64_t)fresh * (a.kv.heads_q / a.kv.heads_kv);
   const int len = ctx + fresh;
   *dec = *tc = 0;
   if (a.tpt > 0 && rows > kKvChunkRows) {
     int32_t n = 0;
-    for (int t = 0; t < fresh; t += 2 * a.tpt) n = sat_add(n, (ctx + min(fresh, t + 2 * a.tpt) + kKvTile - 1) / kKvTile);
+    for (int t = 0; t < fresh; t += 2 * a.tpt) n = sat_add(n, kKvPairUnits + (ctx + min(fresh, t + 2 * a.tpt) + kKvTile - 1) / kKvTile);
     *tc = n;
   } else {
     *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + kKvUnit - 1) / kKvUnit), (int64_t)0x7fffffff);

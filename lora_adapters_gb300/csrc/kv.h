@@ -19,6 +19,12 @@ constexpr int kKvTile = 128;           // rows and keys of one chunk tile
 // A request whose new tokens make more rows than this (per key head) is a
 // chunk: two row tiles at most read the cache in the decode kernel.
 constexpr int kKvChunkRows = 16;
+// What a pair of chunk tiles costs besides its key tiles (queries in, results
+// out, the first scores waited for), in key tiles' time: about 6,000 cycles
+// against 3,000.  Counted with them, the runs of CTAs with many short prompts
+// end when the others' do (32 prompts of 8 to 512 tokens: 95 us with 0, 85 with 1, 86 with
+// 2 and 3; a 1024-token chunk 261, 259, 259 and 261).
+constexpr int kKvPairUnits = 2;
 // Query heads per key head the chunk kernel takes: a 128-row tile then holds
 // four tokens at least, and a request's tiles stay few enough to be counted
 // one by one.
