@@ -16,9 +16,12 @@ constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
 constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
 constexpr int kKvUnit = 16;            // tokens of one decode unit
 constexpr int kKvTile = 128;           // rows and keys of one chunk tile
-// A request whose new tokens make more rows than this (per key head) is a
-// chunk: two row tiles at most read the cache in the decode kernel.
-constexpr int kKvChunkRows = 16;
+// A request whose new tokens make more rows than this (per key head) goes to the
+// chunk kernel, which reads the cache once for 256 of them; the decode kernel
+// reads it again for every row tile.  16 rows: 128 requests of 17 to 8192
+// tokens 368 us against 693, one of 131072 154 against 194, one of 640 14.7
+// against 12.3.
+constexpr int kKvChunkRows = kKvRowTile;
 // What a pair of chunk tiles costs besides its key tiles (queries in, results
 // out, the first scores waited for), in key tiles' time: about 6,000 cycles
 // against 3,000.  Counted with them, the runs of CTAs with many short prompts

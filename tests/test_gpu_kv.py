@@ -7,9 +7,10 @@ type (fp16 2^-11, bf16 2^-8).
    two products of normed values (|x| below about 6 times its weight), cosine
    and sine good to 2^-22 of a unit: |err| <= u |y| + 2^-18 max|pair|.
  - attend: one rounding of the result, u |o|; scores of at most 256 fp32
-   products leave a relative error below 2^-12 in a weight; and a chunk's
-   weights may themselves be rounded to the storage type, where they add at
-   most u times the largest |v| of the request's head (decode keeps them to
+   products leave a relative error below 2^-12 in a weight; and the weights of
+   requests with more than 8 rows (new tokens times query heads a key head)
+   may themselves be rounded to the storage type, where they add at most u
+   times the largest |v| of the request's head (with up to 8 rows they keep
    twice the 16 bits).
 """
 import numpy as np
@@ -273,7 +274,7 @@ def _check_attend(s, q, out, softcap=0.0, scale=None, layer=0, requests=None):
     hq, hkv, d = s.hq, s.hkv, s.d
     scale = d ** -0.5 if scale is None else scale
     cache = s.cache_rows()
-    decode = max(s.new + [0]) <= 1
+    decode = max(s.new + [0]) * (s.hq // s.hkv) <= 8
     t0 = 0
     for r, (c, n) in enumerate(zip(s.ctx, s.new)):
         if n and (requests is None or r in requests):
