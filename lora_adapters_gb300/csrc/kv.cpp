@@ -100,7 +100,6 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv,
   KvDev& d = *dev;
   d = KvDev{};
   d.pool = pv->d_pool;
-  d.num_rows = pv->num_pages * P;
   d.num_pages = (int32_t)pv->num_pages;
   d.per_page = (int32_t)P;
   d.layers = c->layers;
@@ -126,7 +125,6 @@ int64_t place_arrays(KvDev& d, int32_t* base) {
   d.kv_len = q; q += R;
   d.dec_off = q; q += R + 1;
   d.tc_off = q; q += R + 1;
-  d.row = q; q += R;
   return q - base;
 }
 

@@ -29,8 +29,8 @@ __device__ __forceinline__ void report_err(int32_t* err, int code) {
 //
 // One launch.  Every CTA computes the two prefix sums over all requests for
 // itself (R <= 4096: a few loads and one block scan, cheaper than a second
-// launch or a grid-wide wait), then takes tiles of kPlanTokens tokens.  A
-// tile's pages go through shared memory, because `pages` is contiguous along
+// launch or a grid-wide wait), then takes tiles of 8 or 32 tokens.  A tile's
+// pages go through shared memory, because `pages` is contiguous along
 // (layer, K/V) and the slot map along tokens.  A fresh block's table entries
 // are written by the token at its first position, which is always a new one.
 constexpr int kPlanThreads = 512;
@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
       d.dec_off[r] = at[2];
       d.tc_off[r] = at[3];
       d.kv_len[r] = in ? q.ctx + q.fresh : 0;
-      d.row[r] = in ? q.row : 0;
       d.req[r] = in ? make_int4(at[0], q.fresh, q.ctx + q.fresh, q.row) : make_int4(at[0], 0, 0, 0);
       if (in && !idle) {
         int32_t dec, tc;

@@ -60,7 +60,6 @@ struct FastDiv {
 // request is row page(t / P) * P + t % P.
 struct KvDev {
   uint16_t* pool;
-  int64_t num_rows;              // num_pages * per_page (< 2^31)
   int32_t* table;                // [layers][2][max_rows][max_blocks] page of each block, -1: none
   int32_t num_pages;
   int32_t per_page;              // P, tokens per page
@@ -69,7 +68,6 @@ struct KvDev {
   // the planned batch
   int32_t* q_start;              // [R + 1]
   int32_t* kv_len;               // [R] tokens held after the step (0: request left out)
-  int32_t* row;                  // [R] table row
   int32_t* tok_req;              // [T] request of each token, -1: none
   int32_t* tok_pos;              // [T] position of each token in its request
   int4* req;                     // [R] {first token, new tokens, tokens held, table row}, 16-byte aligned

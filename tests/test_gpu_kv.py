@@ -315,6 +315,11 @@ ATTEND = {
     "chunk_group7_d80": ([63, 5], [41, 130], 7, 1, 80, 3, "f16", 0.0),
     "chunk_capped": ([100], [140], 4, 2, 128, 2, "bf16", 12.0),
     "chunk_d96": ([33, 0], [200, 1], 3, 3, 96, 1, "f16", 0.0),
+    "chunk_d112": ([200], [150], 4, 2, 112, 2, "bf16", 0.0),
+    "chunk_group32": ([70, 0], [3, 40], 32, 1, 64, 8, "f16", 0.0),
+    "chunk_group33": ([70, 0], [3, 10], 33, 1, 64, 8, "f16", 0.0),
+    "chunk_many_short": ([0] * 40, [9 + i % 23 for i in range(40)], 8, 8, 64, 2, "f16", 0.0),
+    "decode_group12": ([1000, 3, 128], [1] * 3, 24, 2, 128, 4, "bf16", 0.0),
     "chunk_d256": ([33, 0], [40, 20], 2, 1, 256, 2, "f16", 0.0),
     "chunk_d16": ([5], [300], 4, 4, 16, 4, "bf16", 0.0),
     "mixed": ([9, 600, 0, 77, 0, 300], [1, 1, 90, 1, 400, 33], 8, 4, 128, 2, "bf16", 0.0),
@@ -366,6 +371,29 @@ def test_attend_offsets_past_32_bits(S):
     assert s.num_pages * s.H > 1 << 32
     _, q, out = _fill_and_attend(S, s)
     _check_attend(s, q, out)
+    s.close()
+
+
+def test_rows_that_share_a_prefix(S):
+    """A row that starts with another row's entries (written by the caller)
+    attends over the shared tokens; its own go to its own pages."""
+    P, hkv, d, shared = 4, 2, 64, 24
+    s = Setup(S, [shared, shared], [1, 9], 4, hkv, d, P, "f16", spare_rows=1)
+    n = shared // P
+    s.table[:, :, s.rows[1], :n] = s.table[:, :, s.rows[0], :n]
+    s.kv.table.copy_(torch.from_numpy(s.table))
+    _, q, out = _fill_and_attend(S, s)
+    assert (s.table[:, :, s.rows[1], :n] == s.table[:, :, s.rows[0], :n]).all()
+    _check_attend(s, q, out)
+    s.close()
+
+
+def test_timing_names_the_kernels(S):
+    s = Setup(S, [30, 0], [1, 40], 4, 4, 64, 1, "f16")
+    S.slora_timing_enable(s.pool.handle, True)
+    _fill_and_attend(S, s)
+    t = S.slora_timing_read(s.pool.handle)
+    assert t["kv_plan"][1] == 1 and t["kv_attend"][1] == 1 and t["kv_append"][1] == 0 and t["kv_attend"][0] > 0
     s.close()
 
 
@@ -493,6 +521,8 @@ def test_refusals(S):
     err(kv.append, b, -1, q, k, v)
     err(kv.attend, b, 0, q, out, softcap=-1.0)
     err(kv.attend, b, 0, q, out, scale=float("nan"))
+    err(kv.attend, b, 0, q, out, scale=0.0)
+    err(kv.attend, b, 0, q, out, scale=-1.0)
     err(kv.attend, b, 0, z(2, 260)[:, 1:257], out)       # not 16-byte aligned
     err(kv.attend, b, 0, z(2, 257)[:, :256], out)        # row stride not a multiple of 8
     err(kv.append, b, 0, q, k, v, q_weight=z(64))        # weights go together
