@@ -442,7 +442,9 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hbw = a.hbw, blocks = d.heads_kv / hbw, group = d.heads_q / d.heads_kv, dim = d.head_dim;
   const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, groups);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // what the plan says about the first item is read while the decode kernel
+  // still runs; its parts are read after it, and no block leaves before it
+  bool waited = false;
   // items: request, row, key head (fastest)
   const int per_req = a.rows * d.heads_kv;
   const int64_t items = (int64_t)a.R * per_req, stride = (int64_t)gridDim.x * (WIDE ? 1 : blockDim.x / 32);
@@ -458,6 +460,8 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
     const int64_t us = (int64_t)off * blocks + (int64_t)(hb * tiles + row / kKvRowTile) * nchunk;
     const int64_t g0 = us / sp.run, g1 = (us + nchunk - 1) / sp.run;
     if (g0 == g1) continue;                               // the decode kernel wrote it
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
     JoinSum<V> s;
     for (int64_t g = g0 + (WIDE ? warp : 0); g <= g1; g += 4 * W) {   // four parts on their way at a time
       float2 ml[4];
@@ -507,6 +511,7 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
       __syncthreads();
     }
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Rows are spread over gridDim.y blocks of every CTA's split segment.

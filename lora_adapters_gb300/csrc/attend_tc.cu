@@ -62,12 +62,12 @@ constexpr int kTmemCols = 512;                  // S_A, S_B, O_A, O_B of 128 col
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                    // O is rescaled when a maximum grew by more (powers of two)
 
-// Polls of a wait before it gives up (SLORA_ERR_TIMEOUT); a wait lasts
-// microseconds when all is well.
-constexpr uint32_t kPolls = 1u << 20;
+// A wait gives up after kWaitLimit polls (SLORA_ERR_TIMEOUT).  The longest
+// honest one is the query loader's, for a part of the run: 40 ms for the
+// largest cache that fits this GPU.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kPolls; ++i)
+  for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
