@@ -592,8 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         if (!CAP) mx *= sc;                                   // scale > 0; -inf stays
         if (i == p.i0) {
           m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + kGrow || (m == -INFINITY && mx > m))) {
-          // the products up to the previous tile are done (S came after them)
+        } else if (__any_sync(0xffffffffu, live && (mx > m + kGrow || (m == -INFINITY && mx > m)))) {
+          // the products up to the previous tile are done (S came after them).
+          // Rows without a query have no vote: they hold what an earlier part
+          // left, and when the others are rescaled shows in their last bits.
           const float mn = fmaxf(m, mx);
           const float f = mn == m ? 1.f : ex2(m - mn);
           m = mn;

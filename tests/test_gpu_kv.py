@@ -342,6 +342,26 @@ def test_attend_layers_and_scale(S):
     s.close()
 
 
+@pytest.mark.parametrize("group", [31, 9])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attend_bits_do_not_depend_on_earlier_calls(S, group, dtype):
+    """Groups that leave rows of a 128-row tile without a query: what an earlier
+    call left in their place does not reach the other rows, not even through
+    the moment at which their sums are rescaled."""
+    # several key tiles in every run; the other call fills all 128 rows
+    s = Setup(S, [9000, 7100, 7700], [13, 8, 40], 4 * group, 4, 128, 4, dtype, seed=16)
+    s2 = Setup(S, [9000, 7100, 7700], [12, 8, 40], 4 * 32, 4, 128, 4, dtype, seed=17)
+    b2, q2, out2 = _fill_and_attend(S, s2)
+    b, q, out = _fill_and_attend(S, s)
+    for scale in (0.01, 1.0, 100.0):
+        s2.kv.attend(b2, 0, (q2 * scale).contiguous(), out2[:, : 4 * 32 * 128])
+        again = torch.empty(s.T, 4 * group * 128, dtype=TDT[dtype], device="cuda")
+        s.kv.attend(b, 0, q, again)
+        assert torch.equal(again.view(torch.int16), out[:, : 4 * group * 128].contiguous().view(torch.int16)), scale
+    s.close()
+    s2.close()
+
+
 @pytest.mark.parametrize("new", [1, 64])
 def test_attend_peaked_and_equal_scores(S, new):
     """One key far above the rest, and keys that are all the same: the softmax
