@@ -44,13 +44,7 @@ constexpr int kDecWarps = 4;             // per CTA
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecCtas = 3;              // per SM: 170 registers a thread
 constexpr int kDecMinUnits = 1;          // shortest run (one 640-token request: 12.5 us with 1, 13.0 with 2, 15.6 with 4)
-constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Streaming 16-byte load: every byte of the cache is used once per call, and the
 // rest of its 256 bytes by the same warp or its neighbours (1 % on 7B decode).
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
@@ -129,8 +123,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   const int kk = lane & 3, nn = lane >> 2;
   const int64_t row_bytes = (int64_t)d.heads_kv * dim * 2;
   const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
-  const float sc = CAP ? 2.f * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
-  const float cap2 = a.softcap * kLog2e;
+  const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
   if (u >= u1) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -276,8 +269,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       const int j0 = c * 16 + nn, j1 = j0 + 8;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float x = s[i] * sc;
-        if (CAP) x = cap2 - 2.f * cap2 * __frcp_rn(1.f + ex2(x));   // cap tanh(.), in powers of two
+        const float x = CAP ? capped<true>(s[i], sc, cap_t, cap2) : s[i] * sc;
         const bool seen = (i & 2 ? v1 : v0) && (i & 2 ? j1 : j0) < (i & 1 ? lim1 : lim0);
         s[i] = seen ? x : -INFINITY;
       }

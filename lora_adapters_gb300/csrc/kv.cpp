@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <limits>
 #include <new>
 #include <vector>
 
@@ -361,6 +362,11 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.ldo = ldo;
   a.scale = scale;
   a.softcap = softcap;
+  if (softcap > 0.f) {   // kept finite, four times each too: a product q . k of 0 has the score 0 at every softcap
+    const double most = std::numeric_limits<float>::max() / 4;
+    a.cap_t = (float)std::min((double)scale / softcap, most);
+    a.cap2 = (float)std::min((double)softcap * 1.4426950408889634, most);
+  }
   a.part_o = kv->d_part_o;
   a.part_ml = kv->d_part_ml;
   a.tc_split = kv->d_tc_split;

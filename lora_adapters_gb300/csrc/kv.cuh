@@ -47,4 +47,33 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     Elem<E>::from2(x[6], x[7]));
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+// A capped score in powers of two, log2(e) softcap tanh(t), t = x scale / softcap
+// for the product x = q . k; unit = log2(e) scale, cap2 = log2(e) softcap.
+//   |t| >= 1/4:  1 - 2 / (1 + e^(2t)), absolute error 2^-22, relative 2^-19.6 at 1/4;
+//   below, where that difference cancels:  t (1 - t^2/3 + 2 t^4/15 - 17 t^6/315
+//   + 62 t^8/2835), the series of tanh, whose next term is below 2^-26 there.  In
+//   it log2(e) softcap t is x unit, so a softcap far above the scores leaves them
+//   as they are.
+// ANY = false leaves the second out, for softcap up to kCapNear: the error of a
+// score is then softcap 2^-22, at most 2^-16, for scores of every size.
+constexpr float kCapNear = 64.f;
+template <bool ANY>
+__device__ __forceinline__ float capped(float x, float unit, float cap_t, float cap2) {
+  const float far = fmaf(-2.f * cap2, __fdividef(1.f, 1.f + ex2(x * (2.f * kLog2e * cap_t))), cap2);
+  if (!ANY) return far;
+  const float t = x * cap_t, u = t * t;
+  float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+  p = fmaf(u, p, 2.f / 15.f);
+  p = fmaf(u, p, -1.f / 3.f);
+  const float y = x * unit;
+  return fabsf(t) < 0.25f ? fmaf(y * u, p, y) : far;
+}
+
 }  // namespace slora

@@ -117,6 +117,7 @@ struct KvAttendArgs {
   uint16_t* out;
   int64_t ldo;
   float scale, softcap;
+  float cap_t, cap2;             // softcap > 0: scale / softcap, softcap log2(e)
   float* part_o;                 // parts of split segments: [kv_attend_parts][kv_attend_cols]
   float2* part_ml;               // [kv_attend_parts] their maximum (in powers of two) and sum
   int32_t hbw;                   // neighbouring key heads worked on side by side
