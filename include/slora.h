@@ -592,7 +592,10 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
  * strides ldq, ldo; out rows of tokens without a request are not written;
  * d_out must not overlap d_q.  Slots past a request's length are never used,
  * whatever they hold; a value that is not finite within a request's stored
- * tokens may reach any of that request's outputs, and no other request's.
+ * tokens may reach any of that request's outputs, and no other request's.  A
+ * table entry within a request's length that names no page of the pool, K's or
+ * V's, raises the device status SLORA_ERR_INVALID, and its tokens are left out
+ * of the sums (a row that sees no key at all becomes zeros).
  */
 int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, const void* d_q, int64_t ldq,
                     void* d_out, int64_t ldo, float scale, float softcap);

@@ -161,7 +161,9 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     f.at = (f.hb * hbw + hsub) * dim * 2;
   }
   int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
-  // The next unit's pool rows, one a lane, and where its head starts in them.
+  // The next unit's pool rows, one a lane (-1: past the request's length, kNoPage:
+  // no such page), and where its head starts in them.
+  constexpr int kNoPage = -2;
   auto fetch = [&](int& at) -> int {
     if (f.left == 0) return -1;
     --f.left;
@@ -184,7 +186,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     if (j >= f.len) return -1;
     const int b = (int)a.per_page_div.div((uint32_t)j);
     const int page = __ldg(f.tab + b);
-    return (uint32_t)page < (uint32_t)d.num_pages ? page * P + (j - b * P) : -1;
+    return (uint32_t)page < (uint32_t)d.num_pages ? page * P + (j - b * P) : kNoPage;
   };
   uint4 kf[NC][2], vf[NB][4];
   auto load_k = [&](int slot, int at) {
@@ -212,7 +214,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
   };
-  int at = 0, at_next = 0;
+  int at = 0, at_next = 0, lowest = 0;
   int slot = fetch(at), slot_next = fetch(at_next);
   load_k(slot, at);
   load_v(slot, at);
@@ -265,7 +267,10 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       at = at_next;
       slot_next = fetch(at_next);
       load_k(slot, at);
-      const bool v0 = __shfl_sync(0xffffffffu, held, nn) >= 0, v1 = __shfl_sync(0xffffffffu, held, nn + 8) >= 0;
+      // a token without a K or a V row has no weight
+      const uint32_t none = __ballot_sync(0xffffffffu, held < 0), gone = (none | none >> 16) >> nn;
+      const bool v0 = !(gone & 1), v1 = !(gone >> 8 & 1);
+      lowest = min(lowest, held);
       const int j0 = c * 16 + nn, j1 = j0 + 8;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -368,6 +373,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
   }
+  if (lowest == kNoPage) report_err(d.error, kErrInvalid);
   // after chunks: their kernel may still run, and this grid ends after it
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -25,8 +25,8 @@
 //  - the work, (request, key head, pair of tiles) x 128-key tiles laid end to
 //    end, is cut into equal runs, one per CTA; what a run holds of a segment
 //    cut by its ends goes to scratch as (m, l, O), joined in order afterwards.
-// A position past the request's length reads the request's first key instead
-// and gets weight 0, so whatever its slot holds is never touched.
+// A position past the request's length, or one whose table entry names no page,
+// reads nothing: its key and value are zeros and its weight is 0.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -71,9 +71,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
-__device__ __forceinline__ void report_err(int32_t* err, int code) {
-  if (err) atomicCAS(err, 0, code);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -129,9 +126,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
-// 16 bytes global -> shared, not kept in L1.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes global -> shared, not kept in L1; bytes = 0: zeros, nothing is read.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // One arrival on the barrier when all copies of this thread so far have landed.
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
@@ -268,6 +265,10 @@ struct TcSmem {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t part_full[kParts], part_empty[kParts];
   Part part[kParts];
+  // Positions of a K tile whose entry names no page, a bit each, in the word of the
+  // warp that loads them.  Tile k is loaded when the scores of tile k - 2 are done,
+  // which begin after the softmax of tile k - 3: of four places, k - 4's is free.
+  alignas(16) uint32_t holes[4][4];
   uint32_t tmem_slot;
 };
 
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   if (warp == kWarpMma) tmem_alloc(&sm.tmem_slot, kTmemCols);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kv_full[s], kLoaders);
+      mbar_init(&sm.kv_full[s], kLoaders + (s & 1 ? 0 : 4));   // even stages hold K tiles, whose holes come with them
       mbar_init(&sm.kv_empty[s], 1);
     }
     for (int k = 0; k < kParts; ++k) {
@@ -358,20 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       if (p.i1 == 0) break;
       const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)p.row * d.max_blocks;
       const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)p.hk * dim * 2 + ch * 16;
-      int kslot, vslot;
+      int kslot, vslot;            // pool rows, -1: none
+      uint32_t holes;
       auto lookup = [&](int i) {
-        int j = i * kKvTile + 32 * warp + lane;
-        j = j < p.len ? j : 0;
-        const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
-        const int kp = __ldg(tab + b), vp = __ldg(tab + plane + b);
-        // an entry that names no page: row 0, as the request's result is
-        // undefined (its plan reported the entry) but the copy is not
-        kslot = (uint32_t)kp < (uint32_t)d.num_pages ? kp * d.per_page + off : 0;
-        vslot = (uint32_t)vp < (uint32_t)d.num_pages ? vp * d.per_page + off : 0;
+        const int j = i * kKvTile + 32 * warp + lane;
+        kslot = vslot = -1;
+        if (j < p.len) {
+          const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
+          const int kp = __ldg(tab + b), vp = __ldg(tab + plane + b);
+          if ((uint32_t)kp < (uint32_t)d.num_pages && (uint32_t)vp < (uint32_t)d.num_pages) {
+            kslot = kp * d.per_page + off;
+            vslot = vp * d.per_page + off;
+          }
+        }
+        holes = __ballot_sync(0xffffffffu, j < p.len && kslot < 0);
+        if (holes && lane == 0) report_err(d.error, kErrInvalid);
       };
       lookup(p.i0);
       for (int i = p.i0; i < p.i1 && ok; ++i) {
         const int kc = kslot, vc = vslot;
+        const uint32_t hc = holes;
         if (i + 1 < p.i1) lookup(i + 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half, ++n) {
@@ -384,11 +391,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int row = __shfl_sync(0xffffffffu, half ? vc : kc, 4 * j + sub);
-            const uint8_t* src = base + row * row_bytes;
+            const uint8_t* src = base + max(row, 0) * row_bytes;
+            const uint32_t bytes = row < 0 ? 0 : 16;
             // row 32 w + 4 j + sub of the tile; its chunk ch goes to ch ^ (row & 7)
             const uint32_t to = dst + 4 * j * kRowBytes + ((ch ^ ((4 * j + sub) & 7)) << 4);
-            cp16(to, src);
-            if (ch1) cp16(to + kAtom, src + 128);
+            cp16(to, src, bytes);
+            if (ch1) cp16(to + kAtom, src + 128, bytes);
+          }
+          if (half == 0 && lane == 0) {
+            sm.holes[(n >> 1) & 3][warp] = hc;
+            mbar_arrive(&sm.kv_full[st]);
           }
           cp_arrive(&sm.kv_full[st]);
         }
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
     const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
     const int my_tok = rho / group, my_head = rho - my_tok * group;
-    uint32_t ns = 0, nf = 0, nq = 0;
+    uint32_t ns = 0, nf = 0, nq = 0, nk = 0;                  // nk: K tiles of earlier parts
     for (;;) {
       if (!next_part(p, true)) break;
       __syncwarp();
@@ -545,6 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       const int end = x ? p.end[1] : p.end[0], tokens = x ? p.tokens[1] : p.tokens[0];
       const uint32_t has0 = p.end[0] > p.i0, has1 = p.end[1] > p.i0, qb = (nq + (x ? has0 : 0)) % kQTiles;
       nq += has0 + has1;
+      const uint32_t k0 = nk - p.i0;
+      nk += p.i1 - p.i0;
       const bool live = my_tok < tokens;
       const int pos_first = p.pos + x * tpt;                  // the tile's earliest position
       const int pos = pos_first + min(my_tok, max(tokens - 1, 0));
@@ -561,9 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         // capped, masked and searched for the maximum
         uint32_t s[4][32];
         const int lim = pos - i * kKvTile;
-        const bool edge = (i + 1) * kKvTile - 1 > pos_first;  // some row may not see the whole tile
         float mx = -INFINITY, my = -INFINITY;
         tmem_ld32_nowait(t_s, s[0]);
+        const uint4 hole = *reinterpret_cast<const uint4*>(sm.holes[(k0 + i) & 3]);
+        // some row may not see the whole tile
+        const bool edge = (i + 1) * kKvTile - 1 > pos_first || (hole.x | hole.y | hole.z | hole.w) != 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_wait_ld(s[c]);
@@ -574,9 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
               s[c][j] = __float_as_uint(capped<CAP == kCapAny>(__uint_as_float(s[c][j]), sc, cap_t, cap2));
           }
           if (edge) {
+            const uint32_t gone = (lim >= 32 * c + 31 ? 0u : lim < 32 * c ? ~0u : ~1u << (lim - 32 * c)) |
+                                  (c == 0 ? hole.x : c == 1 ? hole.y : c == 2 ? hole.z : hole.w);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (32 * c + j > lim) s[c][j] = 0xff800000u;    // -inf
+              if ((gone >> j) & 1) s[c][j] = 0xff800000u;     // -inf
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {

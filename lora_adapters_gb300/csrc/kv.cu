@@ -13,12 +13,6 @@
 namespace slora {
 namespace {
 
-constexpr int kErrInvalid = -1;   // == SLORA_ERR_INVALID
-
-__device__ __forceinline__ void report_err(int32_t* err, int code) {
-  if (err) atomicCAS(err, 0, code);
-}
-
 // ================================================================ plan
 // Per request r, with len = ctx + new:
 //   q_start_r = sum of the earlier requests' new tokens,

@@ -1,4 +1,5 @@
-// Element conversions shared by the key-value cache kernels.
+// Element conversions, scores and error reports shared by the key-value cache
+// kernels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -45,6 +46,11 @@ template <class E>
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(Elem<E>::from2(x[0], x[1]), Elem<E>::from2(x[2], x[3]), Elem<E>::from2(x[4], x[5]),
                     Elem<E>::from2(x[6], x[7]));
+}
+
+constexpr int kErrInvalid = -1;   // == SLORA_ERR_INVALID
+__device__ __forceinline__ void report_err(int32_t* err, int code) {
+  if (err) atomicCAS(err, 0, code);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -1,9 +1,12 @@
 """The paged key-value cache operators at their edges, on the GPU against the
 fp64 oracle; tolerances are those of tests/test_gpu_kv.py where none is derived
 beside the test."""
+import numpy as np
 import pytest
+import torch
 
-from tests.test_gpu_kv import S, Setup, _check_attend, _fill_and_attend  # noqa: F401
+from oracle import kv as okv
+from tests.test_gpu_kv import S, Setup, U, _check_attend, _fill_and_attend, f64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -33,4 +36,44 @@ def test_softcap_around_large_scores(S, new):
     s = Setup(S, [300], [new], 4, 4, 64, 1, "f16", seed=22)
     _, q, out = _fill_and_attend(S, s, softcap=100.0, scale=64 ** -0.5 * 16)
     _check_attend(s, q, out, softcap=100.0, scale=64 ** -0.5 * 16)
+    s.close()
+
+
+@pytest.mark.parametrize("which", ["K", "V", "KV"])
+@pytest.mark.parametrize("dtype,hq,hkv,d,P", [("f16", 4, 2, 64, 4), ("bf16", 5, 1, 128, 3), ("f16", 3, 3, 80, 1),
+                                               ("bf16", 2, 2, 256, 2)])
+def test_entries_that_name_no_page(S, which, dtype, hq, hkv, d, P):
+    """A table entry within a request's length that names no page is reported,
+    its tokens get no weight, and no other memory stands in for them (page 0
+    holds NaN); the other requests keep their bits."""
+    ctx, new = [700, 300, 600, 5, 2000, 90, 60], [1, 40, 150, 9, 1, 1, 30]
+    s = Setup(S, ctx, new, hq, hkv, d, P, dtype, seed=26, first_page=1)
+    s.pool.buffer[0].fill_(float("nan"))
+    b, q, out = _fill_and_attend(S, s)
+    good = out.clone()
+    holes = {0: [0, 5], 1: [2, 30], 2: list(range(128 // P + 1, 256 // P + 1)), 4: [399 // P],
+             5: list(range(-(-91 // P))), 6: list(range(-(-90 // P)))}       # 5 and 6: nothing is left
+    for r, blocks in holes.items():
+        for i, blk in enumerate(blocks):
+            for j in (0, 1):
+                if "KV"[j] in which:
+                    s.kv.table[0, j, int(s.rows[r]), blk] = [-1, s.num_pages, -7, 1 << 30][i % 4]
+    s.kv.attend(b, 0, q, out[:, : hq * d])
+    assert s.pool.status() == S.ERR_INVALID and s.pool.status() == S.OK
+    cache, t0 = s.cache_rows(), 0
+    for r, (c, n) in enumerate(zip(ctx, new)):
+        if r not in holes:
+            assert torch.equal(out[t0: t0 + n], good[t0: t0 + n]), r
+        elif r in (5, 6):
+            assert not out[t0: t0 + n, : hq * d].any(), r
+        else:
+            held = np.array([p for p in range(c + n) if p // P not in holes[r]])
+            at = torch.from_numpy(held).cuda()
+            keys, vals = (f64(cache[s.slot_rows(r, 0, j)[at]]).reshape(-1, hkv, d) for j in (0, 1))
+            want = okv.attend(f64(q[t0: t0 + n]).reshape(n, hq, d), keys, vals, held.size - n, d ** -0.5, 0.0)
+            got = f64(out[t0: t0 + n, : hq * d]).reshape(n, hq, d)
+            vmax = np.repeat(np.abs(vals).max((0, 2)), hq // hkv)[None, :, None]
+            err = np.abs(got - want)
+            assert (err <= U[dtype] * np.abs(want) + (2.0 ** -12 + U[dtype]) * vmax).all(), (r, err.max())
+        t0 += n
     s.close()
