@@ -337,7 +337,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       if (row >= rows) continue;
       const float l = x ? l1 : l0;
       if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         uint16_t* dst = a.out + (int64_t)(q0 + row / group) * a.ldo + (int64_t)(hk * group + row % group) * dim + nn * 8;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -389,9 +389,10 @@ constexpr int kJoinWideWarps = 16;
 template <int V>
 struct JoinSum {
   float m = -INFINITY, l = 0.f, o[V] = {};
-  // (a part with m = -inf has no weight, and its sums may not have been written)
+  // (a part without weight: its sums may not have been written.  m = -inf alone does
+  // not say so: scores that are not numbers leave it there, and l is not a number)
   __device__ __forceinline__ void add(float2 ml, const float (&y)[V]) {
-    if (ml.x == -INFINITY) return;
+    if (ml.y == 0.f) return;
     const float mn = fmaxf(m, ml.x), f = ex2(m - mn), w = ex2(ml.x - mn);
     m = mn;
     l = l * f + ml.y * w;
@@ -416,7 +417,7 @@ __device__ __forceinline__ void load_row(const float* row, int lane, float (&y)[
 }
 template <class E, int V>
 __device__ __forceinline__ void store_row(uint16_t* row, int lane, int dim, const float (&o)[V], float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   if constexpr (V == 2) {
     if (lane * 2 < dim) *reinterpret_cast<uint32_t*>(row + lane * 2) = Elem<E>::from2(o[0] * inv, o[1] * inv);
   } else {
@@ -493,13 +494,13 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
         const float own = m;
 #pragma unroll
         for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        if (lane < W) s_f[lane] = own == -INFINITY ? 0.f : ex2(own - m);
+        if (lane < W) s_f[lane] = ex2(own - m);
         __syncwarp();
         float l = 0.f, y[V] = {};
 #pragma unroll 4
         for (int k = 0; k < W; ++k) {
+          if (s_l[k] == 0.f) continue;                    // no weight
           const float f = s_f[k];
-          if (f == 0.f) continue;
           l += s_l[k] * f;
 #pragma unroll
           for (int j = 0; j < V; ++j) y[j] += s_o[k][j * 32 + lane] * f;

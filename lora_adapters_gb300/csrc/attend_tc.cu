@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         // own 32 rows one row a lane and reads them back row by row, so that
         // global memory sees whole rows.
         uint8_t* stage = sm.q[qb][0] + 32 * quarter * 256;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.tok + x * tpt + my_tok) * a.ldo +
                                                           (int64_t)(p.hk * group + my_head) * dim)
                              : reinterpret_cast<uint8_t*>(a.tc_part_o + part * kKvTile);
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty[qb]);
       }
-      if (!whole && live) a.tc_part_ml[part] = make_float2(m, l);   // m = -inf: the part has no weight, O unwritten
+      if (!whole && live) a.tc_part_ml[part] = make_float2(m, l);   // l = 0: the part has no weight, O unwritten
     }
   }
   if (!ok) report_err(d.error, kErrTimeout);

@@ -77,3 +77,37 @@ def test_entries_that_name_no_page(S, which, dtype, hq, hkv, d, P):
             assert (err <= U[dtype] * np.abs(want) + (2.0 ** -12 + U[dtype]) * vmax).all(), (r, err.max())
         t0 += n
     s.close()
+
+
+@pytest.mark.parametrize("ctx,new", [(40, 1), (3000, 1), (20000, 1), (100, 40), (20000, 16)])
+def test_a_query_that_is_not_a_number(S, ctx, new):
+    """It makes its own row NaN, wherever its segment is split, and no other."""
+    s = Setup(S, [ctx, 7], [new, 1], 4, 2, 64, 4, "f16", seed=24)
+    b, q, out = _fill_and_attend(S, s)
+    want = out.clone()
+    t = new // 2
+    want[t, 3 * 64: 4 * 64] = float("nan")
+    q[t, 3 * 64 + 5] = float("nan")          # head 3 of one token
+    s.kv.attend(b, 0, q, out[:, : 4 * 64])
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(9.0), want.nan_to_num(9.0))
+    s.close()
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("heads,ctx,new,first,count", [(2, 1000, 1, 16, 16), (2, 1000, 1, 990, 4), (1, 1000, 1, 0, 1000),
+                                                       (2, 40000, 1, 16, 32), (1, 16000, 16, 256, 128),
+                                                       (2, 16000, 16, 300, 1), (2, 40, 30, 3, 2)])
+def test_keys_that_are_not_numbers(S, heads, ctx, new, first, count, softcap):
+    """They reach every row that sees them, also where a part of a split segment
+    holds nothing else."""
+    s = Setup(S, [ctx, 7], [new, 1], heads, heads, 64, 4, "f16", seed=25)
+    b, q, out = _fill_and_attend(S, s, softcap=softcap)
+    want = out.clone()
+    at = 64 * (heads - 1)                    # the last head's
+    want[:new, at: at + 64] = float("nan")
+    s.cache_rows()[s.slot_rows(0, 0, 0)[first: first + count], at:] = float("nan")
+    s.kv.attend(b, 0, q, out[:, : 64 * heads], softcap=softcap)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(9.0), want.nan_to_num(9.0))
+    s.close()
