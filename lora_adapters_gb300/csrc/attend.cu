@@ -22,7 +22,9 @@
 //    same permutation for K and Q, chosen so that a 16-byte load is two steps'
 //    operands;
 //  - P is split into two 16-bit parts, hi and lo = p - hi, each its own
-//    product: the weights keep twice the storage type's bits;
+//    product: the weights keep twice the storage type's bits.  fp16 has few
+//    exponents, so there P is 2^14 e^(s - m) (its sum alike): 22 bits for weights
+//    above 2^-28 of the largest, an error of 2^-39 of it below;
 //  - the work, (request, row tile, key head) x 16-token units laid end to end,
 //    is cut into equal runs, one per group of warps, whatever the lengths.  A
 //    run that starts or ends inside a segment leaves (m, l, o) in scratch, and
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(kDecThreads, D <= 128 ? kDecCtas : 2)
 kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int NB = D / 64;        // 64-element blocks of a head (V)
   constexpr int NC = D / 32;        // 32-element chunks of a head (K, Q)
+  constexpr float kUp = Elem<E>::kBf16 ? 0.f : 14.f;   // weights are held times 2^kUp
   const KvDev& d = a.kv;
   const int tid = threadIdx.x, lane = tid & 31;
   const int hbw = a.hbw, blocks = d.heads_kv / hbw;
@@ -298,7 +301,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         }
       }
       // a row that has seen no key yet has m = -inf; its weights are zeros
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      const float z0 = m0 == -INFINITY ? 0.f : m0 - kUp, z1 = m1 == -INFINITY ? 0.f : m1 - kUp;
       const float p0 = ex2(s[0] - z0), p1 = ex2(s[1] - z1), p2 = ex2(s[2] - z0), p3 = ex2(s[3] - z1);
       l0 += p0 + p2;
       l1 += p1 + p3;

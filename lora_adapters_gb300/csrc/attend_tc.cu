@@ -10,7 +10,10 @@
 // and O / sum(P) at the end.  S, P and O live in TMEM; S is read once and P,
 // rounded to the storage type (its sum is taken before the rounding), written
 // over it.  The rounding adds at most one unit of the storage type relative to
-// the largest value, the size of the result's own rounding.
+// the largest value, the size of the result's own rounding.  fp16 has few
+// exponents, so there P is 2^7 times that (its sum alike, which the quotient
+// undoes): 11 bits for weights above 2^-21 of 2^m, an error of 2^-32 of it below,
+// and at most 2^15 where the maximum has grown past m.
 //
 // Bound: the tensor cores where contexts are long (4 head_dim operations per
 // score against a softmax of about ten instructions, the exponentials first),
@@ -18,7 +21,7 @@
 //  - two tiles (A, B) of one request and key head share every K and V tile and
 //    take turns: while one tile's softmax runs, the tensor cores work on the
 //    other's products;
-//  - O is rescaled only when a row's maximum has grown by more than 2^8 (P
+//  - O is rescaled only when a row's maximum has grown by more than 2^8 (e^(s - m)
 //    then stays below 2^8, and fp32 sums lose nothing by it);
 //  - keys and values are gathered from their pages by four warps with 16-byte
 //    asynchronous copies into a ring of tiles;
@@ -547,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
     const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
+    constexpr float kUp = Elem<E>::kBf16 ? 0.f : 7.f;        // weights are held times 2^kUp
     const int my_tok = rho / group, my_head = rho - my_tok * group;
     uint32_t ns = 0, nf = 0, nq = 0, nk = 0;                  // nk: K tiles of earlier parts
     for (;;) {
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
             tmem_st16(t_o + c, r);
           }
         }
-        const float z = m == -INFINITY ? 0.f : m;             // a row that sees nothing yet: all weights 0
+        const float z = m == -INFINITY ? 0.f : m - kUp;       // a row that sees nothing yet: all weights 0
         const uint64_t sc2 = CAP ? pair(1.f, 1.f) : pair(sc, sc), z2 = pair(-z, -z);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

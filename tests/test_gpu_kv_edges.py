@@ -1,12 +1,14 @@
 """The paged key-value cache operators at their edges, on the GPU against the
 fp64 oracle; tolerances are those of tests/test_gpu_kv.py where none is derived
 beside the test."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import kv as okv
-from tests.test_gpu_kv import S, Setup, U, _check_attend, _fill_and_attend, f64  # noqa: F401
+from tests.test_gpu_kv import S, Setup, TDT, U, _check_attend, _fill_and_attend, f64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +113,52 @@ def test_keys_that_are_not_numbers(S, heads, ctx, new, first, count, softcap):
     assert torch.equal(torch.isnan(out), torch.isnan(want))
     assert torch.equal(out.nan_to_num(9.0), want.nan_to_num(9.0))
     s.close()
+
+
+def _long_segments(S, ctx, new, hkv, d, R, dtype, above, sink, rest):
+    """R requests over the same ctx + new keys, key 1000 `above` nats over the others, all of
+    whose weights are e^-above; its value `sink`, the others' from rest(n, cols).  With
+    so many requests a segment lies in one run, whose running sums serve all of it.
+    The outputs [R, new, heads * d], and for every token the sums of weights and of
+    weighted values in 64 bits."""
+    s = Setup(S, [ctx], [new], hkv, hkv, d, 64, dtype, seed=23, spare_rows=R - 1, T=R * new)
+    s.oracle_plan()
+    n = ctx + new
+    s.kv.table[:] = torch.from_numpy(s.table[:, :, s.rows[0]]).cuda()[:, :, None]
+    b = s.plan(ctx=s.dev([ctx] * R), new=s.dev([new] * R), pages=s.dev(np.tile(s.opened, R)), rows=s.dev(np.arange(R)))
+    k = torch.zeros(n, hkv * d, device="cuda")
+    k[1000] = above / (4.0 * d ** 0.5)       # q . k scale = above
+    v = rest(n, hkv * d).to(TDT[dtype])
+    v[1000] = sink
+    cache = s.cache_rows()
+    cache[s.slot_rows(0, 0, 0)] = k.to(TDT[dtype])
+    cache[s.slot_rows(0, 0, 1)] = v
+    q = torch.full((R * new, hkv * d), 4.0, dtype=TDT[dtype], device="cuda")
+    out = torch.empty_like(q)
+    s.kv.attend(b, 0, q, out)
+    assert s.pool.status() == S.OK
+    w = torch.full((n, 1), math.exp(-above), dtype=torch.float64, device="cuda")
+    w[1000] = 1
+    sums = torch.cumsum(w, 0)[-new:], torch.cumsum(w * v.double(), 0)[-new:]
+    s.close()
+    return out.view(R, new, -1).double(), *sums
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("above", [14, 17, 18, 20])
+@pytest.mark.parametrize("ctx,new,hkv,d,R", [(1 << 17, 1, 16, 16, 114), (1 << 17, 16, 4, 64, 40)])
+def test_small_weights_of_a_long_context(S, dtype, above, ctx, new, hkv, d, R):
+    """One key `above` nats over 131,072 others, its value zero: the result is what
+    all the others add up to, e^-above each, in the decode and the chunk kernel.
+
+    Tolerance: the result's rounding and, in the chunk kernel, the weights' (u each);
+    2^-12 for fp32 arithmetic; the products, one for every 16 keys (two in the decode
+    kernel), cut off at most 2^-23 of the running sum each; and the weights' own error
+    below fp16's exponents, 2^-32 of the largest for each key (2^-39)."""
+    out, w, want = _long_segments(S, ctx, new, hkv, d, R, dtype, above, 0.0,
+                                  lambda n, c: torch.randn(n, c, device="cuda").abs())
+    u, decode = U[dtype], new == 1
+    tol = (2 * u + 2.0 ** -12 + ctx * 2.0 ** (-26 if decode else -27)) * want / w
+    tol += 2.0 ** (-39 if decode else -32) * math.exp(above) * want
+    err = (out - want / w).abs()
+    assert (err <= tol).all(), float((err / tol).max())
