@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       const int pos_first = p.pos + x * tpt;                  // the tile's earliest position
       const int pos = pos_first + min(my_tok, max(tokens - 1, 0));
       float m = -INFINITY;
-      uint64_t l2a = 0, l2b = 0;                              // pairs of partial sums (+0, +0)
+      float l = 0.f;
       for (int i = p.i0; i < end; ++i) {
         if (!wait_warp(&sm.s_full[x], ns & 1)) {
           ok = false;
@@ -617,8 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
           const float mn = fmaxf(m, mx);
           const float f = mn == m ? 1.f : ex2(m - mn);
           m = mn;
-          l2a = fma2(l2a, pair(f, f), 0);
-          l2b = fma2(l2b, pair(f, f), 0);
+          l *= f;
 #pragma unroll 1
           for (int c = 0; c < dim; c += 16) {
             float v[16];
@@ -630,6 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
           }
         }
         const float z = m == -INFINITY ? 0.f : m - kUp;       // a row that sees nothing yet: all weights 0
+        // a tile's weights are added up first: one by one, small ones are lost beside a large sum
+        uint64_t l2a = 0, l2b = 0;                            // pairs of partial sums (+0, +0)
         const uint64_t sc2 = CAP ? pair(1.f, 1.f) : pair(sc, sc), z2 = pair(-z, -z);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -650,10 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[x]);
+        const float2 la = unpair(l2a), lb = unpair(l2b);
+        l += (la.x + la.y) + (lb.x + lb.y);
       }
       if (!ok) break;
-      const float2 la = unpair(l2a), lb = unpair(l2b);
-      const float l = (la.x + la.y) + (lb.x + lb.y);
       const bool whole = p.whole != 0;
       // slot 0: the segment began in an earlier run; slot 1: it begins here
       const int64_t part = (((int64_t)blockIdx.x * 2 + (p.i0 == 0 ? 1 : 0)) * 2 + x) * kKvTile + rho;

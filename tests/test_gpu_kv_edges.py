@@ -162,3 +162,14 @@ def test_small_weights_of_a_long_context(S, dtype, above, ctx, new, hkv, d, R):
     tol += 2.0 ** (-39 if decode else -32) * math.exp(above) * want
     err = (out - want / w).abs()
     assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_chunk_sum_of_small_weights_beside_a_large_one(S, dtype):
+    """One key 17.4375 nats over 262,144 others, alone with a value: the result is 1
+    over the sum of the weights, 0.7 % of it in weights below 2^-25 of the largest.
+    Tolerance: the result's rounding and 2^-12."""
+    out, w, want = _long_segments(S, 1 << 18, 16, 4, 64, 40, dtype, 17.4375, 1.0,
+                                  lambda n, c: torch.zeros(n, c, device="cuda"))
+    err = (out * w / want - 1).abs().max().item()
+    assert err <= U[dtype] + 2.0 ** -12, err
