@@ -588,7 +588,12 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
  *     out = sum_{j <= p} softmax_j(c(scale * q . k_j)) v_j,
  * c(s) = softcap * tanh(s / softcap), or s itself for softcap 0.  The step's
  * own keys and values must be appended first.  scale > 0.  Scores, softmax and sums are
- * fp32, the result is rounded once.  d_q, d_out: T rows of heads_q * head_dim,
+ * fp32 (a sum of n keys' products on the tensor cores may come out n 2^-26 of itself too
+ * small), the result is rounded once.  For the product with the values the softmax weights
+ * are held in the storage type: in two parts, twice its bits, where a request has at most 8
+ * rows (new tokens times query heads of a key head), head_dim is below 64 or above 128, or
+ * more than 32 query heads share a key head; elsewhere in one, which adds at most one unit
+ * of the type relative to the largest value.  d_q, d_out: T rows of heads_q * head_dim,
  * strides ldq, ldo; out rows of tokens without a request are not written;
  * d_out must not overlap d_q.  Slots past a request's length are never used,
  * whatever they hold; a value that is not finite within a request's stored
