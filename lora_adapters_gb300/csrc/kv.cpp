@@ -347,7 +347,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   if (int rc = check_batch(kv, batch, layer)) return rc;
   if (!std::isfinite(scale) || scale <= 0.f) return fail(SLORA_ERR_INVALID, "scale must be finite and > 0");
   if (!std::isfinite(softcap) || softcap < 0.f) return fail(SLORA_ERR_INVALID, "softcap must be finite and >= 0");
-  if (kv->T == 0 || kv->R == 0) return SLORA_OK;
+  if (kv->T == 0 || kv->R == 0 || kv->max_new == 0) return SLORA_OK;   // no request can have a row
   const int64_t wq = (int64_t)kv->dev.heads_q * kv->dev.head_dim;
   if (int rc = check_rows("q", d_q, ldq, wq)) return rc;
   if (int rc = check_rows("out", d_out, ldo, wq)) return rc;

@@ -173,3 +173,17 @@ def test_chunk_sum_of_small_weights_beside_a_large_one(S, dtype):
                                   lambda n, c: torch.zeros(n, c, device="cuda"))
     err = (out * w / want - 1).abs().max().item()
     assert err <= U[dtype] + 2.0 ** -12, err
+
+
+def test_a_step_without_new_tokens(S):
+    """Planned with max_new 0 (room for tokens, none in use): append and attend write nothing."""
+    s = Setup(S, [4, 8], [0, 0], 2, 1, 64, 4, "f16", T=6)
+    b = s.plan()
+    q = s.randn(6, 128)
+    out = torch.full((6, 128), 3.0, dtype=torch.float16, device="cuda")
+    before = s.pool.buffer.clone()
+    s.kv.append(b, 0, q, q[:, :64], q[:, 64:], q_out=out)
+    s.kv.attend(b, 0, q, out)
+    assert s.pool.status() == S.OK and (out == 3).all()
+    assert torch.equal(s.pool.buffer.view(torch.int16), before.view(torch.int16))
+    s.close()
