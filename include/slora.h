@@ -488,8 +488,8 @@ typedef struct slora_kv_config {
 /*
  * The planned batch.  Its arrays lie in the caller's d_arrays (see
  * slora_kv_create), at the same places in every batch: the next slora_kv_plan
- * on the cache overwrites them and makes earlier batches stale (generation
- * check).
+ * on the cache overwrites them and makes earlier batches stale.  A batch serves the
+ * cache that planned it alone (both by the generation).
  */
 typedef struct slora_kv_batch {
   int32_t R;                /* requests */

@@ -7,6 +7,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -42,6 +43,9 @@ struct slora_kv {
 };
 
 namespace {
+
+// Planned batches of all caches are numbered together: a batch is one cache's alone.
+std::atomic<uint64_t> g_generation{0};
 
 struct NvtxRange {
   explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -132,7 +136,7 @@ int64_t place_arrays(KvDev& d, int32_t* base) {
 int check_batch(const slora_kv* kv, const slora_kv_batch* b, int32_t layer) {
   if (!kv) return fail(SLORA_ERR_INVALID, "kv is NULL");
   if (!b || b->generation == 0 || b->generation != kv->generation)
-    return fail(SLORA_ERR_INVALID, "the batch is missing or stale (plan again after every slora_kv_plan)");
+    return fail(SLORA_ERR_INVALID, "the batch is missing, stale (use the last slora_kv_plan's) or another cache's");
   if (layer < 0 || layer >= kv->dev.layers)
     return fail(SLORA_ERR_INVALID, "layer %d not in [0, %d)", layer, kv->dev.layers);
   return SLORA_OK;
@@ -289,7 +293,7 @@ int slora_kv_plan(slora_kv* kv, int32_t R, const int32_t* d_row, const int32_t* 
     CUDA_TRY(launch_kv_plan(a, kv->pv.compute));
     tm.done();
   }
-  kv->generation++;
+  kv->generation = ++g_generation;
   kv->R = R;
   kv->T = T;
   kv->max_new = max_new;

@@ -187,3 +187,27 @@ def test_a_step_without_new_tokens(S):
     assert s.pool.status() == S.OK and (out == 3).all()
     assert torch.equal(s.pool.buffer.view(torch.int16), before.view(torch.int16))
     s.close()
+
+
+def test_a_batch_of_another_cache_is_refused(S):
+    """Two caches on one pool, planned in lock-step with different sizes: a batch's
+    tensors are checked for its own T, so the other cache must not take it."""
+    s = Setup(S, [4, 8], [1, 1], 2, 1, 64, 4, "f16", T=6)
+    other = S.KVCache(s.pool, 1, 2, 1, 64, 4, 8)
+    mine = s.plan()
+    pages = s.dev([0, 1] * 2)
+    theirs = other.plan(s.dev([0, 0]), s.dev([1, 1]), pages, 2, 1)
+    q, out = s.randn(6, 128), torch.full((6, 128), 3.0, dtype=torch.float16, device="cuda")
+    for kv, b in ((s.kv, theirs), (other, mine)):
+        with pytest.raises(S.SloraError) as e:
+            kv.append(b, 0, q, q[:, :64], q[:, 64:], q_out=out)
+        assert e.value.code == S.ERR_INVALID
+        with pytest.raises(S.SloraError) as e:
+            kv.attend(b, 0, q, out)
+        assert e.value.code == S.ERR_INVALID
+    assert (out == 3).all()
+    other.append(theirs, 0, q, q[:, :64], q[:, 64:], q_out=out)
+    other.attend(theirs, 0, q, out)
+    assert s.pool.status() == S.OK and (out[2:] == 3).all()
+    other.close()
+    s.close()
