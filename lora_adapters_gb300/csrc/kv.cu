@@ -55,9 +55,17 @@ __device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ct
   const int len = ctx + fresh;
   *dec = *tc = 0;
   if (a.tpt > 0 && rows > kKvChunkRows) {
-    int32_t n = 0;
-    for (int t = 0; t < fresh; t += 2 * a.tpt) n = sat_add(n, kKvPairUnits + (ctx + min(fresh, t + 2 * a.tpt) + kKvTile - 1) / kKvTile);
-    *tc = n;
+    // pairs of S = 2 tpt tokens; full pair i needs floor((ctx + S + 127 + S i) / 128)
+    // key tiles.  S is even, so 64 pairs on it is S / 2 tiles more: one step for all the
+    // pairs with the same i % 64, whatever the lengths
+    const int step = 2 * a.tpt, full = fresh / step, first = ctx + step + kKvTile - 1;
+    int64_t n = (int64_t)kKvPairUnits * full;
+    for (int i = 0; i < min(full, 64); ++i) {
+      const int64_t same = (full - i + 63) / 64;
+      n += same * ((first + step * i) / kKvTile) + same * (same - 1) / 2 * a.tpt;
+    }
+    if (fresh % step) n += kKvPairUnits + (len + kKvTile - 1) / kKvTile;
+    *tc = (int32_t)min(n, (int64_t)0x7fffffff);
   } else {
     *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + kKvUnit - 1) / kKvUnit), (int64_t)0x7fffffff);
   }

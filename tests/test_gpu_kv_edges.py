@@ -211,3 +211,32 @@ def test_a_batch_of_another_cache_is_refused(S):
     assert s.pool.status() == S.OK and (out[2:] == 3).all()
     other.close()
     s.close()
+
+
+def test_plan_is_quick_at_lengths_that_are_no_batch(S):
+    """New tokens far beyond T (a caller's mistake that only the device sees) are left out
+    and reported without counting their tiles one by one."""
+    P, R = 1024, 3
+    pool = S.Pool(40, 64 * P, "f16", [(8, 8)], 1, 1, 8, device=torch.device("cuda", 0))
+    kv = S.KVCache(pool, 1, 32, 1, 64, R, (1 << 30) // P)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    args = dev([0, 5, 77]), dev([1 << 30, (1 << 30) - 5, 1 << 29]), dev([0, 1])
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    b = kv.plan(*args, 8, 1 << 30)
+    end.record()
+    assert pool.status() == S.ERR_INVALID
+    assert not b.kv_len.any() and (b.tok_req == -1).all()
+    assert start.elapsed_time(end) < 20.0        # 2^27 steps a request took a second
+    kv.close()
+    pool.close()
+
+
+@pytest.mark.parametrize("dtype,hq,ctx,new", [("f16", 32, 0, 700), ("bf16", 31, 333, 517), ("f16", 20, 127, 900),
+                                               ("bf16", 9, 5, 2000)])
+def test_chunks_of_many_tiles(S, dtype, hq, ctx, new):
+    """More than 64 pairs of row tiles in a request, beside requests with none and one."""
+    s = Setup(S, [ctx, 40, 0], [new, 1, 3], hq, 1, 64, 4, dtype, seed=27)
+    _, q, out = _fill_and_attend(S, s)
+    _check_attend(s, q, out)
+    s.close()
