@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <limits>
 #include <new>
 #include <vector>
@@ -150,6 +151,21 @@ int check_rows(const char* what, const void* p, int64_t ld, int64_t cols) {
     return fail(SLORA_ERR_INVALID, "%s: row stride %lld must be a multiple of 8 and cover %lld elements", what,
                 (long long)ld, (long long)cols);
   return SLORA_OK;
+}
+
+// Whether two matrices of T rows of `cols` elements share any.  Rows of one stride are
+// compared exactly (slices of one product lie between each other's rows); of two
+// strides, only their starts.
+bool overlap(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t cols, int64_t T) {
+  if (p == q) return true;
+  if (ldp != ldq) return false;
+  const int64_t apart = (static_cast<const char*>(q) - static_cast<const char*>(p)) / 2;
+  int64_t rows = apart / ldp, off = apart % ldp;
+  if (off < 0) {
+    off += ldp;
+    --rows;
+  }
+  return (off < cols && std::abs(rows) < T) || (ldp - off < cols && std::abs(rows + 1) < T);
 }
 
 }  // namespace
@@ -316,6 +332,8 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   if (int rc = check_rows("v", d_v, ldv, wk)) return rc;
   if (int rc = check_rows("q_out", d_q_out, ldqo, wq)) return rc;
   if (d_q_out == d_q && ldqo != ldq) return fail(SLORA_ERR_INVALID, "q_out in place needs q's row stride");
+  if (d_q_out != d_q && overlap(d_q, ldq, d_q_out, ldqo, wq, kv->T))
+    return fail(SLORA_ERR_INVALID, "q_out overlaps q");
   if (!d_q_weight != !d_k_weight) return fail(SLORA_ERR_INVALID, "norm weights of queries and keys go together");
   if ((reinterpret_cast<uintptr_t>(d_q_weight) | reinterpret_cast<uintptr_t>(d_k_weight)) & 15)
     return fail(SLORA_ERR_INVALID, "norm weights must be 16-byte aligned");
@@ -355,6 +373,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   const int64_t wq = (int64_t)kv->dev.heads_q * kv->dev.head_dim;
   if (int rc = check_rows("q", d_q, ldq, wq)) return rc;
   if (int rc = check_rows("out", d_out, ldo, wq)) return rc;
+  if (overlap(d_q, ldq, d_out, ldo, wq, kv->T)) return fail(SLORA_ERR_INVALID, "out overlaps q");
   KvAttendArgs a{};
   a.kv = kv->dev;
   a.R = kv->R;

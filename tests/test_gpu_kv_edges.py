@@ -240,3 +240,35 @@ def test_chunks_of_many_tiles(S, dtype, hq, ctx, new):
     _, q, out = _fill_and_attend(S, s)
     _check_attend(s, q, out)
     s.close()
+
+
+def test_overlapping_results_are_refused(S):
+    """out over q (attend), q_out over q but for in place (append); slices of one product
+    side by side are no overlap."""
+    s = Setup(S, [4, 8, 9], [1, 1, 1], 2, 1, 64, 4, "f16")
+    b, q, out = _fill_and_attend(S, s)
+    w = 128
+    two = torch.zeros(8, 2 * w, dtype=torch.float16, device="cuda")
+    flat = torch.zeros(8 * w, dtype=torch.float16, device="cuda")
+    k, v = s.randn(3, 64), s.randn(3, 64)
+    rows = lambda at: flat[at: at + 3 * w].view(3, w)
+    bad = [(two[:3, :w], two[:3, :w]), (two[:3, :w], two[:3, 64: 64 + w]), (two[:3, 64: 64 + w], two[:3, :w]),
+           (rows(0), rows(2 * w)), (rows(3 * w - 8), rows(0)), (two[:3, w:], two[1:4, 64: 64 + w])]
+    for a, o in bad:
+        with pytest.raises(S.SloraError) as e:
+            s.kv.attend(b, 0, a, o)
+        assert e.value.code == S.ERR_INVALID
+        if a.data_ptr() != o.data_ptr():
+            with pytest.raises(S.SloraError) as e:
+                s.kv.append(b, 0, a, k, v, q_out=o)
+            assert e.value.code == S.ERR_INVALID
+    good = [(two[:3, :w], two[:3, w:]), (two[:3, w:], two[:3, :w]), (two[1:4, w:], two[:3, :w]),
+            (rows(0), rows(3 * w)), (rows(3 * w), rows(0)), (two[:3, :w], two[3:6, 64: 64 + w])]
+    for a, o in good:
+        a.copy_(q)
+        s.kv.attend(b, 0, a, o)
+        assert torch.equal(o, out[:3, :w])
+    for a, o in good + [(q, None)]:
+        s.kv.append(b, 0, a, k, v, q_out=o)
+    assert s.pool.status() == S.OK
+    s.close()
