@@ -370,6 +370,12 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   if (!std::isfinite(scale) || scale <= 0.f) return fail(SLORA_ERR_INVALID, "scale must be finite and > 0");
   if (!std::isfinite(softcap) || softcap < 0.f) return fail(SLORA_ERR_INVALID, "softcap must be finite and >= 0");
   if (kv->T == 0 || kv->R == 0 || kv->max_new == 0) return SLORA_OK;   // no request can have a row
+  const int32_t group = kv->dev.heads_q / kv->dev.heads_kv;
+  const int64_t rows = (int64_t)std::min(kv->max_new, kv->T) * group;     // of one key head in one request
+  // chunks are possible where one request may bring more than kKvChunkRows rows
+  const bool chunks = kv->tpt > 0 && rows > kKvChunkRows;
+  if (!chunks && rows * kv->dev.heads_kv > INT32_MAX)
+    return fail(SLORA_ERR_INVALID, "max_new * heads_q = %lld is 2^31 or more", (long long)rows * kv->dev.heads_kv);
   const int64_t wq = (int64_t)kv->dev.heads_q * kv->dev.head_dim;
   if (int rc = check_rows("q", d_q, ldq, wq)) return rc;
   if (int rc = check_rows("out", d_out, ldo, wq)) return rc;
@@ -397,10 +403,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.tpt = kv->tpt;
   a.tc_part_o = kv->d_tc_part_o;
   a.tc_part_ml = kv->d_tc_part_ml;
-  const int32_t group = kv->dev.heads_q / kv->dev.heads_kv;
-  // chunks are possible where one request may bring more than kKvChunkRows rows
-  const bool chunks = kv->tpt > 0 && (int64_t)std::min(kv->max_new, kv->T) * group > kKvChunkRows;
-  a.rows = chunks ? kKvChunkRows : (int32_t)((int64_t)std::min(kv->max_new, kv->T) * group);
+  a.rows = chunks ? kKvChunkRows : (int32_t)rows;
   if (chunks) {
     const uint64_t dims[3] = {(uint64_t)kv->dev.head_dim, (uint64_t)kv->dev.heads_q, (uint64_t)kv->T};
     const uint64_t strides[2] = {2 * (uint64_t)kv->dev.head_dim, 2 * (uint64_t)ldq};

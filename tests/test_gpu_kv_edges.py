@@ -272,3 +272,18 @@ def test_overlapping_results_are_refused(S):
         s.kv.append(b, 0, a, k, v, q_out=o)
     assert s.pool.status() == S.OK
     s.close()
+
+
+def test_more_rows_than_31_bits_count_are_refused(S):
+    """32,768 tokens of 65,536 query heads (refused before any pointer is used)."""
+    T, heads = 1 << 15, 1 << 16
+    pool = S.Pool(40, 64, "f16", [(8, 8)], 1, 1, T, device=torch.device("cuda", 0))
+    kv = S.KVCache(pool, 1, heads, 1, 16, 2, T // 4)
+    z = torch.zeros(2, dtype=torch.int32, device="cuda")
+    b = kv.plan(z, z, None, T, T)
+    with pytest.raises(S.SloraError) as e:
+        S.slora_kv_attend(kv.handle, b.raw, 0, pool.buffer.data_ptr(), heads * 16, z.data_ptr(), heads * 16, 1.0)
+    assert e.value.code == S.ERR_INVALID and "2^31" in str(e.value)
+    assert pool.status() == S.OK
+    kv.close()
+    pool.close()
