@@ -549,8 +549,10 @@ class KVCache:
         cfg = (layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
         n = slora_kv_array_ints(pool.handle, *cfg)     # also refuses what the cache cannot be
         i32 = dict(dtype=torch.int32, device=pool.buffer.device)
-        self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
-        self.arrays = torch.empty(n, **i32)
+        # of the stream that writes them: memory that another one still uses is not theirs
+        with torch.cuda.stream(pool.compute_stream):
+            self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
+            self.arrays = torch.empty(n, **i32)
         self.handle = slora_kv_create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
         self._lib, self._int32, self._views = lib(), torch.int32, {}
         self._wq, self._wk = heads_q * head_dim, heads_kv * head_dim

@@ -287,3 +287,24 @@ def test_more_rows_than_31_bits_count_are_refused(S):
     assert pool.status() == S.OK
     kv.close()
     pool.close()
+
+
+def test_cache_memory_belongs_to_the_compute_stream(S, monkeypatch):
+    """The table and the batch arrays are cleared on the pool's compute stream, so that
+    is the stream they are allocated for, whichever is current."""
+    stream = torch.cuda.Stream()
+    pool = S.Pool(8, 256, "f16", [(8, 8)], 1, 1, 4, device=torch.device("cuda", 0), compute_stream=stream)
+    seen, real = [], torch.empty
+
+    def empty(*a, **kw):
+        seen.append(torch.cuda.current_stream())
+        return real(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    kv = S.KVCache(pool, 1, 2, 1, 64, 2, 3)
+    assert len(seen) == 2 and all(x == stream for x in seen)
+    assert torch.cuda.current_stream() != stream
+    stream.synchronize()
+    assert (kv.table == -1).all() and not kv.arrays.any()
+    kv.close()
+    pool.close()
