@@ -518,14 +518,35 @@ class Pool:
 
 
 class KVBatch:
-    """A planned step: the arrays of slora_kv_batch as views of the cache's
-    ``arrays`` tensor (the cache's next plan overwrites them)."""
+    """A planned step.  The arrays of slora_kv_batch are views of the cache's
+    ``arrays`` tensor, made when they are asked for (the cache's next plan
+    overwrites them)."""
 
-    __slots__ = ("raw", "ref", "q_start", "kv_len", "tok_req", "tok_pos", "slots")
+    __slots__ = ("raw", "ref", "R", "T", "_arrays", "_layout")
 
-    def __init__(self, raw: slora_kv_batch, views):
-        self.raw, self.ref = raw, ctypes.byref(raw)
-        self.q_start, self.kv_len, self.tok_req, self.tok_pos, self.slots = views
+    def __init__(self, raw: slora_kv_batch, R: int, T: int, arrays, layout):
+        self.raw, self.ref, self.R, self.T, self._arrays, self._layout = raw, ctypes.byref(raw), R, T, arrays, layout
+
+    @property
+    def q_start(self):
+        return self._arrays.as_strided((self.R + 1,), (1,), self._layout[0])
+
+    @property
+    def kv_len(self):
+        return self._arrays.as_strided((self.R,), (1,), self._layout[1])
+
+    @property
+    def tok_req(self):
+        return self._arrays.as_strided((self.T,), (1,), self._layout[2])
+
+    @property
+    def tok_pos(self):
+        return self._arrays.as_strided((self.T,), (1,), self._layout[3])
+
+    @property
+    def slots(self):
+        _, _, _, _, at, layers, n = self._layout
+        return self._arrays.as_strided((layers, 2, self.T), (2 * n, n, 1), at)
 
 
 class KVCache:
@@ -554,7 +575,7 @@ class KVCache:
             self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
             self.arrays = torch.empty(n, **i32)
         self.handle = slora_kv_create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
-        self._lib, self._int32, self._views = lib(), torch.int32, {}
+        self._lib, self._int32, self._layout = lib(), torch.int32, None
         self._wq, self._wk = heads_q * head_dim, heads_kv * head_dim
 
     def close(self):
@@ -595,17 +616,6 @@ class KVCache:
             raise ValueError(f"{name} must be a contiguous CUDA {self.pool.dtype} tensor of {self.head_dim}")
         return t.data_ptr()
 
-    def _batch_views(self, raw):
-        layers, R, T, n = self.table.shape[0], raw.R, raw.T, raw.slot_stride
-        base = self.arrays.data_ptr()
-
-        def view(ptr, length):
-            at = (ptr - base) // 4
-            return self.arrays[at:at + length]
-
-        return (view(raw.q_start, R + 1), view(raw.kv_len, R), view(raw.tok_req, T), view(raw.tok_pos, T),
-                view(raw.slots, 2 * layers * n).view(layers, 2, n)[:, :, :T])
-
     def plan(self, ctx, new, pages, T: int, max_new: int, rows=None) -> KVBatch:
         """ctx, new, rows: int32 per request; pages: the opened blocks' pages in
         order (int32, [block][layer][K, V]); T: tokens the batch has room for."""
@@ -617,13 +627,11 @@ class KVCache:
                                        self._i32("new", new), self._i32("pages", pages),
                                        pages.numel() if pages is not None else 0, T, max_new, ctypes.byref(raw)),
                "slora_kv_plan")
-        # the arrays stay where they are: the views of a batch of these sizes serve the next one too
-        views = self._views.get((R, T))
-        if views is None:
-            if len(self._views) >= 256:
-                self._views.clear()
-            views = self._views[(R, T)] = self._batch_views(raw)
-        return KVBatch(raw, views)
+        if self._layout is None:       # where the arrays lie, the same in every batch
+            base = self.arrays.data_ptr()
+            self._layout = (*((p - base) // 4 for p in (raw.q_start, raw.kv_len, raw.tok_req, raw.tok_pos, raw.slots)),
+                            self.table.shape[0], raw.slot_stride)
+        return KVBatch(raw, R, T, self.arrays, self._layout)
 
     def append(self, batch: KVBatch, layer: int, q, k, v, q_out=None, q_weight=None, k_weight=None,
                eps: float = 1e-6) -> None:

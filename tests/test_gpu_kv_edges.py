@@ -308,3 +308,20 @@ def test_cache_memory_belongs_to_the_compute_stream(S, monkeypatch):
     assert (kv.table == -1).all() and not kv.arrays.any()
     kv.close()
     pool.close()
+
+
+def test_batches_of_many_sizes_leave_nothing_behind(S):
+    """A server's (R, T) changes every step: the cache keeps no views of batches, and a
+    batch's are right when they are asked for."""
+    s = Setup(S, [3, 0, 9], [1, 5, 2], 2, 1, 16, 4, "f16", layers=3, T=40)
+    size = lambda: sum(len(x) for x in vars(s.kv).values() if isinstance(x, (dict, list)))
+    before = size()
+    for T in range(8, 41):
+        b = s.plan(T=T)
+        s.T = T
+        want = s.oracle_plan()
+    assert size() == before
+    for k, w in want.items():
+        assert np.array_equal(getattr(b, k).cpu().numpy(), w), k
+    assert s.pool.status() == S.OK
+    s.close()
