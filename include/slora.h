@@ -366,7 +366,10 @@ int slora_debug_set_fault(slora_pool* pool, int32_t kind, int64_t nth);
  * slora_device_status as SLORA_ERR_DEVICE_ASSERT (the index is replaced by
  * 0, so no access leaves its buffer and no kernel waits for a copy that
  * never comes); results of that call are then meaningless.  Other builds
- * compile no checks.
+ * compile no checks.  slora_kv_append checks the slots, slora_kv_attend the
+ * table rows and token indices that they read from a planned batch's arrays;
+ * pages of the block table are checked in every build (slora_kv_plan and
+ * slora_kv_attend).
  *
  * slora_debug_poke_page_table writes `value` into entry `entry` of the
  * pool's device page table (entries of adapter a start at a * stride) and

@@ -145,7 +145,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     f.len = rq.z;
     f.n = (rq.z + kKvUnit - 1) / kKvUnit;
     f.tiles = (rq.y * group + kKvRowTile - 1) / kKvRowTile;
-    f.tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)rq.w * d.max_blocks;
+    f.tab = d.table + (2 * a.layer + (lane >> 4)) * plane + (int64_t)dbg_index(rq.w, d.max_rows, d.error) * d.max_blocks;
   };
   // requests without units here: no new tokens, or a chunk
   auto no_units = [&](const int4& rq) {
@@ -235,7 +235,7 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     {
       const int row = rt * kKvRowTile + nn;
       const bool in = row < rows;
-      const uint16_t* src = a.q + (int64_t)(q0 + (in ? row / group : 0)) * a.ldq +
+      const uint16_t* src = a.q + (int64_t)dbg_index(q0 + (in ? row / group : 0), a.T, d.error) * a.ldq +
                             (int64_t)(hk * group + (in ? row % group : 0)) * dim;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -341,7 +341,8 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       const float l = x ? l1 : l0;
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* dst = a.out + (int64_t)(q0 + row / group) * a.ldo + (int64_t)(hk * group + row % group) * dim + nn * 8;
+        uint16_t* dst = a.out + (int64_t)dbg_index(q0 + row / group, a.T, d.error) * a.ldo +
+                        (int64_t)(hk * group + row % group) * dim + nn * 8;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float y[8];
@@ -481,7 +482,8 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) s.add(ml[k], y[k]);
     }
-    uint16_t* dst = a.out + (int64_t)(rq.x + row / group) * a.ldo + (int64_t)(hk * group + row % group) * dim;
+    uint16_t* dst = a.out + (int64_t)dbg_index(rq.x + row / group, a.T, d.error) * a.ldo +
+                    (int64_t)(hk * group + row % group) * dim;
     if constexpr (!WIDE) {
       store_row<E, V>(dst, lane, dim, s.o, s.l);
     } else {                                              // the warps' sums, in their order
@@ -547,7 +549,8 @@ __global__ void __launch_bounds__(kChunkJoinThreads) kv_chunk_join_kernel(const 
 #pragma unroll
       for (int k = 0; k < 4; ++k) s.add(ml[k], y[k]);
     }
-    store_row<E, 4>(a.out + (int64_t)(sg.x + x * a.tpt + tok) * a.ldo + (int64_t)(sg.z * group + rho - tok * group) * dim,
+    store_row<E, 4>(a.out + (int64_t)dbg_index(sg.x + x * a.tpt + tok, a.T, d.error) * a.ldo +
+                        (int64_t)(sg.z * group + rho - tok * group) * dim,
                     lane, dim, s.o, s.l);
   }
 }

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) part_read();
       if (p.i1 == 0) break;
-      const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)p.row * d.max_blocks;
+      const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)dbg_index(p.row, d.max_rows, d.error) * d.max_blocks;
       const uint8_t* base = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)p.hk * dim * 2 + ch * 16;
       int kslot, vslot;            // pool rows, -1: none
       uint32_t holes;
@@ -672,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         // global memory sees whole rows.
         uint8_t* stage = sm.q[qb][0] + 32 * quarter * 256;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)(p.tok + x * tpt + my_tok) * a.ldo +
+        const int tok = p.tok + x * tpt + my_tok;
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + (int64_t)(live ? dbg_index(tok, a.T, d.error) : tok) * a.ldo +
                                                           (int64_t)(p.hk * group + my_head) * dim)
                              : reinterpret_cast<uint8_t*>(a.tc_part_o + part * kKvTile);
         const uint32_t rows_live = __ballot_sync(0xffffffffu, live);

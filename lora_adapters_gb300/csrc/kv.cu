@@ -372,7 +372,10 @@ __global__ void __launch_bounds__(kAppendThreads, NORM && !INTER ? 3 : 4) kv_app
   if (t >= a.T) return;
   const int pos = d.tok_pos[t];
   const int32_t* slots = d.slots + (int64_t)2 * a.layer * d.max_tokens + t;
-  const int ks = slots[0], vs = slots[d.max_tokens];
+  const int64_t pool_rows = (int64_t)d.num_pages * d.per_page;
+  int ks = slots[0], vs = slots[d.max_tokens];
+  if (ks >= 0) ks = dbg_index(ks, pool_rows, d.error);
+  if (vs >= 0) vs = dbg_index(vs, pool_rows, d.error);
   if (pos < 0) return;                           // a token without a request
   Lane ln;
   ln.lane = tid & 31;

@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "internal.h"
+
 namespace slora {
 
 template <class T>

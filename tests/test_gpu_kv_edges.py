@@ -2,6 +2,9 @@
 fp64 oracle; tolerances are those of tests/test_gpu_kv.py where none is derived
 beside the test."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -325,3 +328,15 @@ def test_batches_of_many_sizes_leave_nothing_behind(S):
         assert np.array_equal(getattr(b, k).cpu().numpy(), w), k
     assert s.pool.status() == S.OK
     s.close()
+
+
+def test_debug_build_catches_planted_indices():
+    """The SLORA_DEBUG build, in a process of its own: tests/debug_kv_check.py."""
+    from lora_adapters_gb300 import build
+
+    build.build(debug=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-m", "tests.debug_kv_check"], cwd=root, env=dict(os.environ, SLORA_DEBUG="1"),
+                         capture_output=True, text=True, timeout=600)
+    assert res.returncode == 0, res.stdout[-2000:] + res.stderr[-4000:]
+    assert "debug build OK" in res.stdout
