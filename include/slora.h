@@ -536,8 +536,11 @@ int slora_kv_destroy(slora_kv* kv);
  * SLORA_ROTARY_INTERLEAVED: elements 2i and 2i + 1.  h_inv_freq: host, copied
  * before the call returns.  Every scaling of the frequencies for long
  * contexts is a choice of h_inv_freq and mscale.  The turn is reduced as a
- * 64-bit fixed-point fraction of a circle (t times the frequency modulo
- * 2^64), so it is exact to 2^-32 turn at every position below 2^31.
+ * 64-bit fixed-point fraction of a circle (t times the frequency modulo 2^64),
+ * so that what is left of it is the frequency's own error: at most
+ * t * h_inv_freq[i] * 2^-55 turn (2^-25 for frequency 1 at position 2^30).  The
+ * rest is fp32: the angle within half a turn to 2^-25 turn, its cosine and sine
+ * to about 2^-21.
  * Errors: SLORA_ERR_INVALID (sizes, layout, a frequency or mscale that is not
  * finite).  Blocks the host until the compute stream has taken the table;
  * not to be called while the stream is being captured.

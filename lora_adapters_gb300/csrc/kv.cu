@@ -387,9 +387,10 @@ __global__ void __launch_bounds__(kAppendThreads, NORM && !INTER ? 3 : 4) kv_app
   ln.partner = (ln.lane & ~(G - 1)) | (ln.turned ? pl : ln.li);
   ln.inv_d = 1.f / (float)D;
   ln.eps = a.eps;
-  // Cosine and sine of this lane's pairs: the angle as the exact fraction of a
-  // turn, modulo one, a signed 64-bit number; within half a turn the
-  // approximate functions are good to 2^-21, 1/1024 of the storage type's unit.
+  // Cosine and sine of this lane's pairs: the angle as a fraction of a turn modulo
+  // one, a signed 64-bit number that wraps around without error, then in fp32
+  // (2^-25 turn); within half a turn the approximate functions are good to 2^-21,
+  // 1/1024 of fp16's unit and 2^-13 of bf16's.
 #pragma unroll
   for (int j = 0; j < (INTER ? 4 : 8); ++j) {
     const int pi = INTER ? ln.li * 4 + j : (ln.li < half ? ln.li : pl) * 8 + j;

@@ -38,7 +38,8 @@ inline int32_t kv_chunk_tokens(int32_t group, int32_t head_dim) {
   return head_dim < 64 || head_dim > 128 || group > kKvChunkGroup ? 0 : kKvTile / group;
 }
 
-// Quotients of 31-bit numbers by a fixed divisor: mul = ceil(2^(32 + shift) / d)
+// Quotients of 31-bit numbers by a fixed divisor (Granlund and Montgomery, "Division
+// by Invariant Integers using Multiplication", PLDI 1994): mul = ceil(2^(32 + shift) / d)
 // with 2^shift >= d, so that n * mul / 2^(32 + shift) is below 1/d too large
 // for every n < 2^32, and the floor is right; mul takes 33 bits, its top bit
 // is the extra addition of n.
