@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kDecWarps = 4;             // per CTA
 constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kDecCtas = 3;              // per SM: 170 registers a thread
+constexpr int kDecCtas = 3;              // per SM: 170 registers a thread (D = 128 spills 56 to 60 bytes;
+                                         // D = 256, two a SM and 255 registers, 320 to 380)
 constexpr int kDecMinUnits = 1;          // shortest run (one 640-token request: 12.5 us with 1, 13.0 with 2, 15.6 with 4)
 
 // Streaming 16-byte load: every byte of the cache is used once per call, and the

@@ -278,7 +278,7 @@ struct TcSmem {
 // STEPS: 16-element steps of a head, 8 or 4; 0: head_dim 80, 96 or 112 (a
 // branch to the right run of MMAs costs 7 % of the kernel).
 // CAP: scores as they are, capped with softcap <= kCapNear, or with any softcap (a
-// 1024-token chunk over 16 K tokens, 40 query heads on 8: 260, 482 and 734 us).
+// 1024-token chunk over 16 K tokens, 40 query heads on 8: 263, 486 and 747 us).
 enum { kCapNone = 0, kCapSmall, kCapAny };
 template <class E, int CAP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ KvAttendArgs a) {

@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
 // own, and nothing waits at a barrier.  kAppendAhead loads a lane are on their
 // way before the first is worked on.  Measured: 8256 tokens of 56 heads, normed,
 // half of each head turned, 46.6 us (5.0 TB/s); the half layout over whole heads
-// 56 us (its exchange takes eight shuffles a lane); 256 tokens of 96 heads
-// 6.9 us, at the cost of the call.
+// 56 us (its exchange takes eight shuffles a lane), not normed 45.6 us (four
+// shuffles; 64 bytes of spills at 64 registers); 256 tokens of 96 heads 6.9 us, at
+// the cost of the call.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendAhead = 4;
 

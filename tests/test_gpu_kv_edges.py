@@ -225,6 +225,8 @@ def test_plan_is_quick_at_lengths_that_are_no_batch(S):
     dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
     args = dev([0, 5, 77]), dev([1 << 30, (1 << 30) - 5, 1 << 29]), dev([0, 1])
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    kv.plan(dev([0]), dev([1]), dev([0, 1]), 8, 1)
+    assert pool.status() == S.OK
     start.record()
     b = kv.plan(*args, 8, 1 << 30)
     end.record()
