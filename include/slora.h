@@ -611,6 +611,53 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
 int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, const void* d_q, int64_t ldq,
                     void* d_out, int64_t ldo, float scale, float softcap);
 
+/*
+ * Stored keys and values of single tokens as rows of the pool's 16-bit type: for
+ * each i < n the token at position d_pos[i] of table row d_row[i] (device int32[n];
+ * the same token may be named more than once), its heads_kv * head_dim elements to
+ * row i of d_k and of d_v (row strides ldk, ldv; either may be NULL, not both).  A
+ * cache of 16 bits gives the stored bits, one held in 4 the numbers its codes stand
+ * for.  A negative position: row i is left as it is.  A row or position outside the
+ * table, or an entry that names no page of the pool, raises the device status
+ * SLORA_ERR_INVALID and leaves the row as it is.  What a slot holds that no append
+ * wrote is not defined.  Pointers 16-byte aligned, strides multiples of 8; d_k and d_v
+ * must not overlap.  Needs no planned batch.
+ */
+int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, const int32_t* d_pos, void* d_k,
+                  int64_t ldk, void* d_v, int64_t ldv);
+
+/*
+ * ---- A cache held in 4 bits ----------------------------------------------
+ * slora_kv_q4_create makes a cache whose keys and values are quantised as
+ * slora_kv_append writes them; every slora_kv_* call takes its handle.  32
+ * elements of a head are a group (the last one of a head_dim that is no multiple of
+ * 32 has 16).  With m the group's element of largest magnitude (the positive one if
+ * both signs reach it) and M = |m| rounded up to five significant bits, with m's
+ * sign, element x is kept as
+ *     k = clamp(floor(8 x / M + 1/2), -7, 8)     and stands for     M k / 8,
+ * which both 16-bit types hold exactly: slora_kv_read returns, and slora_kv_attend
+ * computes with, these numbers.  An element is off by at most |M| / 16, one whose
+ * sign is not m's by at most |M| / 8.  Keys are quantised from their fp32 value after
+ * norm and rotary turn, with no rounding in between, and codes are those of the
+ * formula in exact arithmetic (where fp32 cannot tell, it is evaluated in 64 bits).
+ * M is kept in the storage type: fp16's is a multiple of 2^-21 and at most 31 * 2^11,
+ * bf16's a multiple of 2^-100 and at most 31 * 2^123; larger elements are held as the
+ * largest M.  A group with an element that is not finite stands for NaN throughout.
+ *
+ * A token's row in a page takes 18 * ceil(head_dim / 32) * heads_kv bytes, rounded up
+ * to 16: for every head the codes k + 7, 16 bytes a group, then M as [head][group].
+ * With ng groups, the code of element 32 g + r of a head lies
+ *     in K at bits 16 (r % 2) + 4 (r % 8 / 2) of the head's 32-bit word (r / 8) ng + g,
+ *     in V at bits 4 (r % 4) of its 16-bit word (r / 4) ng + g.
+ * A page holds as many rows as fit, P = 2 * page_elems / row bytes, the first at its
+ * start; position t of a table row is row t % P of page table[layer][kv][i][t / P]
+ * (slots of a batch: page * P + t % P).  page_elems need not be a multiple of anything
+ * but must hold a row.
+ */
+int slora_kv_q4_array_ints(const slora_pool* pool, const slora_kv_config* config, int64_t* n);
+int slora_kv_q4_create(slora_kv** out, slora_pool* pool, const slora_kv_config* config, int32_t* d_table,
+                       int32_t* d_arrays);
+
 #ifdef __cplusplus
 }
 #endif

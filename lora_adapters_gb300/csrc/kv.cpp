@@ -1,8 +1,8 @@
 // Host side of the paged key-value cache: argument checks and launches of
-// slora_kv_plan, slora_kv_append and slora_kv_attend (include/slora.h).  The
-// pages describe the KV half of the unified pool only as an allocation
-// (dongaigc.com summary, section 1; fatihsoysal.com page, section "vLLM'in
-// PagedAttention Mekanizmasi"); the operators on it are this library's own.
+// slora_kv_plan, slora_kv_append, slora_kv_attend and slora_kv_read
+// (include/slora.h).  The pages describe the KV half of the unified pool only as
+// an allocation (dongaigc.com summary, section 1; fatihsoysal.com page, section
+// "vLLM'in PagedAttention Mekanizmasi"); the operators on it are this library's own.
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -81,7 +81,8 @@ void free_kv(slora_kv* kv) {
 }
 
 // A cache's sizes over a pool: checked, and its KvDev without the arrays.
-int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv, KvDev* dev) {
+// q4: a cache held in 4 bits.
+int check_config(const slora_pool* pool, const slora_kv_config* c, bool q4, PoolView* pv, KvDev* dev) {
   if (!pool) return fail(SLORA_ERR_INVALID, "pool is NULL");
   if (!c) return fail(SLORA_ERR_INVALID, "config is NULL");
   *pv = pool_view(pool);
@@ -96,10 +97,13 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv,
     return fail(SLORA_ERR_INVALID, "max_requests=%d not in [1, %d]", c->max_requests, SLORA_KV_MAX_REQUESTS);
   if (c->max_blocks < 1) return fail(SLORA_ERR_INVALID, "max_blocks=%d", c->max_blocks);
   const int64_t width = (int64_t)c->heads_kv * c->head_dim;
-  if (pv->H % width)
+  const int64_t groups = (c->head_dim + 31) / 32, row_bytes = (18 * groups * c->heads_kv + 15) / 16 * 16;
+  if (q4 && 2 * (int64_t)pv->H < row_bytes)
+    return fail(SLORA_ERR_INVALID, "a page of %d elements does not hold a token's %lld bytes", pv->H, (long long)row_bytes);
+  if (!q4 && pv->H % width)
     return fail(SLORA_ERR_INVALID, "page_elems=%d must be a multiple of heads_kv * head_dim = %lld", pv->H,
                 (long long)width);
-  const int64_t P = pv->H / width;
+  const int64_t P = q4 ? 2 * (int64_t)pv->H / row_bytes : pv->H / width;
   if (pv->num_pages * P >= INT32_MAX || c->max_blocks * P > (1 << 30))
     return fail(SLORA_ERR_INVALID, "more than 2^31 - 2 tokens in the pool, or 2^30 in a table row");
   if ((int64_t)c->heads_q * c->head_dim >= INT32_MAX) return fail(SLORA_ERR_INVALID, "heads_q * head_dim too large");
@@ -116,6 +120,11 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, PoolView* pv,
   d.max_blocks = c->max_blocks;
   d.max_tokens = std::max(pv->max_tokens, 1);
   d.error = pv->d_error;
+  if (q4) {
+    d.groups = (int32_t)groups;
+    d.row_bytes = (int32_t)row_bytes;
+    d.page_bytes = 2 * (int64_t)pv->H;
+  }
   return SLORA_OK;
 }
 
@@ -168,28 +177,21 @@ bool overlap(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t col
   return (off < cols && std::abs(rows) < T) || (ldp - off < cols && std::abs(rows + 1) < T);
 }
 
-}  // namespace
-
-extern "C" {
-
-int slora_kv_array_ints(const slora_pool* pool, const slora_kv_config* c, int64_t* n) {
-  SLORA_RANGE("slora_kv_array_ints");
+int array_ints(const slora_pool* pool, const slora_kv_config* c, bool q4, int64_t* n) {
   if (!n) return fail(SLORA_ERR_INVALID, "n is NULL");
   PoolView pv;
   KvDev d;
-  if (int rc = check_config(pool, c, &pv, &d)) return rc;
+  if (int rc = check_config(pool, c, q4, &pv, &d)) return rc;
   *n = place_arrays(d, nullptr);
   return SLORA_OK;
 }
 
-int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, int32_t* d_table,
-                    int32_t* d_arrays) {
-  SLORA_RANGE("slora_kv_create");
+int create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, bool q4, int32_t* d_table, int32_t* d_arrays) {
   if (!out) return fail(SLORA_ERR_INVALID, "out is NULL");
   *out = nullptr;
   PoolView pv;
   KvDev d;
-  if (int rc = check_config(pool, c, &pv, &d)) return rc;
+  if (int rc = check_config(pool, c, q4, &pv, &d)) return rc;
   if (!d_table || !d_arrays || reinterpret_cast<uintptr_t>(d_table) & 3 || reinterpret_cast<uintptr_t>(d_arrays) & 15)
     return fail(SLORA_ERR_INVALID, "d_table and d_arrays must be device pointers to int32, d_arrays 16-byte aligned");
 
@@ -208,7 +210,7 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
     const int64_t parts = kv_attend_parts(pv.num_sms);
     CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));
     CUDA_TRY(cudaMalloc(&kv->d_part_ml, sizeof(float2) * (size_t)parts));
-    kv->tpt = kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
+    kv->tpt = q4 ? 0 : kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
     if (kv->tpt > 0) {
       CUDA_TRY(prepare_kv_chunk_kernels());
       const int64_t rows = kv_chunk_part_rows(pv.num_sms);
@@ -231,6 +233,32 @@ int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, 
   }
   *out = kv;
   return SLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int slora_kv_array_ints(const slora_pool* pool, const slora_kv_config* c, int64_t* n) {
+  SLORA_RANGE("slora_kv_array_ints");
+  return array_ints(pool, c, false, n);
+}
+
+int slora_kv_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, int32_t* d_table,
+                    int32_t* d_arrays) {
+  SLORA_RANGE("slora_kv_create");
+  return create(out, pool, c, false, d_table, d_arrays);
+}
+
+int slora_kv_q4_array_ints(const slora_pool* pool, const slora_kv_config* c, int64_t* n) {
+  SLORA_RANGE("slora_kv_q4_array_ints");
+  return array_ints(pool, c, true, n);
+}
+
+int slora_kv_q4_create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, int32_t* d_table,
+                       int32_t* d_arrays) {
+  SLORA_RANGE("slora_kv_q4_create");
+  return create(out, pool, c, true, d_table, d_arrays);
 }
 
 int slora_kv_destroy(slora_kv* kv) {
@@ -357,8 +385,10 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.rot_dim = kv->rot_dim;
   a.interleaved = kv->interleaved;
   a.mscale = kv->mscale;
+  a.per_page_div = kv->per_page_div;
   KvTimed tm(kv->pool, kKvTimerAppend);
-  CUDA_TRY(launch_kv_append(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  CUDA_TRY(d.groups ? launch_kv_q4_append(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute)
+                    : launch_kv_append(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
   tm.done();
   return SLORA_OK;
 }
@@ -412,7 +442,42 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   }
   KvTimed tm(kv->pool, kKvTimerAttend);
   if (chunks) CUDA_TRY(launch_kv_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
-  CUDA_TRY(launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute));
+  CUDA_TRY(kv->dev.groups ? launch_kv_q4_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute)
+                          : launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute));
+  tm.done();
+  return SLORA_OK;
+}
+
+int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, const int32_t* d_pos, void* d_k,
+                  int64_t ldk, void* d_v, int64_t ldv) {
+  SLORA_RANGE("slora_kv_read");
+  if (!kv) return fail(SLORA_ERR_INVALID, "kv is NULL");
+  const KvDev& d = kv->dev;
+  if (layer < 0 || layer >= d.layers) return fail(SLORA_ERR_INVALID, "layer %d not in [0, %d)", layer, d.layers);
+  if (n < 0) return fail(SLORA_ERR_INVALID, "n=%d", n);
+  if (n == 0) return SLORA_OK;
+  if (!d_row || !d_pos || (reinterpret_cast<uintptr_t>(d_row) | reinterpret_cast<uintptr_t>(d_pos)) & 3)
+    return fail(SLORA_ERR_INVALID, "d_row and d_pos must be device pointers to int32");
+  if (!d_k && !d_v) return fail(SLORA_ERR_INVALID, "neither keys nor values are wanted");
+  const int64_t width = (int64_t)d.heads_kv * d.head_dim;
+  if (d_k)
+    if (int rc = check_rows("k", d_k, ldk, width)) return rc;
+  if (d_v)
+    if (int rc = check_rows("v", d_v, ldv, width)) return rc;
+  if (d_k && d_v && overlap(d_k, ldk, d_v, ldv, width, n)) return fail(SLORA_ERR_INVALID, "v overlaps k");
+  KvReadArgs a{};
+  a.kv = d;
+  a.n = n;
+  a.layer = layer;
+  a.row = d_row;
+  a.pos = d_pos;
+  a.k = static_cast<uint16_t*>(d_k);
+  a.v = static_cast<uint16_t*>(d_v);
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.per_page_div = kv->per_page_div;
+  KvTimed tm(kv->pool, kKvTimerRead);
+  CUDA_TRY(launch_kv_read(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
   tm.done();
   return SLORA_OK;
 }

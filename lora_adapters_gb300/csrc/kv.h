@@ -1,5 +1,5 @@
-// Internal interface of the paged key-value cache: kv.cpp (host), kv.cu and
-// attend.cu (kernels), pool.cpp (the pool).  Not installed; the public ABI is
+// Internal interface of the paged key-value cache: kv.cpp (host), kv.cu, kv_q4.cu,
+// attend.cu, attend_tc.cu and attend_q4.cu (kernels), pool.cpp (the pool).  Not installed; the public ABI is
 // include/slora.h.
 #pragma once
 
@@ -56,9 +56,10 @@ struct FastDiv {
 #endif
 };
 
-// What the kernels of one cache share.  The pool's buffer is addressed as a
-// matrix of token rows of heads_kv * head_dim elements: position t of a
-// request is row page(t / P) * P + t % P.
+// What the kernels of one cache share.  The pool's buffer of a 16-bit cache is
+// addressed as a matrix of token rows of heads_kv * head_dim elements: position t
+// of a request is row page(t / P) * P + t % P.  In a 4-bit cache the token's row
+// begins row_bytes * (t % P) bytes into its page (kv_q4.cuh).
 struct KvDev {
   uint16_t* pool;
   int32_t* table;                // [layers][2][max_rows][max_blocks] page of each block, -1: none
@@ -76,6 +77,10 @@ struct KvDev {
   int32_t* tc_off;               // [R + 1] prefix sums of 128-key tiles, the chunk kernel's work per key head
   int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
   int32_t* error;                // the pool's device error word
+  // 4-bit caches
+  int32_t groups;                // of 32 elements a head has, 0: a 16-bit cache
+  int32_t row_bytes;             // of a token's row
+  int64_t page_bytes;
 };
 
 struct KvPlanArgs {
@@ -107,8 +112,20 @@ struct KvAppendArgs {
   int32_t interleaved;
   float mscale;
   int32_t parts;                 // warps per token (set by the launcher)
+  FastDiv per_page_div;          // 4-bit caches
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_q4_append(const KvAppendArgs& a, int dtype, int num_sms, cudaStream_t st);
+
+struct KvReadArgs {
+  KvDev kv;
+  int32_t n, layer;
+  const int32_t *row, *pos;      // [n] table row and position of each token, position < 0: none
+  uint16_t *k, *v;               // NULL: not wanted
+  int64_t ldk, ldv;
+  FastDiv per_page_div;
+};
+cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, int num_sms, cudaStream_t st);
 
 struct KvAttendArgs {
   KvDev kv;
@@ -141,6 +158,8 @@ int32_t kv_attend_cols(int32_t head_dim);
 // The decode kernel (after_chunks: while the chunk kernel launched before it
 // still runs), and the joins of what either kernel split.
 cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
+// The same over a 4-bit cache.
+cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).
 struct PoolView {
@@ -157,7 +176,7 @@ PoolView pool_view(const slora_pool* p);
 // slora_last_error_string().
 int encode_map(CUtensorMap* m, const void* base, int dtype, int rank, const uint64_t* dims, const uint64_t* strides,
                const uint32_t* box);
-enum KvTimer { kKvTimerPlan = 0, kKvTimerAppend, kKvTimerAttend };
+enum KvTimer { kKvTimerPlan = 0, kKvTimerAppend, kKvTimerAttend, kKvTimerRead };
 // Brackets a launch with the pool's timing events when timing is on.
 struct KvTimed {
   KvTimed(slora_pool* p, KvTimer which);

@@ -72,11 +72,11 @@ constexpr int32_t kOwnerKV = -2;
 constexpr int32_t kOwnerPending = -3;
 
 enum TimerKind { kTBuild = 0, kTApplyCC, kTShrinkTC, kTExpandTC, kTScatter, kTLoadWait,
-                 kTKvPlan, kTKvAppend, kTKvAttend, kTNum };
+                 kTKvPlan, kTKvAppend, kTKvAttend, kTKvRead, kTNum };
 // load_wait is not a kernel: the time the compute stream waited for adapter
 // copies before a segment build (recorded only when it had to wait)
 const char* kTimerNames[kTNum] = {"build_segments", "apply_cc", "shrink_tc", "expand_tc", "scatter", "load_wait",
-                                   "kv_plan", "kv_append", "kv_attend"};
+                                   "kv_plan", "kv_append", "kv_attend", "kv_read"};
 
 }  // namespace
 

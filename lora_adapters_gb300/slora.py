@@ -111,11 +111,14 @@ _SIGS = {
                                  ctypes.c_float, P, P],
     "slora_kv_array_ints": [P, ctypes.POINTER(slora_kv_config), P],
     "slora_kv_create": [ctypes.POINTER(P), P, ctypes.POINTER(slora_kv_config), P, P],
+    "slora_kv_q4_array_ints": [P, ctypes.POINTER(slora_kv_config), P],
+    "slora_kv_q4_create": [ctypes.POINTER(P), P, ctypes.POINTER(slora_kv_config), P, P],
     "slora_kv_destroy": [P],
     "slora_kv_set_rotary": [P, I32, I32, P, ctypes.c_float],
     "slora_kv_plan": [P, I32, P, P, P, P, I64, I32, I32, ctypes.POINTER(slora_kv_batch)],
     "slora_kv_append": [P, ctypes.POINTER(slora_kv_batch), I32, P, I64, P, I64, P, I64, P, P, ctypes.c_float, P, I64],
     "slora_kv_attend": [P, ctypes.POINTER(slora_kv_batch), I32, P, I64, P, I64, ctypes.c_float, ctypes.c_float],
+    "slora_kv_read": [P, I32, I32, P, P, P, I64, P, I64],
 }
 
 
@@ -359,6 +362,23 @@ def slora_kv_create(pool: int, layers: int, heads_q: int, heads_kv: int, head_di
     return out.value
 
 
+def slora_kv_q4_array_ints(pool: int, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
+                           max_blocks: int) -> int:
+    n = I64()
+    cfg = slora_kv_config(layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
+    _check(lib().slora_kv_q4_array_ints(pool or None, ctypes.byref(cfg), ctypes.byref(n)), "slora_kv_q4_array_ints")
+    return n.value
+
+
+def slora_kv_q4_create(pool: int, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
+                       max_blocks: int, d_table: int, d_arrays: int) -> int:
+    out = P()
+    cfg = slora_kv_config(layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
+    _check(lib().slora_kv_q4_create(ctypes.byref(out), pool or None, ctypes.byref(cfg), d_table or None,
+                                    d_arrays or None), "slora_kv_q4_create")
+    return out.value
+
+
 def slora_kv_destroy(kv: int) -> None:
     _check(lib().slora_kv_destroy(kv), "slora_kv_destroy")
 
@@ -390,6 +410,11 @@ def slora_kv_attend(kv: int, batch: slora_kv_batch, layer: int, d_q: int, ldq: i
                     scale: float, softcap: float = 0.0) -> None:
     _check(lib().slora_kv_attend(kv, ctypes.byref(batch), layer, d_q or None, ldq, d_out or None, ldo, scale, softcap),
            "slora_kv_attend")
+
+
+def slora_kv_read(kv: int, layer: int, n: int, d_row: int, d_pos: int, d_k: int, ldk: int, d_v: int, ldv: int) -> None:
+    _check(lib().slora_kv_read(kv, layer, n, d_row or None, d_pos or None, d_k or None, ldk, d_v or None, ldv),
+           "slora_kv_read")
 
 
 # ---- convenience wrapper for torch tensors -----------------------------------------
@@ -549,32 +574,47 @@ class KVBatch:
         return self._arrays.as_strided((layers, 2, self.T), (2 * n, n, 1), at)
 
 
+def tokens_per_page(page_elems: int, heads_kv: int, head_dim: int, bits: int = 16) -> int:
+    """Tokens whose K (or V) of one layer a page of a KV cache of 16 or 4 bits holds."""
+    if bits == 16:
+        return page_elems // max(1, heads_kv * head_dim)
+    row = -(-18 * -(-head_dim // 32) * heads_kv // 16) * 16      # bytes: 16 of codes and one M a head and group
+    return 2 * page_elems // max(1, row)
+
+
 class KVCache:
     """A paged key-value cache over a Pool (slora_kv_* of slora.h).
 
     ``table`` is the block table [layers, 2, max_requests, max_blocks] (int32).
+    ``bits``: 16, keys and values as they come, or 4, quantised as they are
+    written (slora_kv_q4_create); ``tokens_per_page`` follows from it.
     Calls run on the pool's compute stream: tensors made on another stream are
     the caller's to order, as with every call on the pool.
     """
 
     def __init__(self, pool: Pool, layers: int, heads_q: int, heads_kv: int, head_dim: int, max_requests: int,
-                 max_blocks: int):
+                 max_blocks: int, bits: int = 16):
         import torch
 
         self.handle = 0
+        if bits not in (4, 16):
+            raise ValueError(f"a KV cache holds 16 or 4 bits an element, not {bits}")
         if pool.buffer is None:
             raise ValueError("a KV cache needs a pool with a device buffer")
         self.pool = pool
         self.heads_q, self.heads_kv, self.head_dim = heads_q, heads_kv, head_dim
-        self.tokens_per_page = pool.H // max(1, heads_kv * head_dim)
+        self.bits = bits
+        self.tokens_per_page = tokens_per_page(pool.H, heads_kv, head_dim, bits)
         cfg = (layers, heads_q, heads_kv, head_dim, max_requests, max_blocks)
-        n = slora_kv_array_ints(pool.handle, *cfg)     # also refuses what the cache cannot be
+        array_ints, create = ((slora_kv_array_ints, slora_kv_create) if bits == 16 else
+                              (slora_kv_q4_array_ints, slora_kv_q4_create))
+        n = array_ints(pool.handle, *cfg)     # also refuses what the cache cannot be
         i32 = dict(dtype=torch.int32, device=pool.buffer.device)
         # of the stream that writes them: memory that another one still uses is not theirs
         with torch.cuda.stream(pool.compute_stream):
             self.table = torch.empty((layers, 2, max_requests, max_blocks), **i32)
             self.arrays = torch.empty(n, **i32)
-        self.handle = slora_kv_create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
+        self.handle = create(pool.handle, *cfg, self.table.data_ptr(), self.arrays.data_ptr())
         self._lib, self._int32, self._layout = lib(), torch.int32, None
         self._wq, self._wk = heads_q * head_dim, heads_kv * head_dim
 
@@ -654,3 +694,15 @@ class KVCache:
         po, ldo = self._rows("out", out, T, self._wq)
         _check(self._lib.slora_kv_attend(self.handle, batch.ref, layer, pq, ldq, po, ldo,
                                          self.head_dim ** -0.5 if scale is None else scale, softcap), "slora_kv_attend")
+
+    def read(self, layer: int, rows, pos, k=None, v=None) -> None:
+        """Stored tokens as 16-bit rows: token i is position pos[i] of table row
+        rows[i] (int32; pos[i] < 0: row i is left as it is), k and v
+        [n, heads_kv * head_dim] (either may be None)."""
+        n = rows.numel()
+        if pos.numel() != n:
+            raise ValueError("rows and pos must have one entry per token")
+        pk, ldk = (None, 0) if k is None else self._rows("k", k, n, self._wk)
+        pv, ldv = (None, 0) if v is None else self._rows("v", v, n, self._wk)
+        _check(self._lib.slora_kv_read(self.handle, layer, n, self._i32("rows", rows), self._i32("pos", pos), pk, ldk,
+                                       pv, ldv), "slora_kv_read")
