@@ -36,8 +36,7 @@
 
 #include <algorithm>
 
-#include "kv.cuh"
-#include "kv.h"
+#include "attend.cuh"
 
 namespace slora {
 namespace {
@@ -46,64 +45,6 @@ constexpr int kDecWarps = 4;             // per CTA
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecCtas = 3;              // per SM: 170 registers a thread (D = 128 spills 56 to 60 bytes;
                                          // D = 256, two a SM and 255 registers, 320 to 380)
-constexpr int kDecMinUnits = 1;          // shortest run (one 640-token request: 12.5 us with 1, 13.0 with 2, 15.6 with 4)
-
-// Streaming 16-byte load: every byte of the cache is used once per call, and the
-// rest of its 256 bytes by the same warp or its neighbours (1 % on 7B decode).
-__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-template <class E>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  if constexpr (Elem<E>::kBf16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Transpose of an 8x8 matrix of 16-bit elements held as one packed pair a lane.
-__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// The units of a call: segment = (request, row tile of kKvRowTile rows, block
-// of `hbw` key heads), ceil(len / 16) units each, laid out request by request.
-struct DecSplit {
-  int64_t total;     // units
-  int64_t run;       // units per group of warps
-};
-__device__ __forceinline__ DecSplit dec_split(int units, int blocks, int64_t groups) {
-  DecSplit s;
-  s.total = (int64_t)units * blocks;
-  s.run = max((int64_t)kDecMinUnits, (s.total + groups - 1) / groups);
-  return s;
-}
-// Largest r with off[r] * blocks <= x, by a whole warp: the lanes look at 32
-// places of what is left at a time.
-__device__ __forceinline__ int find_request(const int32_t* off, int R, int64_t x, int blocks) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = R;               // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) >> 5, i = lane * step;
-    const bool le = i < n && (int64_t)__ldg(off + lo + i) * blocks <= x;
-    const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);   // off[lo] <= x always
-    n = min(step, n - k * step);
-    lo += k * step;
-  }
-  return lo;
-}
 
 // D: head_dim rounded up to 64, 128 or 256; elements past head_dim are zeros.
 template <class E, int D, bool CAP>
@@ -459,7 +400,7 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
     const int off = __ldg(d.dec_off + r), off_next = __ldg(d.dec_off + r + 1);
     const int rows = rq.y * group;
     if (row >= rows || off == off_next) continue;         // no such row, or a chunk
-    const int nchunk = (rq.z + 15) >> 4, tiles = (rows + kKvRowTile - 1) / kKvRowTile, n = row % kKvRowTile;
+    const int nchunk = (rq.z + d.unit - 1) >> (31 - __clz(d.unit)), tiles = (rows + kKvRowTile - 1) / kKvRowTile, n = row % kKvRowTile;
     const int hb = hk / hbw, hsub = hk - hb * hbw;
     const int64_t us = (int64_t)off * blocks + (int64_t)(hb * tiles + row / kKvRowTile) * nchunk;
     const int64_t g0 = us / sp.run, g1 = (us + nchunk - 1) / sp.run;
@@ -556,19 +497,23 @@ __global__ void __launch_bounds__(kChunkJoinThreads) kv_chunk_join_kernel(const 
   }
 }
 
-// A launch that may begin before the one ahead of it in the stream has ended.
-template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+// `groups`: the groups of warps that the decode kernel shared the work out to.
+template <class E, int D>
+cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
+  if (after_chunks) {
+    const cudaError_t e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t items = (int64_t)a.R * a.rows * a.kv.heads_kv;
+  // segments of 16 parts or more on average: a block each (a 131072-token
+  // context, 228 parts a row: 24 us with a warp each, 8 with a block)
+  const int64_t segments = (int64_t)a.R * ((a.rows + kKvRowTile - 1) / kKvRowTile) * (a.kv.heads_kv / a.hbw);
+  if (segments * 16 <= groups)
+    return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
+                        kJoinWideWarps * 32, st, a, groups);
+  const int64_t ctas = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, st,
+                      a, groups);
 }
 
 template <class E, int D>
@@ -583,20 +528,7 @@ cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks,
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  if (after_chunks) {
-    e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, st, a);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t groups = (int64_t)grid * kDecWarps / a.hbw, items = (int64_t)a.R * a.rows * a.kv.heads_kv;
-  // segments of 16 parts or more on average: a block each (a 131072-token
-  // context, 228 parts a row: 24 us with a warp each, 8 with a block)
-  const int64_t segments = (int64_t)a.R * ((a.rows + kKvRowTile - 1) / kKvRowTile) * (a.kv.heads_kv / a.hbw);
-  if (segments * 16 <= groups)
-    return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
-                        kJoinWideWarps * 32, st, a, groups);
-  const int64_t ctas = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, st,
-                      a, groups);
+  return launch_join<E, D>(a, num_sms, after_chunks, (int64_t)grid * kDecWarps / a.hbw, st);
 }
 
 template <class E>
@@ -606,6 +538,12 @@ cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, bool after_chunk
   return launch_decode<E, 256>(a, num_sms, after_chunks, st);
 }
 
+template <class E>
+cudaError_t join_dispatch(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
+  if (a.kv.head_dim <= 64) return launch_join<E, 64>(a, num_sms, after_chunks, groups, st);
+  if (a.kv.head_dim <= 128) return launch_join<E, 128>(a, num_sms, after_chunks, groups, st);
+  return launch_join<E, 256>(a, num_sms, after_chunks, groups, st);
+}
 }  // namespace
 
 int64_t kv_attend_parts(int num_sms) { return (int64_t)num_sms * kDecCtas * kDecWarps * 2 * kKvRowTile; }
@@ -627,6 +565,12 @@ cudaError_t prepare_kv_decode_kernels() {
   return cudaSuccess;
 }
 
+cudaError_t launch_kv_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
+                           cudaStream_t st) {
+  return dtype == 0 ? join_dispatch<__half>(a, num_sms, after_chunks, groups, st)
+                    : join_dispatch<__nv_bfloat16>(a, num_sms, after_chunks, groups, st);
+}
+
 cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
   KvAttendArgs a = args;
   // Warps that work side by side on neighbouring heads of the same tokens, so
@@ -634,8 +578,7 @@ cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, b
   // power of two up to 16 that divides the key heads (256 requests, 32 key
   // heads of 128: 334 us with 1, 257 with 4, 247 with 8, 243 with 16, 247
   // with 32; 8 key heads: 367, 352 and 350 us with 1, 4 and 8).
-  a.hbw = 1;
-  while (a.hbw < 16 && a.kv.heads_kv % (2 * a.hbw) == 0) a.hbw *= 2;
+  a.hbw = heads_abreast(a.kv.heads_kv);
   return dtype == 0 ? decode_dispatch<__half>(a, num_sms, after_chunks, st)
                     : decode_dispatch<__nv_bfloat16>(a, num_sms, after_chunks, st);
 }

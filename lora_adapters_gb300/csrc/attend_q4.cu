@@ -1,101 +1,576 @@
-// slora_kv_attend over a cache held in 4 bits: a warp per (token, query head).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-
-#include <algorithm>
-
+// slora_kv_attend for few query rows (decode) over a cache held in 4 bits: the split
+// over the cache's length and the products of attend.cu, from codes.
+//
+// With codes c = k + 7 and a scale M for every token and group of 32 elements
+// (kv_q4.cuh), scores and results are
+//     s_j = q . k_j = sum_g M^K_jg / 8 (sum_e q_e c_e - 7 sum_e q_e),   e in group g,
+//     o_e = sum_j p_j v_je = 1/8 (sum_j (p_j M^V_jg) c_je - 7 sum_j p_j M^V_jg),
+// so that the matrix operands are the codes themselves:
+//  - a code in the low bits of a 16-bit word is the fp16 number c 2^-24 (subnormal), four
+//    bits further up 16 c 2^-24: one AND of a loaded word is an operand register, for
+//    both storage types.  The two positions go to products of their own, and the factor
+//    16 into Q or the result;
+//  - K's scale multiplies a group's accumulator, a pair of steps of the sum over the
+//    head; the offset 7 sum(q) is the accumulator's first value.  Queries are scaled by
+//    a power of two to below 2^14 first, which fp16's exponents hold for bf16 too (bits
+//    below 2^-24 of a row's largest element are lost);
+//  - V's scale goes into the weights: with every weight as two fp16 parts, p = hi + lo,
+//    and M 2^(7 - E) in fp16 (|M| < 2^E so far), hi M is again two parts, a product and
+//    its exact remainder.  Columns of the product that have no row (fewer than 8 query
+//    rows) take other groups' weights: RT rows times 8 / RT groups fill them, and the
+//    weights of a token are then worked out once instead of once a group;
+//  - each unit's result starts from zero and is added to the running one in fp32: with
+//    codes that are never negative, a running sum in the tensor core would lose bits
+//    to its truncation.
+//
+// Bound: what four issue slots a clock can do for the bytes of a unit.  Per 32 tokens of
+// a head of 128 there are 4,608 bytes, 196 cycles of an SM's share of the memory, against
+// 550 (two rows) to 700 (eight) instructions of a warp.
+#include "attend.cuh"
 #include "kv_q4.cuh"
 
 namespace slora {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kDecWarps = 4;             // per CTA
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int q4_ctas(int ng) { return ng <= 4 ? 3 : 2; }   // per SM
 
-template <class E>
-__global__ void __launch_bounds__(kThreads) kv_q4_attend_kernel(const __grid_constant__ KvAttendArgs a) {
-  __shared__ float s_q[kThreads / 32][kKvMaxHeadDim];
-  const KvDev& d = a.kv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = d.head_dim, ng = d.groups;
-  const int group = d.heads_q / d.heads_kv;
-  const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
-  const float sc = kLog2e * a.scale;
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + warp; u < (int64_t)a.T * d.heads_q;
-       u += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int t = (int)(u / d.heads_q), h = (int)(u - (int64_t)t * d.heads_q), hk = h / group;
-    const int req = d.tok_req[t], pos = d.tok_pos[t];
-    if (req < 0) continue;
-    const int row = dbg_index(d.req[req].w, d.max_rows, d.error);
-    const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)row * d.max_blocks;
-    __syncwarp();
-    for (int e = lane; e < dim; e += 32) s_q[warp][e] = Elem<E>::to(a.q[t * a.ldq + h * dim + e]);
-    for (int e = dim + lane; e < 32 * ng; e += 32) s_q[warp][e] = 0.f;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[kKvMaxHeadDim / 32] = {};
-    for (int j0 = 0; j0 <= pos; j0 += 32) {
-      const int j = j0 + lane;
-      const uint8_t *kr = nullptr, *vr = nullptr;
-      if (j <= pos) {
-        const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
-        const int kp = tab[b], vp = tab[plane + b];
-        if ((uint32_t)kp < (uint32_t)d.num_pages && (uint32_t)vp < (uint32_t)d.num_pages) {
-          kr = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, kp, off);
-          vr = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, vp, off);
-        } else {
-          report_err(d.error, kErrInvalid);
-        }
-      }
-      float s = -INFINITY;
-      if (kr) {
-        s = 0.f;
-        const uint32_t* codes = reinterpret_cast<const uint32_t*>(kr + hk * 16 * ng);
-        const uint16_t* Ms = reinterpret_cast<const uint16_t*>(kr + d.heads_kv * 16 * ng) + hk * ng;
-        for (int g = 0; g < ng; ++g) {
-          float x = 0.f;
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const uint32_t c = codes[k4 * ng + g];
-            for (int e = 0; e < 8; ++e)
-              x += (float)((int)(c >> (16 * (e & 1) + 4 * (e >> 1)) & 15) - 7) * s_q[warp][32 * g + 8 * k4 + e];
-          }
-          s += x * (Elem<E>::to(Ms[g]) * 0.125f);
-        }
-        s = a.softcap > 0.f ? capped<true>(s, sc, a.cap_t, a.cap2) : s * sc;
-      }
-      float mn = s;
-      for (int x = 16; x; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-      mn = fmaxf(mn, m);
-      const float f = mn == m ? 1.f : ex2(m - mn);
-      m = mn;
-      const float p = ex2(s - (m == -INFINITY ? 0.f : m));
-      l = l * f + p;
-      for (int g = 0; g < ng; ++g) o[g] *= f;
-      for (int i = 0; i < min(32, pos + 1 - j0); ++i) {
-        const uint8_t* v = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vr), i));
-        const float pi = __shfl_sync(0xffffffffu, p, i);
-        if (!v) continue;
-        const uint16_t* codes = reinterpret_cast<const uint16_t*>(v + hk * 16 * ng);
-        const uint16_t* Ms = reinterpret_cast<const uint16_t*>(v + d.heads_kv * 16 * ng) + hk * ng;
-        for (int g = 0; g < ng; ++g)
-          o[g] += pi * q4_value(codes[(lane >> 2) * ng + g] >> (4 * (lane & 3)) & 15, Elem<E>::to(Ms[g]));
-      }
-    }
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int g = 0; g < ng; ++g) {
-      const int e = 32 * g + lane;
-      if (e < dim) a.out[t * a.ldo + h * dim + e] = (uint16_t)Elem<E>::from2(o[g] * inv, 0.f);
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int src) {
+  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
+}
+// N consecutive words (N = 1, 2, 4, 8) that lie at a multiple of min(4 N, 16) bytes.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = load_stream(p + 16 * i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
   }
+}
+// The same of n <= 2 N halfwords, zeros after them.
+template <int N>
+__device__ __forceinline__ void load_halves(const uint8_t* p, int n, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = 2 * i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i) : 0u;
+    if (2 * i + 1 < n) w[i] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1) << 16;
+  }
+}
+template <class E>
+__device__ __forceinline__ float2 scales(uint32_t w) { return Elem<E>::to2(w); }
+
+// NG: groups of a head, rounded up to 2, 4 or 8; RT: rows that have columns of their own.
+template <class E, int NG, int RT, bool CAP>
+__global__ void __launch_bounds__(kDecThreads, q4_ctas(NG))
+kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
+  constexpr int GC = 8 / RT;        // groups whose weights lie side by side
+  constexpr int PASS = NG / GC;     // sets of weights a token has
+  constexpr int NR = RT == 8 ? 2 : 1;                  // rows of a lane
+  constexpr int NS = NG <= 4 ? 2 : 1, UNIT = 16 * NS;  // kv_q4_unit
+  constexpr int NO = RT == 2 ? NG / 2 : NG;            // groups of a lane's results
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  const KvDev& d = a.kv;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int hbw = a.hbw, blocks = d.heads_kv / hbw;
+  const int64_t gw = (int64_t)blockIdx.x * kDecWarps + (tid >> 5);
+  const int64_t groups = (int64_t)gridDim.x * kDecWarps / hbw;
+  const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, groups);
+  const int64_t grp = gw / hbw;
+  const int64_t u = grp * sp.run, u1 = min(sp.total, u + sp.run);
+  const int hsub = (int)(gw - grp * hbw);
+  const int dim = d.head_dim, P = d.per_page, group = d.heads_q / d.heads_kv, ng = d.groups;
+  const int kk = lane & 3, nn = lane >> 2;
+  const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
+  const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
+  if (u >= u1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  int left = (int)min(u1 - u, (int64_t)0x7fffffff);
+
+  // The units to do are fetched two ahead of the one that is multiplied (attend.cu).
+  struct {
+    int left, r, hb, rt, c;        // units left; request, head block, row tile, unit of the segment
+    int n, tiles, len;             // units of a segment, row tiles, tokens of the request
+    const int32_t* tab;            // the request's K pages
+  } f;
+  auto f_open = [&](const int4& rq) {
+    f.len = rq.z;
+    f.n = (rq.z + UNIT - 1) / UNIT;
+    f.tiles = (rq.y * group + kKvRowTile - 1) / kKvRowTile;
+    f.tab = d.table + 2 * a.layer * plane + (int64_t)dbg_index(rq.w, d.max_rows, d.error) * d.max_blocks;
+  };
+  auto no_units = [&](const int4& rq) {
+    return rq.y == 0 || (a.tpt > 0 && (int64_t)rq.y * group > kKvChunkRows);
+  };
+  {
+    f.left = left;
+    f.r = find_request(d.dec_off, a.R, u, blocks);
+    const int4 rq = __ldg(d.req + f.r);
+    f_open(rq);
+    const int64_t in_req = u - (int64_t)__ldg(d.dec_off + f.r) * blocks;
+    const int seg = (int)(in_req / f.n);
+    f.c = (int)(in_req - (int64_t)seg * f.n);
+    f.hb = seg / f.tiles;
+    f.rt = seg - f.hb * f.tiles;
+  }
+  int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
+  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin
+  // (NULL: past the request's length, or no such page).
+  struct Pages {
+    int k, v, in_page, hk;         // in_page -1: no token
+  };
+  auto fetch = [&](Pages& p) {
+    p.in_page = -1;
+    if (f.left == 0) return;
+    --f.left;
+    if (f.c == f.n) {
+      f.c = 0;
+      if (++f.rt == f.tiles) {
+        f.rt = 0;
+        if (++f.hb == blocks) {
+          f.hb = 0;
+          int4 rq;
+          do rq = __ldg(d.req + ++f.r);
+          while (no_units(rq));
+          f_open(rq);
+        }
+      }
+    }
+    p.hk = f.hb * hbw + hsub;
+    const int j = f.c++ * UNIT + (lane & (UNIT - 1));
+    if (j >= f.len) return;
+    const int b = (int)a.per_page_div.div((uint32_t)j);
+    p.in_page = j - b * P;
+    p.k = __ldg(f.tab + b);
+    p.v = __ldg(f.tab + plane + b);
+  };
+  bool missing = false;
+  const uint8_t *k_row, *v_row;
+  auto resolve = [&](const Pages& p) -> uint32_t {      // the unit's tokens with both rows, a bit each
+    k_row = v_row = nullptr;
+    if (p.in_page >= 0) {
+      if ((uint32_t)p.k < (uint32_t)d.num_pages && (uint32_t)p.v < (uint32_t)d.num_pages) {
+        k_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, p.k, p.in_page);
+        v_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, p.v, p.in_page);
+      } else {
+        missing = true;
+      }
+    }
+    return __ballot_sync(0xffffffffu, k_row != nullptr);
+  };
+  uint32_t kf[2 * NS][NG], km[2 * NS][NG / 2], vf[4 * NS][NG / 2], vm[NG / 2];
+  const int scale_at = d.heads_kv * 16 * ng;
+  const bool whole_groups = ng == NG;
+  auto load_k = [&](int hk) {
+#pragma unroll
+    for (int x = 0; x < 2 * NS; ++x) {
+      const uint8_t* p = shfl_ptr(k_row, nn + 8 * x);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) kf[x][g] = 0;
+#pragma unroll
+      for (int g = 0; g < NG / 2; ++g) km[x][g] = 0;
+      if (p) {
+        const uint8_t *pc = p + (hk * 16 + kk * 4) * ng, *ps = p + scale_at + hk * 2 * ng;
+        if (whole_groups) {
+          load_words<NG>(pc, kf[x]);
+          load_words<NG / 2>(ps, km[x]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            if (g < ng) kf[x][g] = __ldg(reinterpret_cast<const uint32_t*>(pc) + g);
+          load_halves<NG / 2>(ps, ng, km[x]);
+        }
+      }
+    }
+  };
+  auto load_v = [&](int hk) {
+#pragma unroll
+    for (int x = 0; x < 4 * NS; ++x) {
+      const uint8_t* p = shfl_ptr(v_row, (x >> 2) * 16 + 2 * kk + (x & 1) + (x & 2) * 4);
+#pragma unroll
+      for (int g = 0; g < NG / 2; ++g) vf[x][g] = 0;
+      if (p) {
+        const uint8_t* pc = p + (hk * 16 + nn * 2) * ng;
+        if (whole_groups) load_words<NG / 2>(pc, vf[x]);
+        else load_halves<NG / 2>(pc, ng, vf[x]);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG / 2; ++g) vm[g] = 0;
+    if (v_row) {
+      const uint8_t* ps = v_row + scale_at + hk * 2 * ng;
+      if (whole_groups) load_words<NG / 2>(ps, vm);
+      else load_halves<NG / 2>(ps, ng, vm);
+    }
+  };
+  Pages next;
+  fetch(next);
+  uint32_t valid = resolve(next);
+  load_k(next.hk);
+  load_v(next.hk);
+  fetch(next);
+
+  while (left > 0) {
+    int4 rq = __ldg(d.req + r);
+    while (no_units(rq)) rq = __ldg(d.req + ++r);
+    const int len = rq.z, q0 = rq.x, rows = rq.y * group;
+    const int nchunk = (len + UNIT - 1) / UNIT, tiles = (rows + kKvRowTile - 1) / kKvRowTile;
+    const int c1 = min(nchunk, c0 + left);
+    const int hk = hb * hbw + hsub;
+    const int ctx = len - rq.y;
+    // ---- this tile's queries: column n has row n / GC, (token, head of the group).  Eight
+    // elements of every group a lane, in the order of K's codes
+    uint32_t qf[NG][4];
+    float c_first[NG][NR], fac[NR];
+    {
+      const int row = rt * kKvRowTile + nn / GC;
+      const bool in = row < rows;
+      const uint16_t* src = a.q + (int64_t)dbg_index(q0 + (in ? row / group : 0), a.T, d.error) * a.ldq +
+                            (int64_t)(hk * group + (in ? row % group : 0)) * dim;
+      float top = 0.f;
+      uint4 raw[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int e = 32 * g + 8 * kk;
+        raw[g] = make_uint4(0, 0, 0, 0);
+        if (in && e < dim) raw[g] = *reinterpret_cast<const uint4*>(src + e);
+        float x[8];
+        unpack8<E>(raw[g], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^e <= top < 2^(e + 1); e = -100 where it is less
+      const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+      const float down = __uint_as_float((uint32_t)min(127 + 8 + e, 254) << 23) * (CAP ? 1.f : sc);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float x[8], sum = 0.f;
+        unpack8<E>(raw[g], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= up;
+          sum += x[i];
+        }
+        qf[g][0] = Elem<__half>::from2(x[0], x[1]);
+        qf[g][1] = Elem<__half>::from2(x[4], x[5]);
+        qf[g][2] = Elem<__half>::from2(x[2] * 0.0625f, x[3] * 0.0625f);
+        qf[g][3] = Elem<__half>::from2(x[6] * 0.0625f, x[7] * 0.0625f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= -7.f * 0x1p-24f;
+#pragma unroll
+        for (int x2 = 0; x2 < NR; ++x2) c_first[g][x2] = __shfl_sync(0xffffffffu, sum, (2 * kk + x2) * 4);
+      }
+#pragma unroll
+      for (int x2 = 0; x2 < NR; ++x2) fac[x2] = __shfl_sync(0xffffffffu, down, (2 * kk + x2) * 4);
+    }
+    // keys that this lane's rows may see: positions below lim
+    const int my_row = rt * kKvRowTile + 2 * kk / GC;
+    int lim[NR];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) lim[x] = ctx + min(my_row + x, rows - 1) / group + 1;
+
+    // results: elements 32 g + 4 nn + i of the lane's groups and rows; sums of p M a group
+    float o[NO][NR][4], lg[NO][NR], m[NR], l[NR];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NO; ++g) {
+        lg[g][x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[g][x][i] = 0.f;
+      }
+    }
+    int top_m = Elem<E>::kBf16 ? -64 : -8;               // E: every |M| so far is below 2^E
+
+    for (int c = c0; c < c1; ++c) {
+      // ---- scores of tokens nn + 8 x
+      float s[2 * NS][NR];
+#pragma unroll
+      for (int x = 0; x < 2 * NS; x += 2) {
+#pragma unroll
+        for (int y = 0; y < NR; ++y) s[x][y] = s[x + 1][y] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float acc[4] = {c_first[g][0], c_first[g][NR - 1], c_first[g][0], c_first[g][NR - 1]};
+          const uint32_t w0 = kf[x][g], w1 = kf[x + 1][g], h0 = w0 >> 8, h1 = w1 >> 8;
+          mma16816<__half>(acc, w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1]);
+          mma16816<__half>(acc, w0 & kHigh, w1 & kHigh, h0 & kHigh, h1 & kHigh, qf[g][2], qf[g][3]);
+          const float2 M0 = scales<E>(km[x][g / 2]), M1 = scales<E>(km[x + 1][g / 2]);
+#pragma unroll
+          for (int y = 0; y < NR; ++y) {
+            s[x][y] = fmaf(acc[y], g & 1 ? M0.y : M0.x, s[x][y]);
+            s[x + 1][y] = fmaf(acc[2 + y], g & 1 ? M1.y : M1.x, s[x + 1][y]);
+          }
+        }
+      }
+      const uint32_t held = valid >> nn;
+      valid = resolve(next);
+      const int hk_next = next.hk;
+      load_k(hk_next);
+      fetch(next);
+      float n[NR];
+#pragma unroll
+      for (int y = 0; y < NR; ++y) {
+        n[y] = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 2 * NS; ++x) {
+          float v = s[x][y] * fac[y];
+          if (CAP) v = capped<true>(v, sc, cap_t, cap2);
+          const bool seen = (held >> (8 * x) & 1) && c * UNIT + nn + 8 * x < lim[y];
+          s[x][y] = seen ? v : -INFINITY;
+          n[y] = fmaxf(n[y], s[x][y]);
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) n[y] = fmaxf(n[y], __shfl_xor_sync(0xffffffffu, n[y], x));
+        n[y] = fmaxf(n[y], m[y]);
+      }
+      // the unit's largest |M|, of any group and token
+      uint32_t bits = 0;
+#pragma unroll
+      for (int g = 0; g < NG / 2; ++g) bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
+      bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
+      const int e_new = max(top_m, Elem<E>::kBf16 ? (int)(bits >> 7) - 126 : (int)(bits >> 10) - 14);
+      bool grown = e_new != top_m;
+#pragma unroll
+      for (int y = 0; y < NR; ++y) grown |= n[y] != m[y];
+      if (__any_sync(0xffffffffu, grown)) {
+        const float down = ex2((float)(top_m - e_new));
+        top_m = e_new;
+#pragma unroll
+        for (int y = 0; y < NR; ++y) {
+          const float fl = n[y] == m[y] ? 1.f : ex2(m[y] - n[y]), fo = fl * down;
+          m[y] = n[y];
+          l[y] *= fl;
+#pragma unroll
+          for (int g = 0; g < NO; ++g) {
+            lg[g][y] *= fo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[g][y][i] *= fo;
+          }
+        }
+      }
+      // ---- weights times 2^7, in two fp16 parts: both rows' or the one row's twice
+      uint32_t ph[2 * NS], pl[2 * NS];
+      float p[2 * NS][NR];
+#pragma unroll
+      for (int x = 0; x < 2 * NS; ++x) {
+#pragma unroll
+        for (int y = 0; y < NR; ++y) {
+          // a row that has seen no key yet has m = -inf; its weights are zeros
+          p[x][y] = ex2(s[x][y] - (m[y] == -INFINITY ? 0.f : m[y] - 7.f));
+          l[y] += p[x][y];
+        }
+        ph[x] = Elem<__half>::from2(p[x][0], p[x][NR - 1]);
+        const float2 h = Elem<__half>::to2(ph[x]);
+        pl[x] = Elem<__half>::from2(p[x][0] - h.x, p[x][NR - 1] - h.y);
+      }
+      // ---- scales times 2^(7 - E), and results
+      const float m_up = __uint_as_float((uint32_t)(127 + 7 - top_m) << 23);
+      const uint32_t m_up2 = Elem<__half>::from2(m_up, m_up);      // (fp16 caches: E is -8 to 17)
+#pragma unroll
+      for (int ps = 0; ps < PASS; ++ps) {
+        uint32_t bh[2 * NS], bl[2 * NS];
+#pragma unroll
+        for (int x = 0; x < 2 * NS; ++x) {
+          const int src = (nn + 8 * x) & (UNIT - 1);
+          uint32_t w;                                    // the scales of the lane's two columns
+          if constexpr (RT == 8) {
+            w = __shfl_sync(0xffffffffu, vm[ps / 2], src);
+            w = __byte_perm(w, w, ps & 1 ? 0x3232 : 0x1010);
+          } else if constexpr (RT == 4) {
+            w = __shfl_sync(0xffffffffu, vm[ps], src);
+          } else {
+            const uint32_t w0 = __shfl_sync(0xffffffffu, vm[2 * ps], src), w1 = __shfl_sync(0xffffffffu, vm[2 * ps + 1], src);
+            w = kk & 1 ? w1 : w0;
+          }
+          float2 mf;
+          if constexpr (Elem<E>::kBf16) {
+            mf = scales<E>(w);
+            mf.x *= m_up;
+            mf.y *= m_up;
+            w = Elem<__half>::from2(mf.x, mf.y);
+          } else {
+            w = h2_mul(w, m_up2);
+            mf = Elem<__half>::to2(w);
+          }
+          if constexpr (RT == 8) {
+            lg[ps][0] = fmaf(p[x][0], mf.x, lg[ps][0]);
+            lg[ps][NR - 1] = fmaf(p[x][NR - 1], mf.x, lg[ps][NR - 1]);
+          } else {
+            lg[2 * ps][0] = fmaf(p[x][0], mf.x, lg[2 * ps][0]);
+            lg[2 * ps + 1][0] = fmaf(p[x][0], mf.y, lg[2 * ps + 1][0]);
+          }
+          const uint32_t hi = h2_mul(ph[x], w), lo = h2_fma(pl[x], w, h2_fma(ph[x], w, hi ^ 0x80008000u));
+          bh[x] = trans8x8(hi);
+          bl[x] = trans8x8(lo);
+        }
+        float acc[GC][2][4];
+#pragma unroll
+        for (int gi = 0; gi < GC; ++gi) {
+          const int g = ps * GC + gi;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[gi][0][i] = acc[gi][1][i] = 0.f;
+#pragma unroll
+          for (int s2 = 0; s2 < NS; ++s2) {
+            const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+            const uint32_t ta = __byte_perm(vf[4 * s2][g / 2], vf[4 * s2 + 1][g / 2], sel);
+            const uint32_t tb = __byte_perm(vf[4 * s2 + 2][g / 2], vf[4 * s2 + 3][g / 2], sel);
+            const uint32_t ua = ta >> 8, ub = tb >> 8;
+            mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[2 * s2], bh[2 * s2 + 1]);
+            mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[2 * s2], bh[2 * s2 + 1]);
+            mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bl[2 * s2], bl[2 * s2 + 1]);
+            mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bl[2 * s2], bl[2 * s2 + 1]);
+          }
+          // element i of the lane's four: i / 2 the accumulator's row, i % 2 which of the two
+          if constexpr (RT == 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) o[g][y % NR][i] += acc[gi][i & 1][(i & 2) + y];
+          } else if constexpr (RT == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[g][0][i] += acc[gi][i & 1][(i & 2) + (g & 1)];
+          }
+        }
+        if constexpr (RT == 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[2 * ps + j][0][i] += kk & 1 ? acc[2 % GC + j][i & 1][(i & 2) + j] : acc[j % GC][i & 1][(i & 2) + j];
+        }
+      }
+      load_v(hk_next);
+    }
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], x);
+#pragma unroll
+      for (int g = 0; g < NO; ++g)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) lg[g][y] += __shfl_xor_sync(0xffffffffu, lg[g][y], x);
+    }
+    const bool whole = c0 == 0 && c1 == nchunk;
+    const float m_down = __uint_as_float((uint32_t)(127 - 10 + top_m) << 23);     // 2^(E - 7) / 8
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+      const int row = my_row + y;
+      if (row >= rows) continue;
+      const float inv = whole ? (l[y] == 0.f ? 0.f : 1.f / l[y]) : 1.f;
+      uint16_t* dst = a.out + (int64_t)dbg_index(q0 + row / group, a.T, d.error) * a.ldo +
+                      (int64_t)(hk * group + row % group) * dim;
+      // slot 0: the segment began in an earlier run; slot 1: it begins here
+      const int64_t part = (gw * 2 + (c0 == 0 ? 1 : 0)) * kKvRowTile + row - rt * kKvRowTile;
+#pragma unroll
+      for (int gi = 0; gi < NO; ++gi) {
+        const int g = RT == 2 ? gi / 2 * 4 + 2 * (kk & 1) + gi % 2 : gi, e = 32 * g + 4 * nn;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = fmaf(o[gi][y][i], i & 1 ? 0x1p20f : 0x1p24f, -7.f * lg[gi][y]) * m_down * inv;
+        if (whole) {
+          if (e < dim)
+            *reinterpret_cast<uint2*>(dst + e) = make_uint2(Elem<E>::from2(v[0], v[1]), Elem<E>::from2(v[2], v[3]));
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + part * (32 * NG) + e) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      if (!whole && nn == 0 && (RT != 2 || (kk & 1) == 0)) a.part_ml[part] = make_float2(m[y], l[y]);
+    }
+    left -= c1 - c0;
+    c0 = 0;                        // the next segment, if any is left
+    if (++rt == tiles) {
+      rt = 0;
+      if (++hb == blocks) {
+        hb = 0;
+        ++r;
+      }
+    }
+  }
+  if (missing) report_err(d.error, kErrInvalid);
+  // after chunks: their kernel may still run, and this grid ends after it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class E, int NG, int RT>
+cudaError_t launch_rows(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
+  const int grid = num_sms * q4_ctas(NG);
+  auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true> : kv_q4_decode_kernel<E, NG, RT, false>;
+  cudaError_t e;
+  if (after_chunks) {
+    e = launch_early(kernel, dim3(grid), kDecThreads, st, a);
+  } else {
+    kernel<<<grid, kDecThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  return launch_kv_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, (int64_t)grid * kDecWarps / a.hbw, st);
+}
+template <class E>
+cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
+  const int ng = a.kv.groups;
+  if (ng <= 2)
+    return a.rows <= 4 ? launch_rows<E, 2, 4>(a, num_sms, after_chunks, st) : launch_rows<E, 2, 8>(a, num_sms, after_chunks, st);
+  if (ng <= 4)
+    return a.rows <= 2   ? launch_rows<E, 4, 2>(a, num_sms, after_chunks, st)
+           : a.rows <= 4 ? launch_rows<E, 4, 4>(a, num_sms, after_chunks, st)
+                         : launch_rows<E, 4, 8>(a, num_sms, after_chunks, st);
+  return a.rows <= 2 ? launch_rows<E, 8, 2>(a, num_sms, after_chunks, st) : launch_rows<E, 8, 8>(a, num_sms, after_chunks, st);
+}
+
+template <class E, int NG, int RT>
+cudaError_t prepare() {
+  // all of the SM's memory as first-level cache (attend.cu)
+  for (auto k : {kv_q4_decode_kernel<E, NG, RT, false>, kv_q4_decode_kernel<E, NG, RT, true>})
+    if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1))
+      return e;
+  return cudaSuccess;
+}
+template <class E>
+cudaError_t prepare_all() {
+  for (auto f : {prepare<E, 2, 4>, prepare<E, 2, 8>, prepare<E, 4, 2>, prepare<E, 4, 4>, prepare<E, 4, 8>, prepare<E, 8, 2>,
+                 prepare<E, 8, 8>})
+    if (cudaError_t e = f()) return e;
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool, cudaStream_t st) {
-  auto kernel = dtype == 0 ? kv_q4_attend_kernel<__half> : kv_q4_attend_kernel<__nv_bfloat16>;
-  kernel<<<8 * num_sms, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t prepare_kv_q4_decode_kernels() {
+  if (cudaError_t e = prepare_all<__half>()) return e;
+  return prepare_all<__nv_bfloat16>();
+}
+
+cudaError_t launch_kv_q4_decode(const KvAttendArgs& args, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
+  KvAttendArgs a = args;
+  a.hbw = heads_abreast(a.kv.heads_kv);
+  return dtype == 0 ? launch_decode<__half>(a, num_sms, after_chunks, st)
+                    : launch_decode<__nv_bfloat16>(a, num_sms, after_chunks, st);
 }
 
 }  // namespace slora

@@ -120,6 +120,7 @@ int check_config(const slora_pool* pool, const slora_kv_config* c, bool q4, Pool
   d.max_blocks = c->max_blocks;
   d.max_tokens = std::max(pv->max_tokens, 1);
   d.error = pv->d_error;
+  d.unit = q4 ? kv_q4_unit(c->head_dim) : kKvUnit;
   if (q4) {
     d.groups = (int32_t)groups;
     d.row_bytes = (int32_t)row_bytes;
@@ -205,7 +206,8 @@ int create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, bool q4, 
   kv->per_page_div.set((uint32_t)d.per_page);
   auto setup = [&]() -> int {
     CUDA_TRY(prepare_kv_kernels());
-    CUDA_TRY(prepare_kv_decode_kernels());
+    if (q4) CUDA_TRY(prepare_kv_q4_decode_kernels());
+    else CUDA_TRY(prepare_kv_decode_kernels());
     CUDA_TRY(cudaMalloc(&kv->d_freq, sizeof(uint64_t) * (size_t)(c->head_dim / 2)));
     const int64_t parts = kv_attend_parts(pv.num_sms);
     CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));

@@ -48,7 +48,7 @@ __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) {
 }
 
 // The attention's work for one request: decode units (row tiles of its (token,
-// head of the group) rows times 16-token units of its length) or, for a chunk,
+// head of the group) rows times units of its length) or, for a chunk,
 // 128-key tiles of every pair of row tiles, up to the pair's last position, and
 // the pair's own cost.
 __device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ctx, int32_t* dec, int32_t* tc) {
@@ -68,7 +68,7 @@ __device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ct
     if (fresh % step) n += kKvPairUnits + (len + kKvTile - 1) / kKvTile;
     *tc = (int32_t)min(n, (int64_t)0x7fffffff);
   } else {
-    *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + kKvUnit - 1) / kKvUnit), (int64_t)0x7fffffff);
+    *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + a.kv.unit - 1) / a.kv.unit), (int64_t)0x7fffffff);
   }
 }
 

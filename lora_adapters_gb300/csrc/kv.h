@@ -15,6 +15,9 @@ constexpr int kKvMaxRequests = 4096;   // == SLORA_KV_MAX_REQUESTS
 constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
 constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
 constexpr int kKvUnit = 16;            // tokens of one decode unit
+// The same of a 4-bit cache: twice as many, with the steps of the softmax once for all of
+// them, where registers hold their codes and the result.
+inline int32_t kv_q4_unit(int32_t head_dim) { return head_dim <= 128 ? 2 * kKvUnit : kKvUnit; }
 constexpr int kKvTile = 128;           // rows and keys of one chunk tile
 // A request whose new tokens make more rows than this (per key head) goes to the
 // chunk kernel, which reads the cache once for 256 of them; the decode kernel
@@ -77,6 +80,7 @@ struct KvDev {
   int32_t* tc_off;               // [R + 1] prefix sums of 128-key tiles, the chunk kernel's work per key head
   int32_t* slots;                // [layers][2][max_tokens] pool row of each token, -1: none
   int32_t* error;                // the pool's device error word
+  int32_t unit;                  // tokens of one decode unit
   // 4-bit caches
   int32_t groups;                // of 32 elements a head has, 0: a 16-bit cache
   int32_t row_bytes;             // of a token's row
@@ -158,7 +162,11 @@ int32_t kv_attend_cols(int32_t head_dim);
 // The decode kernel (after_chunks: while the chunk kernel launched before it
 // still runs), and the joins of what either kernel split.
 cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
+// The joins alone, of what `groups` groups of warps split.
+cudaError_t launch_kv_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
+                           cudaStream_t st);
 // The same over a 4-bit cache.
+cudaError_t prepare_kv_q4_decode_kernels();
 cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).
