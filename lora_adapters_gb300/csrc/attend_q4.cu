@@ -46,6 +46,11 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
   return y;
 }
+__device__ __forceinline__ uint32_t h2_neg(uint32_t a) {
+  uint32_t y;
+  asm("neg.f16x2 %0, %1;" : "=r"(y) : "r"(a));
+  return y;
+}
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int src) {
   return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
 }
@@ -73,11 +78,18 @@ __device__ __forceinline__ void load_halves(const uint8_t* p, int n, uint32_t (&
     if (2 * i + 1 < n) w[i] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1) << 16;
   }
 }
-template <class E>
-__device__ __forceinline__ float2 scales(uint32_t w) { return Elem<E>::to2(w); }
+// D = A B + C, C in registers of its own.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 
-// NG: groups of a head, rounded up to 2, 4 or 8; RT: rows that have columns of their own.
-template <class E, int NG, int RT, bool CAP>
+// NG: groups of a head, rounded up to 2, 4 or 8 (FULL: just as many); RT: rows that have
+// columns of their own.
+template <class E, int NG, int RT, bool CAP, bool FULL>
 __global__ void __launch_bounds__(kDecThreads, q4_ctas(NG))
 kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int GC = 8 / RT;        // groups whose weights lie side by side
@@ -132,8 +144,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     f.rt = seg - f.hb * f.tiles;
   }
   int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
-  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin
-  // (NULL: past the request's length, or no such page).
+  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin.  A
+  // token past the request's length, or without a page, has the pool's first row: its
+  // scores are masked, and its weights and V's scales are zeros.
   struct Pages {
     int k, v, in_page, hk;         // in_page -1: no token
   };
@@ -165,67 +178,48 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   bool missing = false;
   const uint8_t *k_row, *v_row;
   auto resolve = [&](const Pages& p) -> uint32_t {      // the unit's tokens with both rows, a bit each
-    k_row = v_row = nullptr;
-    if (p.in_page >= 0) {
-      if ((uint32_t)p.k < (uint32_t)d.num_pages && (uint32_t)p.v < (uint32_t)d.num_pages) {
-        k_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, p.k, p.in_page);
-        v_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, p.v, p.in_page);
-      } else {
-        missing = true;
-      }
-    }
-    return __ballot_sync(0xffffffffu, k_row != nullptr);
+    const bool token = p.in_page >= 0;
+    const bool ok = token && (uint32_t)p.k < (uint32_t)d.num_pages && (uint32_t)p.v < (uint32_t)d.num_pages;
+    missing |= token && !ok;
+    const int kp = ok ? p.k : 0, vp = ok ? p.v : 0, at = ok ? p.in_page : 0;
+    k_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, kp, at);
+    v_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, vp, at);
+    return __ballot_sync(0xffffffffu, ok);
   };
-  uint32_t kf[2 * NS][NG], km[2 * NS][NG / 2], vf[4 * NS][NG / 2], vm[NG / 2];
+  uint32_t kf[2 * NS][NG], km[2 * NS][NG / 2], vf[4 * NS][NG / 2], vm[NG / 2], v_tokens;
   const int scale_at = d.heads_kv * 16 * ng;
-  const bool whole_groups = ng == NG;
   auto load_k = [&](int hk) {
 #pragma unroll
     for (int x = 0; x < 2 * NS; ++x) {
       const uint8_t* p = shfl_ptr(k_row, nn + 8 * x);
+      const uint8_t *pc = p + (hk * 16 + kk * 4) * ng, *ps = p + (scale_at + hk * 2 * ng);
+      if constexpr (FULL) {
+        load_words<NG>(pc, kf[x]);
+        load_words<NG / 2>(ps, km[x]);
+      } else {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) kf[x][g] = 0;
-#pragma unroll
-      for (int g = 0; g < NG / 2; ++g) km[x][g] = 0;
-      if (p) {
-        const uint8_t *pc = p + (hk * 16 + kk * 4) * ng, *ps = p + scale_at + hk * 2 * ng;
-        if (whole_groups) {
-          load_words<NG>(pc, kf[x]);
-          load_words<NG / 2>(ps, km[x]);
-        } else {
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            if (g < ng) kf[x][g] = __ldg(reinterpret_cast<const uint32_t*>(pc) + g);
-          load_halves<NG / 2>(ps, ng, km[x]);
-        }
+        for (int g = 0; g < NG; ++g) kf[x][g] = g < ng ? __ldg(reinterpret_cast<const uint32_t*>(pc) + g) : 0u;
+        load_halves<NG / 2>(ps, ng, km[x]);
       }
     }
   };
-  auto load_v = [&](int hk) {
+  auto load_v = [&](int hk, uint32_t tokens) {
 #pragma unroll
     for (int x = 0; x < 4 * NS; ++x) {
-      const uint8_t* p = shfl_ptr(v_row, (x >> 2) * 16 + 2 * kk + (x & 1) + (x & 2) * 4);
-#pragma unroll
-      for (int g = 0; g < NG / 2; ++g) vf[x][g] = 0;
-      if (p) {
-        const uint8_t* pc = p + (hk * 16 + nn * 2) * ng;
-        if (whole_groups) load_words<NG / 2>(pc, vf[x]);
-        else load_halves<NG / 2>(pc, ng, vf[x]);
-      }
+      const uint8_t* pc = shfl_ptr(v_row, (x >> 2) * 16 + 2 * kk + (x & 1) + (x & 2) * 4) + (hk * 16 + nn * 2) * ng;
+      if constexpr (FULL) load_words<NG / 2>(pc, vf[x]);
+      else load_halves<NG / 2>(pc, ng, vf[x]);
     }
-#pragma unroll
-    for (int g = 0; g < NG / 2; ++g) vm[g] = 0;
-    if (v_row) {
-      const uint8_t* ps = v_row + scale_at + hk * 2 * ng;
-      if (whole_groups) load_words<NG / 2>(ps, vm);
-      else load_halves<NG / 2>(ps, ng, vm);
-    }
+    const uint8_t* ps = v_row + (scale_at + hk * 2 * ng);
+    if constexpr (FULL) load_words<NG / 2>(ps, vm);
+    else load_halves<NG / 2>(ps, ng, vm);
+    v_tokens = tokens;
   };
   Pages next;
   fetch(next);
   uint32_t valid = resolve(next);
   load_k(next.hk);
-  load_v(next.hk);
+  load_v(next.hk, valid);
   fetch(next);
 
   while (left > 0) {
@@ -290,6 +284,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     int lim[NR];
 #pragma unroll
     for (int x = 0; x < NR; ++x) lim[x] = ctx + min(my_row + x, rows - 1) / group + 1;
+    const int lim_first = ctx + rt * kKvRowTile / group + 1;       // of the tile's first row
 
     // results: elements 32 g + 4 nn + i of the lane's groups and rows; sums of p M a group
     float o[NO][NR][4], lg[NO][NR], m[NR], l[NR];
@@ -315,11 +310,12 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         for (int y = 0; y < NR; ++y) s[x][y] = s[x + 1][y] = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float acc[4] = {c_first[g][0], c_first[g][NR - 1], c_first[g][0], c_first[g][NR - 1]};
+          float acc[4];
           const uint32_t w0 = kf[x][g], w1 = kf[x + 1][g], h0 = w0 >> 8, h1 = w1 >> 8;
-          mma16816<__half>(acc, w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1]);
+          mma16816_from(acc, w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1], c_first[g][0],
+                        c_first[g][NR - 1], c_first[g][0], c_first[g][NR - 1]);
           mma16816<__half>(acc, w0 & kHigh, w1 & kHigh, h0 & kHigh, h1 & kHigh, qf[g][2], qf[g][3]);
-          const float2 M0 = scales<E>(km[x][g / 2]), M1 = scales<E>(km[x + 1][g / 2]);
+          const float2 M0 = Elem<E>::to2(km[x][g / 2]), M1 = Elem<E>::to2(km[x + 1][g / 2]);
 #pragma unroll
           for (int y = 0; y < NR; ++y) {
             s[x][y] = fmaf(acc[y], g & 1 ? M0.y : M0.x, s[x][y]);
@@ -327,31 +323,43 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           }
         }
       }
-      const uint32_t held = valid >> nn;
+      const uint32_t held_all = valid;
       valid = resolve(next);
       const int hk_next = next.hk;
       load_k(hk_next);
       fetch(next);
+      if (CAP) {
+#pragma unroll
+        for (int y = 0; y < NR; ++y)
+#pragma unroll
+          for (int x = 0; x < 2 * NS; ++x) s[x][y] = capped<true>(s[x][y] * fac[y], sc, cap_t, cap2);
+      }
+      // some token is not there, or after the tile's first row
+      if (held_all != 0xffffffffu || (c + 1) * UNIT > lim_first) {
+#pragma unroll
+        for (int y = 0; y < NR; ++y)
+#pragma unroll
+          for (int x = 0; x < 2 * NS; ++x)
+            if (!(held_all >> (nn + 8 * x) & 1) || c * UNIT + nn + 8 * x >= lim[y]) s[x][y] = -INFINITY;
+      }
       float n[NR];
 #pragma unroll
       for (int y = 0; y < NR; ++y) {
-        n[y] = -INFINITY;
+        n[y] = fmaxf(s[0][y], s[1][y]);
 #pragma unroll
-        for (int x = 0; x < 2 * NS; ++x) {
-          float v = s[x][y] * fac[y];
-          if (CAP) v = capped<true>(v, sc, cap_t, cap2);
-          const bool seen = (held >> (8 * x) & 1) && c * UNIT + nn + 8 * x < lim[y];
-          s[x][y] = seen ? v : -INFINITY;
-          n[y] = fmaxf(n[y], s[x][y]);
-        }
+        for (int x = 2; x < 2 * NS; ++x) n[y] = fmaxf(n[y], s[x][y]);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) n[y] = fmaxf(n[y], __shfl_xor_sync(0xffffffffu, n[y], x));
+        if (!CAP) n[y] *= fac[y];                          // > 0
         n[y] = fmaxf(n[y], m[y]);
       }
       // the unit's largest |M|, of any group and token
       uint32_t bits = 0;
 #pragma unroll
-      for (int g = 0; g < NG / 2; ++g) bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
+      for (int g = 0; g < NG / 2; ++g) {
+        if (!(v_tokens >> (lane & (UNIT - 1)) & 1)) vm[g] = 0;
+        bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
+      }
       bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
       const int e_new = max(top_m, Elem<E>::kBf16 ? (int)(bits >> 7) - 126 : (int)(bits >> 10) - 14);
       bool grown = e_new != top_m;
@@ -381,16 +389,21 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 #pragma unroll
         for (int y = 0; y < NR; ++y) {
           // a row that has seen no key yet has m = -inf; its weights are zeros
-          p[x][y] = ex2(s[x][y] - (m[y] == -INFINITY ? 0.f : m[y] - 7.f));
+          const float z = m[y] == -INFINITY ? 0.f : 7.f - m[y];
+          p[x][y] = ex2(CAP ? s[x][y] + z : fmaf(s[x][y], fac[y], z));
           l[y] += p[x][y];
         }
         ph[x] = Elem<__half>::from2(p[x][0], p[x][NR - 1]);
         const float2 h = Elem<__half>::to2(ph[x]);
         pl[x] = Elem<__half>::from2(p[x][0] - h.x, p[x][NR - 1] - h.y);
       }
-      // ---- scales times 2^(7 - E), and results
+      // ---- the token's scales times 2^(7 - E) in fp16, and results
       const float m_up = __uint_as_float((uint32_t)(127 + 7 - top_m) << 23);
-      const uint32_t m_up2 = Elem<__half>::from2(m_up, m_up);      // (fp16 caches: E is -8 to 17)
+#pragma unroll
+      for (int g = 0; g < NG / 2; ++g) {
+        const float2 M = Elem<E>::to2(vm[g]);
+        vm[g] = Elem<__half>::from2(M.x * m_up, M.y * m_up);
+      }
 #pragma unroll
       for (int ps = 0; ps < PASS; ++ps) {
         uint32_t bh[2 * NS], bl[2 * NS];
@@ -407,16 +420,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             const uint32_t w0 = __shfl_sync(0xffffffffu, vm[2 * ps], src), w1 = __shfl_sync(0xffffffffu, vm[2 * ps + 1], src);
             w = kk & 1 ? w1 : w0;
           }
-          float2 mf;
-          if constexpr (Elem<E>::kBf16) {
-            mf = scales<E>(w);
-            mf.x *= m_up;
-            mf.y *= m_up;
-            w = Elem<__half>::from2(mf.x, mf.y);
-          } else {
-            w = h2_mul(w, m_up2);
-            mf = Elem<__half>::to2(w);
-          }
+          const float2 mf = Elem<__half>::to2(w);
           if constexpr (RT == 8) {
             lg[ps][0] = fmaf(p[x][0], mf.x, lg[ps][0]);
             lg[ps][NR - 1] = fmaf(p[x][NR - 1], mf.x, lg[ps][NR - 1]);
@@ -424,7 +428,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             lg[2 * ps][0] = fmaf(p[x][0], mf.x, lg[2 * ps][0]);
             lg[2 * ps + 1][0] = fmaf(p[x][0], mf.y, lg[2 * ps + 1][0]);
           }
-          const uint32_t hi = h2_mul(ph[x], w), lo = h2_fma(pl[x], w, h2_fma(ph[x], w, hi ^ 0x80008000u));
+          const uint32_t hi = h2_mul(ph[x], w), lo = h2_fma(pl[x], w, h2_fma(ph[x], w, h2_neg(hi)));
           bh[x] = trans8x8(hi);
           bl[x] = trans8x8(lo);
         }
@@ -433,15 +437,18 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         for (int gi = 0; gi < GC; ++gi) {
           const int g = ps * GC + gi;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[gi][0][i] = acc[gi][1][i] = 0.f;
-#pragma unroll
           for (int s2 = 0; s2 < NS; ++s2) {
             const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
             const uint32_t ta = __byte_perm(vf[4 * s2][g / 2], vf[4 * s2 + 1][g / 2], sel);
             const uint32_t tb = __byte_perm(vf[4 * s2 + 2][g / 2], vf[4 * s2 + 3][g / 2], sel);
             const uint32_t ua = ta >> 8, ub = tb >> 8;
-            mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[2 * s2], bh[2 * s2 + 1]);
-            mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[2 * s2], bh[2 * s2 + 1]);
+            if (s2 == 0) {
+              mma16816_from(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[0], bh[1], 0.f, 0.f, 0.f, 0.f);
+              mma16816_from(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[0], bh[1], 0.f, 0.f, 0.f, 0.f);
+            } else {
+              mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[2 * s2], bh[2 * s2 + 1]);
+              mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[2 * s2], bh[2 * s2 + 1]);
+            }
             mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bl[2 * s2], bl[2 * s2 + 1]);
             mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bl[2 * s2], bl[2 * s2 + 1]);
           }
@@ -464,7 +471,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
               o[2 * ps + j][0][i] += kk & 1 ? acc[2 % GC + j][i & 1][(i & 2) + j] : acc[j % GC][i & 1][(i & 2) + j];
         }
       }
-      load_v(hk_next);
+      load_v(hk_next, valid);
     }
 #pragma unroll
     for (int y = 0; y < NR; ++y) {
@@ -517,10 +524,10 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <class E, int NG, int RT>
+template <class E, int NG, int RT, bool FULL = true>
 cudaError_t launch_rows(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
   const int grid = num_sms * q4_ctas(NG);
-  auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true> : kv_q4_decode_kernel<E, NG, RT, false>;
+  auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true, FULL> : kv_q4_decode_kernel<E, NG, RT, false, FULL>;
   cudaError_t e;
   if (after_chunks) {
     e = launch_early(kernel, dim3(grid), kDecThreads, st, a);
@@ -534,6 +541,9 @@ cudaError_t launch_rows(const KvAttendArgs& a, int num_sms, bool after_chunks, c
 template <class E>
 cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
   const int ng = a.kv.groups;
+  if (ng == 1) return launch_rows<E, 2, 8, false>(a, num_sms, after_chunks, st);
+  if (ng == 3) return launch_rows<E, 4, 8, false>(a, num_sms, after_chunks, st);
+  if (ng > 4 && ng < 8) return launch_rows<E, 8, 8, false>(a, num_sms, after_chunks, st);
   if (ng <= 2)
     return a.rows <= 4 ? launch_rows<E, 2, 4>(a, num_sms, after_chunks, st) : launch_rows<E, 2, 8>(a, num_sms, after_chunks, st);
   if (ng <= 4)
@@ -543,10 +553,10 @@ cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks,
   return a.rows <= 2 ? launch_rows<E, 8, 2>(a, num_sms, after_chunks, st) : launch_rows<E, 8, 8>(a, num_sms, after_chunks, st);
 }
 
-template <class E, int NG, int RT>
+template <class E, int NG, int RT, bool FULL = true>
 cudaError_t prepare() {
   // all of the SM's memory as first-level cache (attend.cu)
-  for (auto k : {kv_q4_decode_kernel<E, NG, RT, false>, kv_q4_decode_kernel<E, NG, RT, true>})
+  for (auto k : {kv_q4_decode_kernel<E, NG, RT, false, FULL>, kv_q4_decode_kernel<E, NG, RT, true, FULL>})
     if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1))
       return e;
   return cudaSuccess;
@@ -554,7 +564,7 @@ cudaError_t prepare() {
 template <class E>
 cudaError_t prepare_all() {
   for (auto f : {prepare<E, 2, 4>, prepare<E, 2, 8>, prepare<E, 4, 2>, prepare<E, 4, 4>, prepare<E, 4, 8>, prepare<E, 8, 2>,
-                 prepare<E, 8, 8>})
+                 prepare<E, 8, 8>, prepare<E, 2, 8, false>, prepare<E, 4, 8, false>, prepare<E, 8, 8, false>})
     if (cudaError_t e = f()) return e;
   return cudaSuccess;
 }
