@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) kv_chunk_join_kernel(const 
 template <class E, int D>
 cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
   if (after_chunks) {
-    const cudaError_t e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, st, a);
+    const cudaError_t e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, 0, st, a);
     if (e != cudaSuccess) return e;
   }
   const int64_t items = (int64_t)a.R * a.rows * a.kv.heads_kv;
@@ -510,10 +510,10 @@ cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, i
   const int64_t segments = (int64_t)a.R * ((a.rows + kKvRowTile - 1) / kKvRowTile) * (a.kv.heads_kv / a.hbw);
   if (segments * 16 <= groups)
     return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
-                        kJoinWideWarps * 32, st, a, groups);
+                        kJoinWideWarps * 32, 0, st, a, groups);
   const int64_t ctas = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, st,
-                      a, groups);
+  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, 0,
+                      st, a, groups);
 }
 
 template <class E, int D>
@@ -522,7 +522,7 @@ cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks,
   auto kernel = a.softcap > 0.f ? kv_decode_kernel<E, D, true> : kv_decode_kernel<E, D, false>;
   cudaError_t e;
   if (after_chunks) {
-    e = launch_early(kernel, dim3(grid), kDecThreads, st, a);
+    e = launch_early(kernel, dim3(grid), kDecThreads, 0, st, a);
   } else {
     kernel<<<grid, kDecThreads, 0, st>>>(a);
     e = cudaGetLastError();

@@ -32,9 +32,10 @@
 namespace slora {
 namespace {
 
-constexpr int kDecWarps = 4;             // per CTA
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int q4_ctas(int ng) { return ng <= 4 ? 3 : 2; }   // per SM
+// Warps of a CTA: one for each of the neighbouring key heads that it works on, at most
+// kMaxAbreast; and as many CTAs an SM as make q4_warps.
+constexpr int kMaxAbreast = 6;
+constexpr int q4_warps(int ng) { return ng <= 4 ? 12 : 6; }   // an SM: 170 or 255 registers a thread
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t y;
@@ -54,34 +55,73 @@ __device__ __forceinline__ uint32_t h2_neg(uint32_t a) {
 __device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int src) {
   return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
 }
-// N consecutive words (N = 1, 2, 4, 8) that lie at a multiple of min(4 N, 16) bytes.
+// 16 bytes global -> shared, asynchronously, past the first-level cache; bytes = 0: zeros,
+// nothing is read.
+__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// N consecutive words of shared memory (N = 1, 2, 4, 8), at a multiple of min(4 N, 16) bytes.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
   } else if constexpr (N == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
   } else {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = load_stream(p + 16 * i);
-      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(at + 4 * i));
   }
 }
-// The same of n <= 2 N halfwords, zeros after them.
+__device__ __forceinline__ uint32_t lds_half(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts_half(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void load_halves(const uint8_t* p, int n, uint32_t (&w)[N]) {
+__device__ __forceinline__ void sts(uint32_t at, const uint32_t (&w)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i] = 2 * i < n ? __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i) : 0u;
-    if (2 * i + 1 < n) w[i] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1) << 16;
-  }
+  for (int i = 0; i < N; ++i) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(w[i]) : "memory");
 }
-// D = A B + C, C in registers of its own.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile(
+
+// A CTA's ring of units in shared memory.  Of a unit: K's codes [head][token][16 NG bytes];
+// V's, the same, with 16-byte pieces exchanged so that the four tokens that a warp reads at
+// a time lie in different banks; K's scales and V's, [token][all heads', from the last
+// multiple of 16 bytes before them].
+template <int NG>
+struct Ring {
+  static constexpr int kUnit = NG <= 4 ? 32 : 16;      // kv_q4_unit
+  static constexpr int kStages = 3;
+  static constexpr int kCodes = kUnit * 16 * NG;       // of a head
+  // where 16-byte piece p of token t of V lies
+  static __device__ __forceinline__ int v_piece(int t, int p) {
+    constexpr int kPer = NG == 8 ? 1 : 8 / NG;         // tokens of 128 bytes
+    return (t / kPer) * 128 + ((((t % kPer) * NG + p) ^ (NG == 2 ? 2 * ((t >> 2) & 1) : 2 * ((t >> 1) & 3))) << 4);
+  }
+};
+// Bytes that hold the scales of `heads` neighbouring heads of a token, wherever they begin.
+__host__ __device__ __forceinline__ int scale_bytes(int heads, int ng) {
+  const int n = heads * 2 * ng, step = n & -n;         // they begin at multiples of it
+  return n % 16 ? (n + 31 - step) / 16 * 16 : n;
+}
+template <int NG>
+__host__ __device__ __forceinline__ int stage_bytes(int heads, int ng) {
+  return 2 * (heads * Ring<NG>::kCodes + Ring<NG>::kUnit * scale_bytes(heads, ng));
+}
+
+// D = A B + C.  Not volatile: the compiler may place products that do not depend on each
+// other between those that do.
+__device__ __forceinline__ void mma_h(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
@@ -90,24 +130,27 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32
 // NG: groups of a head, rounded up to 2, 4 or 8 (FULL: just as many); RT: rows that have
 // columns of their own.
 template <class E, int NG, int RT, bool CAP, bool FULL>
-__global__ void __launch_bounds__(kDecThreads, q4_ctas(NG))
+__global__ void __launch_bounds__(kMaxAbreast * 32, q4_warps(NG) / kMaxAbreast)
 kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int GC = 8 / RT;        // groups whose weights lie side by side
   constexpr int PASS = NG / GC;     // sets of weights a token has
   constexpr int NR = RT == 8 ? 2 : 1;                  // rows of a lane
-  constexpr int NS = NG <= 4 ? 2 : 1, UNIT = 16 * NS;  // kv_q4_unit
+  using R = Ring<NG>;
+  constexpr int UNIT = R::kUnit, NS = UNIT / 16;
   constexpr int NO = RT == 2 ? NG / 2 : NG;            // groups of a lane's results
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   const KvDev& d = a.kv;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int hbw = a.hbw, blocks = d.heads_kv / hbw;
-  const int64_t gw = (int64_t)blockIdx.x * kDecWarps + (tid >> 5);
-  const int64_t groups = (int64_t)gridDim.x * kDecWarps / hbw;
-  const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, groups);
-  const int64_t grp = gw / hbw;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ng = d.groups;
+  // a group of CTAs takes the same units of hbw neighbouring heads, one head a warp
+  const int heads = blockDim.x >> 5, hbw = a.hbw, blocks = d.heads_kv / hbw, ctas = hbw / heads;
+  const int grp = blockIdx.x / ctas, hsub0 = (blockIdx.x - grp * ctas) * heads, hsub = hsub0 + warp;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_raw);
+  const int stage_size = stage_bytes<NG>(heads, ng), scale_size = scale_bytes(heads, ng);
+  const int at_v = heads * R::kCodes, at_ks = 2 * at_v, at_vs = at_ks + UNIT * scale_size;   // in a stage
+  const DecSplit sp = dec_split(__ldg(d.dec_off + a.R), blocks, gridDim.x / ctas);
   const int64_t u = grp * sp.run, u1 = min(sp.total, u + sp.run);
-  const int hsub = (int)(gw - grp * hbw);
-  const int dim = d.head_dim, P = d.per_page, group = d.heads_q / d.heads_kv, ng = d.groups;
+  const int dim = d.head_dim, P = d.per_page, group = d.heads_q / d.heads_kv;
   const int kk = lane & 3, nn = lane >> 2;
   const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
   const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
@@ -117,7 +160,8 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   }
   int left = (int)min(u1 - u, (int64_t)0x7fffffff);
 
-  // The units to do are fetched two ahead of the one that is multiplied (attend.cu).
+  // The units to do are on their way to shared memory while the two before them are
+  // multiplied, from one segment into the next; their pages are looked up one ahead of that.
   struct {
     int left, r, hb, rt, c;        // units left; request, head block, row tile, unit of the segment
     int n, tiles, len;             // units of a segment, row tiles, tokens of the request
@@ -144,11 +188,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     f.rt = seg - f.hb * f.tiles;
   }
   int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
-  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin.  A
-  // token past the request's length, or without a page, has the pool's first row: its
-  // scores are masked, and its weights and V's scales are zeros.
+  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin.  Of a
+  // token past the request's length, or without a page, nothing is read: its codes and
+  // scales are zeros, and its scores are masked.
   struct Pages {
-    int k, v, in_page, hk;         // in_page -1: no token
+    int k, v, in_page, hb;         // in_page -1: no token; hb: block of heads
   };
   auto fetch = [&](Pages& p) {
     p.in_page = -1;
@@ -167,7 +211,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         }
       }
     }
-    p.hk = f.hb * hbw + hsub;
+    p.hb = f.hb;
     const int j = f.c++ * UNIT + (lane & (UNIT - 1));
     if (j >= f.len) return;
     const int b = (int)a.per_page_div.div((uint32_t)j);
@@ -176,51 +220,62 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     p.v = __ldg(f.tab + plane + b);
   };
   bool missing = false;
-  const uint8_t *k_row, *v_row;
-  auto resolve = [&](const Pages& p) -> uint32_t {      // the unit's tokens with both rows, a bit each
+  const int scale_at = d.heads_kv * 16 * ng;
+  // This thread's part of a unit's copies: piece `piece` of head `p_head`'s codes, of the tokens
+  // p_token, p_token + 32 / NG, ...  A token's pieces of all heads are consecutive threads'
+  const int p_token = tid / (heads * NG), p_head = tid % (heads * NG) / NG, piece = tid % NG;
+  // Copies the unit whose pages were looked up to a stage of the ring, and looks the next
+  // one's up; the tokens with both rows, a bit each.
+  auto issue = [&](Pages& p, uint32_t stage) -> uint32_t {
     const bool token = p.in_page >= 0;
     const bool ok = token && (uint32_t)p.k < (uint32_t)d.num_pages && (uint32_t)p.v < (uint32_t)d.num_pages;
     missing |= token && !ok;
     const int kp = ok ? p.k : 0, vp = ok ? p.v : 0, at = ok ? p.in_page : 0;
-    k_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, kp, at);
-    v_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, vp, at);
-    return __ballot_sync(0xffffffffu, ok);
+    const uint8_t* pool = reinterpret_cast<const uint8_t*>(d.pool);
+    const uint8_t *k_row = pool + q4_row(d, kp, at), *v_row = pool + q4_row(d, vp, at);
+    const uint32_t valid = __ballot_sync(0xffffffffu, ok), own_bytes = ok ? 16 : 0;
+    const uint32_t to = ring + stage * stage_size, to_k = to + p_head * R::kCodes + piece * 16,
+                   to_v = to + at_v + p_head * R::kCodes;
+    const int head0 = p.hb * hbw + hsub0, in_row = ((head0 + p_head) * ng + piece) * 16;
+#pragma unroll
+    for (int x = 0; x < UNIT * NG / 32; ++x) {
+      const int t = p_token + x * (32 / NG);
+      const uint8_t* src = shfl_ptr(k_row, t) + in_row;
+      if (FULL || piece < ng) cp_async(to_k + t * 16 * NG, src, valid >> t & 1 ? 16 : 0);
+    }
+#pragma unroll
+    for (int x = 0; x < UNIT * NG / 32; ++x) {
+      const int t = p_token + x * (32 / NG);
+      const uint8_t* src = shfl_ptr(v_row, t) + in_row;
+      if (FULL || piece < ng) cp_async(to_v + R::v_piece(t, piece), src, valid >> t & 1 ? 16 : 0);
+    }
+    // scales: K's pieces, then V's, one a warp (UNIT = 16: two) for all tokens
+    const int s_row = scale_at + head0 * 2 * ng, pieces = ((s_row & 15) + heads * 2 * ng + 15) >> 4;
+    for (int i = tid / UNIT; i < 2 * pieces; i += heads * 32 / UNIT) {
+      const bool v = i >= pieces;
+      const int from = (v ? i - pieces : i) * 16;
+      cp_async(to + (v ? at_vs : at_ks) + (lane & (UNIT - 1)) * scale_size + from, (v ? v_row : k_row) + (s_row & ~15) + from,
+               own_bytes);
+    }
+    cp_commit();
+    fetch(p);
+    return valid;
   };
-  uint32_t kf[2 * NS][NG], km[2 * NS][NG / 2], vf[4 * NS][NG / 2], vm[NG / 2], v_tokens;
-  const int scale_at = d.heads_kv * 16 * ng;
-  auto load_k = [&](int hk) {
+  // Scales of a token from the ring.
+  auto token_scales = [&](uint32_t at, uint32_t (&w)[NG / 2]) {
+    if constexpr (FULL) {
+      lds<NG / 2>(at, w);
+    } else {
 #pragma unroll
-    for (int x = 0; x < 2 * NS; ++x) {
-      const uint8_t* p = shfl_ptr(k_row, nn + 8 * x);
-      const uint8_t *pc = p + (hk * 16 + kk * 4) * ng, *ps = p + (scale_at + hk * 2 * ng);
-      if constexpr (FULL) {
-        load_words<NG>(pc, kf[x]);
-        load_words<NG / 2>(ps, km[x]);
-      } else {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) kf[x][g] = g < ng ? __ldg(reinterpret_cast<const uint32_t*>(pc) + g) : 0u;
-        load_halves<NG / 2>(ps, ng, km[x]);
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t h = g < ng ? lds_half(at + 2 * g) : 0u;
+        w[g / 2] = g & 1 ? w[g / 2] | h << 16 : h;
       }
     }
   };
-  auto load_v = [&](int hk, uint32_t tokens) {
-#pragma unroll
-    for (int x = 0; x < 4 * NS; ++x) {
-      const uint8_t* pc = shfl_ptr(v_row, (x >> 2) * 16 + 2 * kk + (x & 1) + (x & 2) * 4) + (hk * 16 + nn * 2) * ng;
-      if constexpr (FULL) load_words<NG / 2>(pc, vf[x]);
-      else load_halves<NG / 2>(pc, ng, vf[x]);
-    }
-    const uint8_t* ps = v_row + (scale_at + hk * 2 * ng);
-    if constexpr (FULL) load_words<NG / 2>(ps, vm);
-    else load_halves<NG / 2>(ps, ng, vm);
-    v_tokens = tokens;
-  };
   Pages next;
   fetch(next);
-  uint32_t valid = resolve(next);
-  load_k(next.hk);
-  load_v(next.hk, valid);
-  fetch(next);
+  uint32_t valid = issue(next, 0), valid1 = issue(next, 1), stage = 0;
 
   while (left > 0) {
     int4 rq = __ldg(d.req + r);
@@ -299,35 +354,58 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         for (int i = 0; i < 4; ++i) o[g][x][i] = 0.f;
       }
     }
+    const int at_scales = ((scale_at + (hb * hbw + hsub0) * 2 * ng) & 15) + warp * 2 * ng;     // of the head, in a token's
     int top_m = Elem<E>::kBf16 ? -64 : -8;               // E: every |M| so far is below 2^E
 
     for (int c = c0; c < c1; ++c) {
+      cp_wait<1>();
+      __syncthreads();             // every thread's copies of this unit have landed, the last unit's are read
+      const uint32_t here = ring + stage * stage_size, my_k = here + warp * R::kCodes, my_v = my_k + at_v, valid2 = issue(next, stage == 0 ? 2 : stage - 1);
       // ---- scores of tokens nn + 8 x
       float s[2 * NS][NR];
 #pragma unroll
       for (int x = 0; x < 2 * NS; x += 2) {
+        uint32_t kf[2][NG], km[2][NG / 2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int t = nn + 8 * (x + z);
+          if constexpr (FULL) {
+            lds<NG>(my_k + t * 16 * NG + kk * 4 * NG, kf[z]);
+          } else {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              uint32_t w[1] = {0u};
+              if (g < ng) lds<1>(my_k + t * 16 * NG + (kk * ng + g) * 4, w);
+              kf[z][g] = w[0];
+            }
+          }
+          token_scales(here + at_ks + t * scale_size + at_scales, km[z]);
+        }
 #pragma unroll
         for (int y = 0; y < NR; ++y) s[x][y] = s[x + 1][y] = 0.f;
+        float acc[NG][4];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float acc[4];
-          const uint32_t w0 = kf[x][g], w1 = kf[x + 1][g], h0 = w0 >> 8, h1 = w1 >> 8;
-          mma16816_from(acc, w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1], c_first[g][0],
-                        c_first[g][NR - 1], c_first[g][0], c_first[g][NR - 1]);
-          mma16816<__half>(acc, w0 & kHigh, w1 & kHigh, h0 & kHigh, h1 & kHigh, qf[g][2], qf[g][3]);
-          const float2 M0 = Elem<E>::to2(km[x][g / 2]), M1 = Elem<E>::to2(km[x + 1][g / 2]);
+          const uint32_t w0 = kf[0][g], w1 = kf[1][g], h0 = w0 >> 8, h1 = w1 >> 8;
+          mma_h(acc[g], w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1], c_first[g][0], c_first[g][NR - 1],
+                c_first[g][0], c_first[g][NR - 1]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t w0 = kf[0][g], w1 = kf[1][g], h0 = w0 >> 8, h1 = w1 >> 8;
+          mma_h(acc[g], w0 & kHigh, w1 & kHigh, h0 & kHigh, h1 & kHigh, qf[g][2], qf[g][3], acc[g][0], acc[g][1], acc[g][2],
+                acc[g][3]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 M0 = Elem<E>::to2(km[0][g / 2]), M1 = Elem<E>::to2(km[1][g / 2]);
 #pragma unroll
           for (int y = 0; y < NR; ++y) {
-            s[x][y] = fmaf(acc[y], g & 1 ? M0.y : M0.x, s[x][y]);
-            s[x + 1][y] = fmaf(acc[2 + y], g & 1 ? M1.y : M1.x, s[x + 1][y]);
+            s[x][y] = fmaf(acc[g][y], g & 1 ? M0.y : M0.x, s[x][y]);
+            s[x + 1][y] = fmaf(acc[g][2 + y], g & 1 ? M1.y : M1.x, s[x + 1][y]);
           }
         }
       }
-      const uint32_t held_all = valid;
-      valid = resolve(next);
-      const int hk_next = next.hk;
-      load_k(hk_next);
-      fetch(next);
       if (CAP) {
 #pragma unroll
         for (int y = 0; y < NR; ++y)
@@ -335,12 +413,12 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           for (int x = 0; x < 2 * NS; ++x) s[x][y] = capped<true>(s[x][y] * fac[y], sc, cap_t, cap2);
       }
       // some token is not there, or after the tile's first row
-      if (held_all != 0xffffffffu || (c + 1) * UNIT > lim_first) {
+      if (valid != 0xffffffffu || (c + 1) * UNIT > lim_first) {
 #pragma unroll
         for (int y = 0; y < NR; ++y)
 #pragma unroll
           for (int x = 0; x < 2 * NS; ++x)
-            if (!(held_all >> (nn + 8 * x) & 1) || c * UNIT + nn + 8 * x >= lim[y]) s[x][y] = -INFINITY;
+            if (!(valid >> (nn + 8 * x) & 1) || c * UNIT + nn + 8 * x >= lim[y]) s[x][y] = -INFINITY;
       }
       float n[NR];
 #pragma unroll
@@ -354,10 +432,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         n[y] = fmaxf(n[y], m[y]);
       }
       // the unit's largest |M|, of any group and token
-      uint32_t bits = 0;
+      uint32_t bits = 0, vm[NG / 2];
+      const uint32_t my_scales = here + at_vs + (lane & (UNIT - 1)) * scale_size + at_scales;
+      token_scales(my_scales, vm);
 #pragma unroll
       for (int g = 0; g < NG / 2; ++g) {
-        if (!(v_tokens >> (lane & (UNIT - 1)) & 1)) vm[g] = 0;
         bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
       }
       bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
@@ -404,22 +483,43 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         const float2 M = Elem<E>::to2(vm[g]);
         vm[g] = Elem<__half>::from2(M.x * m_up, M.y * m_up);
       }
+      __syncwarp();                // (UNIT = 16: two lanes have one token)
+      if constexpr (FULL) {
+        sts<NG / 2>(my_scales, vm);
+      } else {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (g < ng) sts_half(my_scales + 2 * g, g & 1 ? vm[g / 2] >> 16 : vm[g / 2]);
+      }
+      __syncwarp();
+      uint32_t vf[4 * NS][NG / 2];
+#pragma unroll
+      for (int y = 0; y < 4 * NS; ++y) {
+        const int t = (y >> 2) * 16 + 2 * kk + (y & 1) + (y & 2) * 4;
+        if constexpr (FULL) {
+          lds<NG / 2>(my_v + R::v_piece(t, nn * NG / 8) + nn * 2 * NG % 16, vf[y]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const int at = (nn * ng + g) * 2;
+            const uint32_t h = g < ng ? lds_half(my_v + R::v_piece(t, at >> 4) + (at & 15)) : 0u;
+            vf[y][g / 2] = g & 1 ? vf[y][g / 2] | h << 16 : h;
+          }
+        }
+      }
 #pragma unroll
       for (int ps = 0; ps < PASS; ++ps) {
         uint32_t bh[2 * NS], bl[2 * NS];
 #pragma unroll
         for (int x = 0; x < 2 * NS; ++x) {
-          const int src = (nn + 8 * x) & (UNIT - 1);
-          uint32_t w;                                    // the scales of the lane's two columns
-          if constexpr (RT == 8) {
-            w = __shfl_sync(0xffffffffu, vm[ps / 2], src);
-            w = __byte_perm(w, w, ps & 1 ? 0x3232 : 0x1010);
-          } else if constexpr (RT == 4) {
-            w = __shfl_sync(0xffffffffu, vm[ps], src);
-          } else {
-            const uint32_t w0 = __shfl_sync(0xffffffffu, vm[2 * ps], src), w1 = __shfl_sync(0xffffffffu, vm[2 * ps + 1], src);
-            w = kk & 1 ? w1 : w0;
-          }
+          // the scales of the lane's two columns
+          uint32_t w1[1];
+          if constexpr (!FULL) {
+            // (RT is 8: one group's scale, perhaps in the middle of a word)
+            const uint32_t h = ps < ng ? lds_half(here + at_vs + (nn + 8 * x) * scale_size + at_scales + ps * 2) : 0u;
+            w1[0] = h | h << 16;
+          } else lds<1>(here + at_vs + (nn + 8 * x) * scale_size + at_scales + (RT == 8 ? ps / 2 : RT == 4 ? ps : 2 * ps + (kk & 1)) * 4, w1);
+          const uint32_t w = RT == 8 ? __byte_perm(w1[0], w1[0], ps & 1 ? 0x3232 : 0x1010) : w1[0];
           const float2 mf = Elem<__half>::to2(w);
           if constexpr (RT == 8) {
             lg[ps][0] = fmaf(p[x][0], mf.x, lg[ps][0]);
@@ -442,15 +542,18 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             const uint32_t ta = __byte_perm(vf[4 * s2][g / 2], vf[4 * s2 + 1][g / 2], sel);
             const uint32_t tb = __byte_perm(vf[4 * s2 + 2][g / 2], vf[4 * s2 + 3][g / 2], sel);
             const uint32_t ua = ta >> 8, ub = tb >> 8;
-            if (s2 == 0) {
-              mma16816_from(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[0], bh[1], 0.f, 0.f, 0.f, 0.f);
-              mma16816_from(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[0], bh[1], 0.f, 0.f, 0.f, 0.f);
-            } else {
-              mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bh[2 * s2], bh[2 * s2 + 1]);
-              mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bh[2 * s2], bh[2 * s2 + 1]);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const uint32_t b0 = part ? bl[2 * s2] : bh[2 * s2], b1 = part ? bl[2 * s2 + 1] : bh[2 * s2 + 1];
+              if (s2 == 0 && part == 0) {
+                mma_h(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, b0, b1, 0.f, 0.f, 0.f, 0.f);
+                mma_h(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, b0, b1, 0.f, 0.f, 0.f, 0.f);
+              } else {
+                float(&c0)[4] = acc[gi][0], (&c1)[4] = acc[gi][1];
+                mma_h(c0, ta & kLow, ua & kLow, tb & kLow, ub & kLow, b0, b1, c0[0], c0[1], c0[2], c0[3]);
+                mma_h(c1, ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, b0, b1, c1[0], c1[1], c1[2], c1[3]);
+              }
             }
-            mma16816<__half>(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, bl[2 * s2], bl[2 * s2 + 1]);
-            mma16816<__half>(acc[gi][1], ta & kHigh, ua & kHigh, tb & kHigh, ub & kHigh, bl[2 * s2], bl[2 * s2 + 1]);
           }
           // element i of the lane's four: i / 2 the accumulator's row, i % 2 which of the two
           if constexpr (RT == 8) {
@@ -471,7 +574,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
               o[2 * ps + j][0][i] += kk & 1 ? acc[2 % GC + j][i & 1][(i & 2) + j] : acc[j % GC][i & 1][(i & 2) + j];
         }
       }
-      load_v(hk_next, valid);
+      valid = valid1;
+      valid1 = valid2;
+      stage = stage == R::kStages - 1 ? 0 : stage + 1;
     }
 #pragma unroll
     for (int y = 0; y < NR; ++y) {
@@ -492,7 +597,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       uint16_t* dst = a.out + (int64_t)dbg_index(q0 + row / group, a.T, d.error) * a.ldo +
                       (int64_t)(hk * group + row % group) * dim;
       // slot 0: the segment began in an earlier run; slot 1: it begins here
-      const int64_t part = (gw * 2 + (c0 == 0 ? 1 : 0)) * kKvRowTile + row - rt * kKvRowTile;
+      const int64_t part = (((int64_t)grp * hbw + hsub) * 2 + (c0 == 0 ? 1 : 0)) * kKvRowTile + row - rt * kKvRowTile;
 #pragma unroll
       for (int gi = 0; gi < NO; ++gi) {
         const int g = RT == 2 ? gi / 2 * 4 + 2 * (kk & 1) + gi % 2 : gi, e = 32 * g + 4 * nn;
@@ -519,24 +624,31 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
   }
+  cp_wait<0>();
   if (missing) report_err(d.error, kErrInvalid);
   // after chunks: their kernel may still run, and this grid ends after it
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <class E, int NG, int RT, bool FULL = true>
-cudaError_t launch_rows(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
-  const int grid = num_sms * q4_ctas(NG);
+cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStream_t st) {
+  // heads of a CTA, and as many neighbouring ones at a time as up to 16 that several CTAs share
+  int heads = kMaxAbreast;
+  while (a.kv.heads_kv % heads) --heads;
+  a.hbw = std::max(1, 16 / heads) * heads;
+  while (a.kv.heads_kv % a.hbw) a.hbw -= heads;
+  const int grid = num_sms * (q4_warps(NG) / heads), smem = Ring<NG>::kStages * stage_bytes<NG>(heads, a.kv.groups);
+  const int threads = heads * 32;
   auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true, FULL> : kv_q4_decode_kernel<E, NG, RT, false, FULL>;
   cudaError_t e;
   if (after_chunks) {
-    e = launch_early(kernel, dim3(grid), kDecThreads, st, a);
+    e = launch_early(kernel, dim3(grid), threads, smem, st, a);
   } else {
-    kernel<<<grid, kDecThreads, 0, st>>>(a);
+    kernel<<<grid, threads, smem, st>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_kv_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, (int64_t)grid * kDecWarps / a.hbw, st);
+  return launch_kv_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, grid / (a.hbw / heads), st);
 }
 template <class E>
 cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
@@ -555,9 +667,9 @@ cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks,
 
 template <class E, int NG, int RT, bool FULL = true>
 cudaError_t prepare() {
-  // all of the SM's memory as first-level cache (attend.cu)
   for (auto k : {kv_q4_decode_kernel<E, NG, RT, false, FULL>, kv_q4_decode_kernel<E, NG, RT, true, FULL>})
-    if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1))
+    if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Ring<NG>::kStages * stage_bytes<NG>(kMaxAbreast, NG) + 1024))
       return e;
   return cudaSuccess;
 }
@@ -576,9 +688,7 @@ cudaError_t prepare_kv_q4_decode_kernels() {
   return prepare_all<__nv_bfloat16>();
 }
 
-cudaError_t launch_kv_q4_decode(const KvAttendArgs& args, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
-  KvAttendArgs a = args;
-  a.hbw = heads_abreast(a.kv.heads_kv);
+cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
   return dtype == 0 ? launch_decode<__half>(a, num_sms, after_chunks, st)
                     : launch_decode<__nv_bfloat16>(a, num_sms, after_chunks, st);
 }
