@@ -19,9 +19,9 @@ LIB = os.path.join(HERE, "libslora.so")
 OBJ_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libslora_debug.so")
 SOURCES = ["pool.cpp", "kernels.cu", "tc_kernels.cu", "noalloc.cu", "bmm.cu", "kv.cpp", "kv.cu", "kv_q4.cu",
-           "attend.cu", "attend_tc.cu", "attend_q4.cu"]
+           "attend.cu", "attend_tc.cu", "attend_q4.cu", "attend_tc_q4.cu"]
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "kv.h"),
-           os.path.join(CSRC, "kv.cuh"), os.path.join(CSRC, "append.cuh"), os.path.join(CSRC, "attend.cuh"),
+           os.path.join(CSRC, "kv.cuh"), os.path.join(CSRC, "append.cuh"), os.path.join(CSRC, "attend.cuh"), os.path.join(CSRC, "attend_tc.cuh"),
            os.path.join(CSRC, "kv_q4.cuh"),
            os.path.join(ROOT, "include", "slora.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -400,9 +400,10 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
     const int off = __ldg(d.dec_off + r), off_next = __ldg(d.dec_off + r + 1);
     const int rows = rq.y * group;
     if (row >= rows || off == off_next) continue;         // no such row, or a chunk
-    const int nchunk = (rq.z + d.unit - 1) >> (31 - __clz(d.unit)), tiles = (rows + kKvRowTile - 1) / kKvRowTile, n = row % kKvRowTile;
+    const int nchunk = (rq.z + d.unit - 1) >> (31 - __clz(d.unit)), tiles = (rows + a.row_tile - 1) / a.row_tile, rt = row / a.row_tile,
+              n = row - rt * a.row_tile;
     const int hb = hk / hbw, hsub = hk - hb * hbw;
-    const int64_t us = (int64_t)off * blocks + (int64_t)(hb * tiles + row / kKvRowTile) * nchunk;
+    const int64_t us = (int64_t)off * blocks + (int64_t)(hb * tiles + rt) * nchunk;
     const int64_t g0 = us / sp.run, g1 = (us + nchunk - 1) / sp.run;
     if (g0 == g1) continue;                               // the decode kernel wrote it
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -507,7 +508,7 @@ cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, i
   const int64_t items = (int64_t)a.R * a.rows * a.kv.heads_kv;
   // segments of 16 parts or more on average: a block each (a 131072-token
   // context, 228 parts a row: 24 us with a warp each, 8 with a block)
-  const int64_t segments = (int64_t)a.R * ((a.rows + kKvRowTile - 1) / kKvRowTile) * (a.kv.heads_kv / a.hbw);
+  const int64_t segments = (int64_t)a.R * ((a.rows + a.row_tile - 1) / a.row_tile) * (a.kv.heads_kv / a.hbw);
   if (segments * 16 <= groups)
     return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
                         kJoinWideWarps * 32, 0, st, a, groups);

@@ -170,7 +170,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   auto f_open = [&](const int4& rq) {
     f.len = rq.z;
     f.n = (rq.z + UNIT - 1) / UNIT;
-    f.tiles = (rq.y * group + kKvRowTile - 1) / kKvRowTile;
+    f.tiles = (rq.y * group + RT - 1) / RT;
     f.tab = d.table + 2 * a.layer * plane + (int64_t)dbg_index(rq.w, d.max_rows, d.error) * d.max_blocks;
   };
   auto no_units = [&](const int4& rq) {
@@ -281,7 +281,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     int4 rq = __ldg(d.req + r);
     while (no_units(rq)) rq = __ldg(d.req + ++r);
     const int len = rq.z, q0 = rq.x, rows = rq.y * group;
-    const int nchunk = (len + UNIT - 1) / UNIT, tiles = (rows + kKvRowTile - 1) / kKvRowTile;
+    const int nchunk = (len + UNIT - 1) / UNIT, tiles = (rows + RT - 1) / RT;
     const int c1 = min(nchunk, c0 + left);
     const int hk = hb * hbw + hsub;
     const int ctx = len - rq.y;
@@ -290,7 +290,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     uint32_t qf[NG][4];
     float c_first[NG][NR], fac[NR];
     {
-      const int row = rt * kKvRowTile + nn / GC;
+      const int row = rt * RT + nn / GC;
       const bool in = row < rows;
       const uint16_t* src = a.q + (int64_t)dbg_index(q0 + (in ? row / group : 0), a.T, d.error) * a.ldq +
                             (int64_t)(hk * group + (in ? row % group : 0)) * dim;
@@ -335,11 +335,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       for (int x2 = 0; x2 < NR; ++x2) fac[x2] = __shfl_sync(0xffffffffu, down, (2 * kk + x2) * 4);
     }
     // keys that this lane's rows may see: positions below lim
-    const int my_row = rt * kKvRowTile + 2 * kk / GC;
+    const int my_row = rt * RT + 2 * kk / GC;
     int lim[NR];
 #pragma unroll
     for (int x = 0; x < NR; ++x) lim[x] = ctx + min(my_row + x, rows - 1) / group + 1;
-    const int lim_first = ctx + rt * kKvRowTile / group + 1;       // of the tile's first row
+    const int lim_first = ctx + rt * RT / group + 1;       // of the tile's first row
 
     // results: elements 32 g + 4 nn + i of the lane's groups and rows; sums of p M a group
     float o[NO][NR][4], lg[NO][NR], m[NR], l[NR];
@@ -597,7 +597,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       uint16_t* dst = a.out + (int64_t)dbg_index(q0 + row / group, a.T, d.error) * a.ldo +
                       (int64_t)(hk * group + row % group) * dim;
       // slot 0: the segment began in an earlier run; slot 1: it begins here
-      const int64_t part = (((int64_t)grp * hbw + hsub) * 2 + (c0 == 0 ? 1 : 0)) * kKvRowTile + row - rt * kKvRowTile;
+      const int64_t part = (((int64_t)grp * hbw + hsub) * 2 + (c0 == 0 ? 1 : 0)) * kKvRowTile + row - rt * RT;
 #pragma unroll
       for (int gi = 0; gi < NO; ++gi) {
         const int g = RT == 2 ? gi / 2 * 4 + 2 * (kk & 1) + gi % 2 : gi, e = 32 * g + 4 * nn;
@@ -652,17 +652,18 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
 }
 template <class E>
 cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
-  const int ng = a.kv.groups;
-  if (ng == 1) return launch_rows<E, 2, 8, false>(a, num_sms, after_chunks, st);
-  if (ng == 3) return launch_rows<E, 4, 8, false>(a, num_sms, after_chunks, st);
-  if (ng > 4 && ng < 8) return launch_rows<E, 8, 8, false>(a, num_sms, after_chunks, st);
-  if (ng <= 2)
-    return a.rows <= 4 ? launch_rows<E, 2, 4>(a, num_sms, after_chunks, st) : launch_rows<E, 2, 8>(a, num_sms, after_chunks, st);
-  if (ng <= 4)
-    return a.rows <= 2   ? launch_rows<E, 4, 2>(a, num_sms, after_chunks, st)
-           : a.rows <= 4 ? launch_rows<E, 4, 4>(a, num_sms, after_chunks, st)
-                         : launch_rows<E, 4, 8>(a, num_sms, after_chunks, st);
-  return a.rows <= 2 ? launch_rows<E, 8, 2>(a, num_sms, after_chunks, st) : launch_rows<E, 8, 8>(a, num_sms, after_chunks, st);
+  const int ng = a.kv.groups, rt = a.row_tile;       // kv_q4_row_tile
+  switch (ng) {
+    case 1: return launch_rows<E, 2, 8, false>(a, num_sms, after_chunks, st);
+    case 2: return rt == 4 ? launch_rows<E, 2, 4>(a, num_sms, after_chunks, st) : launch_rows<E, 2, 8>(a, num_sms, after_chunks, st);
+    case 3: return launch_rows<E, 4, 8, false>(a, num_sms, after_chunks, st);
+    case 4:
+      return rt == 2   ? launch_rows<E, 4, 2>(a, num_sms, after_chunks, st)
+             : rt == 4 ? launch_rows<E, 4, 4>(a, num_sms, after_chunks, st)
+                       : launch_rows<E, 4, 8>(a, num_sms, after_chunks, st);
+    case 8: return rt == 2 ? launch_rows<E, 8, 2>(a, num_sms, after_chunks, st) : launch_rows<E, 8, 8>(a, num_sms, after_chunks, st);
+    default: return launch_rows<E, 8, 8, false>(a, num_sms, after_chunks, st);
+  }
 }
 
 template <class E, int NG, int RT, bool FULL = true>

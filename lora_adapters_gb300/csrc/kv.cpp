@@ -178,6 +178,18 @@ bool overlap(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t col
   return (off < cols && std::abs(rows) < T) || (ldp - off < cols && std::abs(rows + 1) < T);
 }
 
+// Rows (token, head of the group) that a request of a batch has at most.
+int64_t most_rows(const slora_kv* kv, int32_t T, int32_t max_new) {
+  return (int64_t)std::min(max_new, T) * (kv->dev.heads_q / kv->dev.heads_kv);
+}
+// Chunks are possible where one request may bring more than kKvChunkRows rows.
+bool may_chunk(const slora_kv* kv, int64_t rows) { return kv->tpt > 0 && rows > kKvChunkRows; }
+int32_t row_tile(const slora_kv* kv, int32_t T, int32_t max_new) {
+  const int64_t rows = most_rows(kv, T, max_new);
+  return kv->dev.groups ? kv_q4_row_tile(kv->dev.groups, kv->dev.heads_q / kv->dev.heads_kv, rows, may_chunk(kv, rows))
+                        : kKvRowTile;
+}
+
 int array_ints(const slora_pool* pool, const slora_kv_config* c, bool q4, int64_t* n) {
   if (!n) return fail(SLORA_ERR_INVALID, "n is NULL");
   PoolView pv;
@@ -212,9 +224,9 @@ int create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, bool q4, 
     const int64_t parts = kv_attend_parts(pv.num_sms);
     CUDA_TRY(cudaMalloc(&kv->d_part_o, sizeof(float) * (size_t)parts * (size_t)kv_attend_cols(c->head_dim)));
     CUDA_TRY(cudaMalloc(&kv->d_part_ml, sizeof(float2) * (size_t)parts));
-    kv->tpt = q4 ? 0 : kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
+    kv->tpt = kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
     if (kv->tpt > 0) {
-      CUDA_TRY(prepare_kv_chunk_kernels());
+      CUDA_TRY(q4 ? prepare_kv_q4_chunk_kernels() : prepare_kv_chunk_kernels());
       const int64_t rows = kv_chunk_part_rows(pv.num_sms);
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_o, sizeof(float) * (size_t)rows * kKvTile));
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_ml, sizeof(float2) * (size_t)rows));
@@ -328,6 +340,7 @@ int slora_kv_plan(slora_kv* kv, int32_t R, const int32_t* d_row, const int32_t* 
   a.T = T;
   a.max_new = max_new;
   a.tpt = kv->tpt;
+  a.row_tile = row_tile(kv, T, max_new);
   a.per_page_div = kv->per_page_div;
   a.row = d_row;
   a.ctx = d_ctx;
@@ -403,9 +416,8 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   if (!std::isfinite(softcap) || softcap < 0.f) return fail(SLORA_ERR_INVALID, "softcap must be finite and >= 0");
   if (kv->T == 0 || kv->R == 0 || kv->max_new == 0) return SLORA_OK;   // no request can have a row
   const int32_t group = kv->dev.heads_q / kv->dev.heads_kv;
-  const int64_t rows = (int64_t)std::min(kv->max_new, kv->T) * group;     // of one key head in one request
-  // chunks are possible where one request may bring more than kKvChunkRows rows
-  const bool chunks = kv->tpt > 0 && rows > kKvChunkRows;
+  const int64_t rows = most_rows(kv, kv->T, kv->max_new);
+  const bool chunks = may_chunk(kv, rows);
   if (!chunks && rows * kv->dev.heads_kv > INT32_MAX)
     return fail(SLORA_ERR_INVALID, "max_new * heads_q = %lld is 2^31 or more", (long long)rows * kv->dev.heads_kv);
   const int64_t wq = (int64_t)kv->dev.heads_q * kv->dev.head_dim;
@@ -433,6 +445,7 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
   a.tc_split = kv->d_tc_split;
   a.per_page_div = kv->per_page_div;
   a.tpt = kv->tpt;
+  a.row_tile = row_tile(kv, kv->T, kv->max_new);
   a.tc_part_o = kv->d_tc_part_o;
   a.tc_part_ml = kv->d_tc_part_ml;
   a.rows = chunks ? kKvChunkRows : (int32_t)rows;
@@ -443,7 +456,9 @@ int slora_kv_attend(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
     if (int rc = encode_map(&a.q_map, d_q, kv->pv.dtype, 3, dims, strides, box)) return rc;
   }
   KvTimed tm(kv->pool, kKvTimerAttend);
-  if (chunks) CUDA_TRY(launch_kv_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  if (chunks)
+    CUDA_TRY(kv->dev.groups ? launch_kv_q4_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute)
+                            : launch_kv_chunk(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
   CUDA_TRY(kv->dev.groups ? launch_kv_q4_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute)
                           : launch_kv_decode(a, kv->pv.dtype, kv->pv.num_sms, chunks, kv->pv.compute));
   tm.done();

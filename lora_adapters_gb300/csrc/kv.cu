@@ -68,7 +68,7 @@ __device__ __forceinline__ void plan_work(const KvPlanArgs& a, int fresh, int ct
     if (fresh % step) n += kKvPairUnits + (len + kKvTile - 1) / kKvTile;
     *tc = (int32_t)min(n, (int64_t)0x7fffffff);
   } else {
-    *dec = (int32_t)min((rows + kKvRowTile - 1) / kKvRowTile * (((int64_t)len + a.kv.unit - 1) / a.kv.unit), (int64_t)0x7fffffff);
+    *dec = (int32_t)min((rows + a.row_tile - 1) / a.row_tile * (((int64_t)len + a.kv.unit - 1) / a.kv.unit), (int64_t)0x7fffffff);
   }
 }
 

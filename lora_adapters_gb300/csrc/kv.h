@@ -25,6 +25,16 @@ constexpr int kKvTile = 128;           // rows and keys of one chunk tile
 // tokens 368 us against 693, one of 131072 154 against 194, one of 640 14.7
 // against 12.3.
 constexpr int kKvChunkRows = kKvRowTile;
+// Rows of a decode segment of a 4-bit cache, for a call in which no request has more than
+// `rows` of them: the kernel works a token's weights out 8 / (rows of a tile) times less
+// often with tiles of 2 or 4 (attend_q4.cu).  With chunks in the call the other requests may have
+// up to kKvChunkRows, but mostly have one new token, `group` rows.
+inline int32_t kv_q4_row_tile(int32_t groups, int32_t group, int64_t rows, bool chunks) {
+  const int64_t most = chunks ? group : rows;
+  if (groups % 2 || groups == 6 || most > 4) return kKvRowTile;
+  if (groups == 2) return 4;
+  return most <= 2 ? 2 : groups == 4 ? 4 : kKvRowTile;
+}
 // What a pair of chunk tiles costs besides its key tiles (queries in, results
 // out, the first scores waited for), in key tiles' time: about 6,000 cycles
 // against 3,000.  Counted with them, the runs of CTAs with many short prompts
@@ -91,6 +101,7 @@ struct KvPlanArgs {
   KvDev kv;
   int32_t R, T, max_new;
   int32_t tpt;                   // kv_chunk_tokens
+  int32_t row_tile;              // rows of a decode segment
   int32_t tile;                  // tokens a CTA takes at a time (set by the launcher)
   FastDiv per_page_div;
   const int32_t* row;            // NULL: request r has row r
@@ -144,6 +155,7 @@ struct KvAttendArgs {
   float2* part_ml;               // [kv_attend_parts] their maximum (in powers of two) and sum
   int32_t hbw;                   // neighbouring key heads worked on side by side
   int32_t rows;                  // rows (token, head of the group) a request has at most in the decode kernel
+  int32_t row_tile;              // rows of a decode segment
   FastDiv per_page_div;
   // chunk kernel
   int32_t tpt;                   // kv_chunk_tokens
@@ -162,6 +174,8 @@ int32_t kv_attend_cols(int32_t head_dim);
 // The decode kernel (after_chunks: while the chunk kernel launched before it
 // still runs), and the joins of what either kernel split.
 cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
+cudaError_t prepare_kv_q4_chunk_kernels();
+cudaError_t launch_kv_q4_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 // The joins alone, of what `groups` groups of warps split.
 cudaError_t launch_kv_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
                            cudaStream_t st);
