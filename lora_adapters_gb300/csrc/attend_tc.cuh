@@ -288,41 +288,7 @@ struct TcSmem {
 // The four warps of a 4-bit cache.  Warp w fills rows 32 w .. 32 w + 31 of a tile, four lanes
 // a row, eight rows at a time: a lane loads its share of every group with one load, 8
 // consecutive elements each, and writes each as 16 bytes.  A row's neighbours in the warp
-// are four rows apart, so that eight lanes' pieces lie in different banks.  Codes become
-// numbers in two steps, both exact: k = c - 7 (from 1024 + c, or 128 + c in bf16, which is
-// the code with the exponent's bits around it), then k M / 8.
-template <class E>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  if constexpr (Elem<E>::kBf16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-template <class E>
-__device__ __forceinline__ uint32_t fma2x16(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t y;
-  if constexpr (Elem<E>::kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
-  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
-  return y;
-}
-// The codes in bits 0-3, 4-7, 8-11 and 12-15 of both halves of w, as pairs of numbers; s =
-// M / 8 twice.
-template <class E>
-__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t s, uint32_t (&y)[4]) {
-  if constexpr (Elem<E>::kBf16) {
-    constexpr uint32_t kBase = 0x43004300u, kOne = 0x3f803f80u, kOff = 0xc307c307u;     // 128, 1, -135
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2<E>(fma2x16<E>((w >> 4 * i & 0x000f000fu) | kBase, kOne, kOff), s);
-  } else {
-    constexpr uint32_t kBase = 0x64006400u, kOne = 0x3c003c00u, kOff = 0xe407e407u;     // 1024, 1, -1031
-    constexpr uint32_t kSixteenth = 0x2c002c00u, kOff16 = 0xd470d470u;                  // 1 / 16, -71
-    const uint32_t h = w >> 8;
-    y[0] = mul2<E>(fma2x16<E>((w & 0x000f000fu) | kBase, kOne, kOff), s);
-    y[1] = mul2<E>(fma2x16<E>((w & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
-    y[2] = mul2<E>(fma2x16<E>((h & 0x000f000fu) | kBase, kOne, kOff), s);
-    y[3] = mul2<E>(fma2x16<E>((h & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
-  }
-}
+// are four rows apart, so that eight lanes' pieces lie in different banks.
 template <class E, int NG, class Wait, class Next, class Read>
 __device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool& ok, int warp, int lane, Wait wait_warp,
                                         Next next_part, Read part_read) {
@@ -368,27 +334,7 @@ __device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool&
         for (int g = 0; g < NG; ++g) t.w[j][g] = 0;
 #pragma unroll
         for (int g = 0; g < kM; ++g) t.m[j][g] = 0;
-        if (r) {
-          const uint8_t *c = r + kk * 4 * NG, *m = r + scales;
-          if constexpr (NG == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(c));
-            t.w[j][0] = x.x; t.w[j][1] = x.y; t.w[j][2] = x.z; t.w[j][3] = x.w;
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(m));
-            t.m[j][0] = y.x; t.m[j][1] = y.y;
-          } else if constexpr (NG == 2) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(c));
-            t.w[j][0] = x.x; t.w[j][1] = x.y;
-            t.m[j][0] = __ldg(reinterpret_cast<const uint32_t*>(m));
-          } else {
-            const uint32_t* cw = reinterpret_cast<const uint32_t*>(c);
-            const uint16_t* mh = reinterpret_cast<const uint16_t*>(m);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              t.w[j][g] = __ldg(cw + g);
-              t.m[j][g / 2] |= (uint32_t)__ldg(mh + g) << 16 * (g & 1);
-            }
-          }
-        }
+        if (r) q4_load<NG>(r + kk * 4 * NG, r + scales, t.w[j], t.m[j]);
       }
     };
     auto store = [&](const Tile& t, uint32_t st, bool v) {
@@ -397,21 +343,8 @@ __device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool&
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint32_t eighth = Elem<E>::kBf16 ? 0x3e003e00u : 0x30003000u;
-          const uint32_t s = mul2<E>(__byte_perm(t.m[j][g / 2], 0, g & 1 ? 0x3232 : 0x1010), eighth);
           uint32_t y[4];
-          if (v) {
-            // halfwords 2 kk NG + g and (2 kk + 1) NG + g: elements 0-3 and 4-7 of the eight
-            constexpr int kOdd = NG & 1;
-            const uint32_t lo = t.w[j][g / 2], hi = t.w[j][(NG + g) / 2];
-            const uint32_t sel = (g & 1 ? 0x32 : 0x10) | ((g + kOdd) & 1 ? 0x7600 : 0x5400);
-            uint32_t x[4];
-            q4_pairs<E>(__byte_perm(lo, hi, sel), s, x);
-            y[0] = __byte_perm(x[0], x[1], 0x5410); y[1] = __byte_perm(x[2], x[3], 0x5410);
-            y[2] = __byte_perm(x[0], x[1], 0x7632); y[3] = __byte_perm(x[2], x[3], 0x7632);
-          } else {
-            q4_pairs<E>(t.w[j][g], s, y);
-          }
+          q4_eight<E, NG>(t.w[j], t.m[j], g, v, y);
           const int ch = 4 * g + kk;           // 16-byte piece of the row
           const uint32_t to = dst + 8 * j * kRowBytes + (ch >> 3) * kAtom + (((ch & 7) ^ sub) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])

@@ -494,7 +494,7 @@ int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, 
   a.ldv = ldv;
   a.per_page_div = kv->per_page_div;
   KvTimed tm(kv->pool, kKvTimerRead);
-  CUDA_TRY(launch_kv_read(a, kv->pv.dtype, kv->pv.num_sms, kv->pv.compute));
+  CUDA_TRY(launch_kv_read(a, kv->pv.dtype, kv->pv.compute));
   tm.done();
   return SLORA_OK;
 }

@@ -140,7 +140,7 @@ struct KvReadArgs {
   int64_t ldk, ldv;
   FastDiv per_page_div;
 };
-cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, int num_sms, cudaStream_t st);
+cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, cudaStream_t st);
 
 struct KvAttendArgs {
   KvDev kv;

@@ -22,98 +22,132 @@ namespace {
 //    border (2n + 1) M / 16 at most 9, so the two are equal or at least 2^-11 of the
 //    border apart.  t = 8 x / M evaluated with an error below 2^-18 and raised by
 //    2^-15 then rounds to the right integer, ties upwards;
-//  - a normed or rotated key has an error of at most kErr times the head's largest
-//    element (cosine and sine 2^-22, two products and a sum; the pair's length is at
-//    most sqrt(2) times that element; the norm's factor 2^-21).  Where that could
-//    change a code, M's rounding or the choice between the two signs, the warp
-//    works the elements in question out again in fp64 (requantise: about one head in
-//    200).
+//  - a rotated key has an error of at most 2^-20.7 of the head's largest element (angle
+//    2^-23.3, cosine and sine 2^-24 more, mscale's product 2^-24: 2^-22.1 each, times the
+//    sum of two elements, at most twice the largest rotated one; a product's and a sum's
+//    rounding), a normed one of 2^-19.6 (every element's factor 2^-23, the norm's
+//    2^-20.9: nine roundings of the sum of squares, halved, and the root's two units).  Where
+//    that could change a code, M's rounding or the choice between the two signs, the warp
+//    works the elements in question out again in fp64 (exact_scale, exact_codes).
 constexpr int kAppendThreads = 256;
-constexpr float kErr = 0x1p-19f;
+constexpr float kErrTurned = 0x1.6p-21f, kErrNormed = 0x1.6p-20f;     // 2^-20.5, 2^-19.5
 
-// What requantise needs of a lane.
+// What the two need of a lane.
 struct Exact {
   const uint64_t* freq;
   int64_t pos;
   float mscale, eps;
-  int head_dim, half;            // half: lanes between the halves of the half layout
+  double inv_d;                  // 1 / head_dim
+  int half;                      // lanes between the halves of the half layout
 };
 
-// The group's codes (packed as K's) and M in fp64 where they are in question: `need`
-// has a bit for each of the lane's elements, all of them set where M is.  By a whole
-// warp; r: the lane's raw elements, w: its weights.
+// Element e of eight packed in r.
+template <class E>
+__device__ __forceinline__ float element(const uint4& r, int e) {
+  const uint32_t w = e & 4 ? (e & 2 ? r.w : r.z) : (e & 2 ? r.y : r.x);
+  return Elem<E>::to((uint16_t)(e & 1 ? w >> 16 : w));
+}
+
+// Normed and rotated elements in fp64, by a whole warp; r: the lane's raw elements, w: its
+// weights.  One element at a time, the same of every lane: the calls below ask for few, and
+// what unrolled code costs first is its fetch (256 tokens of 96 heads 29 us, 14 as it is).
 template <class E, bool NORM, bool INTER, int G>
-__device__ __noinline__ uint2 requantise(const Exact ex, uint4 r, const float* w, uint32_t need, bool scale_too, float M,
-                                         uint32_t word) {
-  const int lane = threadIdx.x & 31, li = lane & (G - 1);
-  const int pl = li < ex.half ? li + ex.half : li - ex.half;
-  const bool turned = li < 2 * ex.half;
-  const int partner = (lane & ~(G - 1)) | (turned ? pl : li);
-  float own[8], other[8];
-  unpack8<E>(r, own);
-  if (!INTER) {
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, r.x, partner);
-    o.y = __shfl_sync(0xffffffffu, r.y, partner);
-    o.z = __shfl_sync(0xffffffffu, r.z, partner);
-    o.w = __shfl_sync(0xffffffffu, r.w, partner);
-    unpack8<E>(o, other);
-  }
+struct Turned {
+  const Exact& ex;
+  const float* w;
+  const float* wo;               // the partner's weights
+  uint4 r, o;                    // own and partner's raw elements
   double rs = 1.0;
-  if (NORM) {
-    double ss = 0.0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss += (double)own[e] * own[e];
-#pragma unroll
-    for (int o = G >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    rs = 1.0 / sqrt(ss / ex.head_dim + (double)ex.eps);
-  }
-  double x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = own[e];
-    if (!__any_sync(0xffffffffu, (need >> e) & 1)) continue;
-    const int partner_e = INTER ? e ^ 1 : e;
-    double a = own[e], b = INTER ? own[partner_e] : other[e];
-    if (NORM) {                                    // (x w exactly: equal magnitudes stay equal)
-      a = a * w[e] * rs;
-      b = b * (INTER ? w[partner_e] : w[((turned ? pl : li) - li) * 8 + e]) * rs;
+  int li, first_pair;
+  bool turned, lower;
+
+  __device__ __forceinline__ Turned(const Exact& x, const uint4& raw, const float* weights) : ex(x), w(weights), r(raw), o(raw) {
+    const int lane = threadIdx.x & 31;
+    li = lane & (G - 1);
+    const int pl = li < ex.half ? li + ex.half : li - ex.half;
+    turned = li < 2 * ex.half;
+    lower = li < ex.half;
+    first_pair = INTER ? li * 4 : (lower ? li : pl) * 8;
+    wo = INTER || !turned ? w : w + (pl - li) * 8;
+    if (!INTER) {
+      const int partner = (lane & ~(G - 1)) | (turned ? pl : li);
+      o.x = __shfl_sync(0xffffffffu, r.x, partner);
+      o.y = __shfl_sync(0xffffffffu, r.y, partner);
+      o.z = __shfl_sync(0xffffffffu, r.z, partner);
+      o.w = __shfl_sync(0xffffffffu, r.w, partner);
     }
-    x[e] = a;
-    if (turned) {
-      const int pi = INTER ? li * 4 + e / 2 : (li < ex.half ? li : pl) * 8 + e;
-      double c, s;
-      sincospi((double)(int64_t)((uint64_t)ex.pos * ex.freq[pi]) * 0x1p-63, &s, &c);
-      const bool first = INTER ? (e & 1) == 0 : li < ex.half;
-      x[e] = (a * c + (first ? -b : b) * s) * (double)ex.mscale;
-    }
-  }
-  if (__any_sync(0xffffffffu, scale_too)) {
-    double hi = x[0], lo = x[0];
+    if (NORM) {
+      // squares of 16-bit numbers are exact in fp32; 1 / sqrt(v) from fp32's 22 bits by two
+      // of Newton's steps, y <- y (3 - v y^2) / 2, each of which doubles them
+      float v[8];
+      unpack8<E>(r, v);
+      double s0 = 0.0, s1 = 0.0;
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      hi = fmax(hi, x[e]);
-      lo = fmin(lo, x[e]);
-    }
+      for (int e = 0; e < 8; e += 2) {
+        s0 += (double)(v[e] * v[e]);
+        s1 += (double)(v[e + 1] * v[e + 1]);
+      }
+      double ss = s0 + s1;
+#pragma unroll 1
+      for (int x2 = G >> 1; x2; x2 >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x2);
+      ss = fma(ss, ex.inv_d, (double)ex.eps);
+      rs = (double)rsqrtf((float)ss);
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    }
-    if (scale_too && M == M) {                     // (a group that is not finite stays so)
-      const double m = hi >= -lo ? hi : lo;
-      M = copysignf(q4_scale<E>(__double2float_ru(fabs(m))), (float)m);   // (upwards, as M itself)
+      for (int i = 0; i < 2; ++i) rs = rs * fma(-0.5 * ss * rs, rs, 1.5);
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if ((need >> e) & 1) {
-      const double k = M == 0.f ? 0.0 : fmin(fmax(floor(8.0 * x[e] / (double)M + 0.5), -7.0), 8.0);
+  __device__ __forceinline__ double operator()(int e) const {
+    double x = element<E>(r, e);
+    if (NORM) x = x * w[e] * rs;                   // (x w exactly: equal magnitudes stay equal)
+    if (!turned) return x;
+    const int pe = INTER ? e ^ 1 : e;
+    double b = INTER ? element<E>(r, pe) : element<E>(o, pe), c, s;
+    if (NORM) b = b * wo[pe] * rs;
+    sincospi((double)(int64_t)((uint64_t)ex.pos * ex.freq[first_pair + (INTER ? e / 2 : e)]) * 0x1p-63, &s, &c);
+    return (x * c + ((INTER ? (e & 1) == 0 : lower) ? -b : b) * s) * (double)ex.mscale;
+  }
+};
+
+// M of the lane's group, from those of its elements that may be the largest (a bit each).
+template <class E, bool NORM, bool INTER, int G>
+__device__ __noinline__ float exact_scale(const Exact ex, uint4 r, const float* w, uint32_t largest) {
+  const Turned<E, NORM, INTER, G> x(ex, r, w);
+  double hi = 0.0, lo = 0.0;
+#pragma unroll 1
+  for (uint32_t left = __reduce_or_sync(0xffffffffu, largest); left; left &= left - 1) {
+    const int e = __ffs(left) - 1;
+    const double v = x(e);
+    if (largest >> e & 1) {
+      hi = fmax(hi, v);
+      lo = fmin(lo, v);
+    }
+  }
+#pragma unroll 1
+  for (int y = 1; y < 4; y <<= 1) {
+    hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, y));
+    lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, y));
+  }
+  return copysignf(q4_scale<E>(__double2float_ru(fmax(hi, -lo))), hi >= -lo ? 1.f : -1.f);   // (upwards, as M itself)
+}
+// The codes (packed as K's) with those replaced that `need` has a bit for.
+template <class E, bool NORM, bool INTER, int G>
+__device__ __noinline__ uint32_t exact_codes(const Exact ex, uint4 r, const float* w, uint32_t need, float M, uint32_t word) {
+  const Turned<E, NORM, INTER, G> x(ex, r, w);
+#pragma unroll 1
+  for (uint32_t left = __reduce_or_sync(0xffffffffu, need); left; left &= left - 1) {
+    const int e = __ffs(left) - 1;
+    const double v = x(e);
+    if (need >> e & 1) {
+      // n <= t < n + 1 as fp32 sees t = 8 x / M; the border between n and n + 1 is
+      // (n + 1/2) M / 8, compared exactly
+      const float am = fabsf(M), n = M == 0.f ? 0.f : floorf(fminf(fmaxf(8.f * (float)v / M, -8.f), 9.f));
+      const double y = M < 0.f ? -8.0 * v : 8.0 * v;
+      const int k = min(max((int)n + (M != 0.f && y >= (double)((n + 0.5f) * am)), -7), 8);
       const int at = 16 * (e & 1) + 4 * (e >> 1);
-      word = (word & ~(15u << at)) | (uint32_t)((int)k + 7) << at;
+      word = (word & ~(15u << at)) | (uint32_t)(k + 7) << at;
     }
   }
-  return make_uint2(word, __float_as_uint(M));
+  return word;
 }
 
 __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float e) {   // of codes k, the first lowest
@@ -191,13 +225,14 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
   };
   // the lane's and its group's error bound, in the head's largest element
   const bool group_err = NORM || (ln.li & ~3) < 2 * half;
+  constexpr float kErr = NORM ? kErrNormed : kErrTurned;
   const float my_err = NORM || ln.turned ? kErr : 0.f, bump = NORM || ln.turned ? 0.f : 0x1p-15f;
   Exact ex;
   ex.freq = a.freq;
   ex.pos = pos;
   ex.mscale = a.mscale;
   ex.eps = a.eps;
-  ex.head_dim = D;
+  ex.inv_d = 1.0 / D;
   ex.half = half;
   const float* kw = s_w[1] + ln.li * 8;
   auto heads = [&](const uint16_t* src, uint8_t* row, int j0, int j1, auto is_value) {
@@ -224,7 +259,22 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
           lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         }
         const float m = hi >= -lo ? hi : lo, am = fabsf(m);
-        float M = copysignf(q4_scale<E>(am), m);
+        float M = copysignf(q4_scale<E>(am), m), top = am;
+        if (!kValue) {
+#pragma unroll
+          for (int o = 4; o < G; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));    // the head's largest
+          const float err = group_err ? kErr * top : 0.f;
+          const bool scale = err > 0.f && am <= 3.402823466e38f &&
+                             (q4_scale<E>(am + err) != q4_scale<E>(fmaxf(am - err, 0.f)) || fabsf(hi + lo) <= 2.f * err);
+          if (__any_sync(0xffffffffu, scale)) {
+            uint32_t largest = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (scale && fabsf(x[e]) >= am - 2.f * err) largest |= 1u << e;
+            const float f = exact_scale<E, NORM, INTER, G>(ex, raw[j], kw, largest);
+            if (scale) M = f;
+          }
+        }
         const float inv = M == 0.f ? 0.f : 8.f / M;
         float k[8], off[8];
         round8(x, inv, kValue ? 0x1p-15f : bump, k, off);
@@ -235,24 +285,15 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
         } else {
           const uint32_t a0 = nibbles(k[0], k[2], k[4], k[6]), a1 = nibbles(k[1], k[3], k[5], k[7]);
           word = __byte_perm(a0, a1, 0x5410);
-          float top = am;                        // the head's largest element
-#pragma unroll
-          for (int o = 4; o < G; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float err = my_err * top, m_err = group_err ? kErr * top : 0.f;
-          const float limit = 0.5f - 0x1p-18f - err * fabsf(inv);
+          const float limit = 0.5f - 0x1p-19f - my_err * top * fabsf(inv);    // (t itself: 2^-19.5)
           const float far0 = fmaxf(fmaxf(fabsf(off[0]), fabsf(off[1])), fmaxf(fabsf(off[2]), fabsf(off[3])));
           const float far1 = fmaxf(fmaxf(fabsf(off[4]), fabsf(off[5])), fmaxf(fabsf(off[6]), fabsf(off[7])));
-          const bool code = my_err > 0.f && fmaxf(far0, far1) > limit;
-          const bool scale = m_err > 0.f && am <= 3.402823466e38f &&
-                             (q4_scale<E>(am + m_err) != q4_scale<E>(fmaxf(am - m_err, 0.f)) || fabsf(hi + lo) <= 2.f * m_err);
-          if (__any_sync(0xffffffffu, code || scale)) {
-            uint32_t need = scale ? 0xffu : 0u;
+          if (__any_sync(0xffffffffu, my_err > 0.f && fmaxf(far0, far1) > limit)) {
+            uint32_t need = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (my_err > 0.f && fabsf(off[e]) > limit) need |= 1u << e;
-            const uint2 f = requantise<E, NORM, INTER, G>(ex, raw[j], kw, need, scale, M, word);
-            word = f.x;
-            M = __uint_as_float(f.y);
+            word = exact_codes<E, NORM, INTER, G>(ex, raw[j], kw, need, M, word);
           }
         }
         if (stored && row && h < d.heads_kv) {
@@ -285,56 +326,72 @@ void (*append_kernel(bool norm, bool inter, int lanes))(const KvAppendArgs) {
 }
 
 // ================================================================ read
-// Token i: position pos_i of table row row_i, K and V as rows of 16-bit elements.
+// Token i: position pos_i of table row row_i, K and V as rows of 16-bit elements.  A warp a
+// token; a lane's share of a head of a 4-bit cache is a quarter of each group, 8 elements, one
+// load of codes for all groups and one of scales, stored as 16 bytes a group.  Bound: memory,
+// the 16-bit rows first, once the three loads in a chain (row and position, page, codes) are
+// hidden by other warps.
 constexpr int kReadThreads = 256;
 
-template <class E, bool Q4>
+// NG: 0, or the groups of a head of a 4-bit cache.
+template <class E, int NG>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ KvReadArgs a) {
   const KvDev& d = a.kv;
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kReadThreads / 32), plane = (int64_t)d.max_rows * d.max_blocks;
-  const int width = d.heads_kv * d.head_dim;
-  for (int64_t u = (int64_t)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5); u < 2 * (int64_t)a.n; u += warps) {
-    const int i = (int)(u >> 1), j = (int)(u & 1);
+  const int i = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  if (i >= a.n) return;
+  const int row = __ldg(a.row + i), pos = __ldg(a.pos + i);
+  if (pos < 0) return;
+  const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
+  const int b = (int)a.per_page_div.div((uint32_t)pos), in_page = pos - b * d.per_page;
+  const bool inside = row >= 0 && row < d.max_rows && b < d.max_blocks;
+  int page[2] = {-1, -1};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (inside && (j ? a.v : a.k)) page[j] = __ldg(d.table + (2 * a.layer + j) * plane + (int64_t)row * d.max_blocks + b);
+  const int dim = d.head_dim, width = d.heads_kv * dim;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
     uint16_t* out = j ? a.v : a.k;
-    const int row = __ldg(a.row + i), pos = __ldg(a.pos + i);
-    if (!out || pos < 0) continue;
-    int page = -1, in_page = 0;
-    if (row >= 0 && row < d.max_rows) {
-      const int b = (int)a.per_page_div.div((uint32_t)pos);
-      in_page = pos - b * d.per_page;
-      if (b < d.max_blocks) page = __ldg(d.table + (2 * a.layer + j) * plane + (int64_t)row * d.max_blocks + b);
-    }
-    if ((uint32_t)page >= (uint32_t)d.num_pages) {
+    if (!out) continue;
+    if ((uint32_t)page[j] >= (uint32_t)d.num_pages) {
       if (lane == 0) report_err(d.error, kErrInvalid);
       continue;
     }
     out += i * (j ? a.ldv : a.ldk);
-    if (!Q4) {
-      const uint16_t* src = d.pool + ((int64_t)page * d.per_page + in_page) * width;
-      for (int e = lane * 8; e < width; e += 256) *reinterpret_cast<uint4*>(out + e) = *reinterpret_cast<const uint4*>(src + e);
+    if constexpr (NG == 0) {
+      const uint16_t* src = d.pool + ((int64_t)page[j] * d.per_page + in_page) * width;
+      for (int e = lane * 8; e < width; e += 256) *reinterpret_cast<uint4*>(out + e) = __ldg(reinterpret_cast<const uint4*>(src + e));
     } else {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, page, in_page);
-      const int ng = d.groups, words = 4 * ng;     // 8 elements each
-      for (int w = lane; w < words * d.heads_kv; w += 32) {
-        const int h = w / words, li = w - h * words, g = li >> 2, k4 = li & 3;
-        if (li * 8 >= d.head_dim) continue;
-        const uint8_t* codes = src + h * 16 * ng;
-        const float M = Elem<E>::to(reinterpret_cast<const uint16_t*>(src + (int64_t)d.heads_kv * 16 * ng)[h * ng + g]);
-        float x[8];
-        if (j) {
-          const uint32_t c = reinterpret_cast<const uint16_t*>(codes)[2 * k4 * ng + g] |
-                             (uint32_t)reinterpret_cast<const uint16_t*>(codes)[(2 * k4 + 1) * ng + g] << 16;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, page[j], in_page);
+#pragma unroll 2
+      for (int u = lane; u < 4 * d.heads_kv; u += 32) {
+        const int h = u >> 2, k4 = u & 3;
+        uint32_t w[NG], m[(NG + 1) / 2];
+        q4_load<NG>(src + (h * 16 + k4 * 4) * NG, src + (d.heads_kv * 16 + h * 2) * NG, w, m);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = q4_value(c >> (4 * e) & 15, M);
-        } else {
-          const uint32_t c = reinterpret_cast<const uint32_t*>(codes)[k4 * ng + g];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = q4_value(c >> (16 * (e & 1) + 4 * (e >> 1)) & 15, M);
+        for (int g = 0; g < NG; ++g) {
+          uint32_t y[4];
+          q4_eight<E, NG>(w, m, g, j == 1, y);
+          if (32 * g + 8 * k4 < dim)
+            *reinterpret_cast<uint4*>(out + h * dim + 32 * g + 8 * k4) = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        *reinterpret_cast<uint4*>(out + h * d.head_dim + li * 8) = pack8<E>(x);
       }
     }
+  }
+}
+
+template <class E>
+void (*read_kernel(int groups))(const KvReadArgs) {
+  switch (groups) {
+    case 1: return kv_read_kernel<E, 1>;
+    case 2: return kv_read_kernel<E, 2>;
+    case 3: return kv_read_kernel<E, 3>;
+    case 4: return kv_read_kernel<E, 4>;
+    case 5: return kv_read_kernel<E, 5>;
+    case 6: return kv_read_kernel<E, 6>;
+    case 7: return kv_read_kernel<E, 7>;
+    default: return kv_read_kernel<E, 8>;
   }
 }
 
@@ -353,12 +410,10 @@ cudaError_t launch_kv_q4_append(const KvAppendArgs& args, int dtype, int num_sms
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, int num_sms, cudaStream_t st) {
-  const int64_t ctas = (2 * (int64_t)a.n + kReadThreads / 32 - 1) / (kReadThreads / 32);
-  const int grid = (int)std::min<int64_t>(ctas, 16 * num_sms);
-  auto kernel = a.kv.groups == 0 ? kv_read_kernel<__half, false>
-                                 : dtype == 0 ? kv_read_kernel<__half, true> : kv_read_kernel<__nv_bfloat16, true>;
-  kernel<<<grid, kReadThreads, 0, st>>>(a);
+cudaError_t launch_kv_read(const KvReadArgs& a, int dtype, cudaStream_t st) {
+  auto kernel = a.kv.groups == 0 ? kv_read_kernel<__half, 0>
+                                 : dtype == 0 ? read_kernel<__half>(a.kv.groups) : read_kernel<__nv_bfloat16>(a.kv.groups);
+  kernel<<<(unsigned)(((int64_t)a.n + kReadThreads / 32 - 1) / (kReadThreads / 32)), kReadThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -58,8 +58,81 @@ __device__ __forceinline__ float q4_scale(float a) {
   const float up = __uint_as_float((__float_as_uint(a) + 0x7ffffu) & 0xfff80000u);
   return fminf(a < 16.f * kFinest ? ceilf(a * kPerFinest) * kFinest : up, kLargest);
 }
-// What a code stands for.
-__device__ __forceinline__ float q4_value(uint32_t code, float M) { return (float)((int)code - 7) * (M * 0.125f); }
+template <class E>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if constexpr (Elem<E>::kBf16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <class E>
+__device__ __forceinline__ uint32_t fma2x16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  if constexpr (Elem<E>::kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+// Codes become numbers in two steps, both exact: k = c - 7 (from 1024 + c, or 128 + c in
+// bf16, which is the code with an exponent's bits around it), then k M / 8.
+// The codes in bits 0-3, 4-7, 8-11 and 12-15 of both halves of w, as pairs of numbers; s =
+// M / 8 twice.
+template <class E>
+__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t s, uint32_t (&y)[4]) {
+  if constexpr (Elem<E>::kBf16) {
+    constexpr uint32_t kBase = 0x43004300u, kOne = 0x3f803f80u, kOff = 0xc307c307u;     // 128, 1, -135
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2<E>(fma2x16<E>((w >> 4 * i & 0x000f000fu) | kBase, kOne, kOff), s);
+  } else {
+    constexpr uint32_t kBase = 0x64006400u, kOne = 0x3c003c00u, kOff = 0xe407e407u;     // 1024, 1, -1031
+    constexpr uint32_t kSixteenth = 0x2c002c00u, kOff16 = 0xd470d470u;                  // 1 / 16, -71
+    const uint32_t h = w >> 8;
+    y[0] = mul2<E>(fma2x16<E>((w & 0x000f000fu) | kBase, kOne, kOff), s);
+    y[1] = mul2<E>(fma2x16<E>((w & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
+    y[2] = mul2<E>(fma2x16<E>((h & 0x000f000fu) | kBase, kOne, kOff), s);
+    y[3] = mul2<E>(fma2x16<E>((h & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
+  }
+}
+// A lane's share of a head: the words that hold 8 elements of every group (c: the
+// quarter's first byte), and the scales of the groups (m).
+template <int NG>
+__device__ __forceinline__ void q4_load(const uint8_t* c, const uint8_t* m, uint32_t (&w)[NG], uint32_t (&s)[(NG + 1) / 2]) {
+  if constexpr (NG % 4 == 0) {
+#pragma unroll
+    for (int g = 0; g < NG; g += 4) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(c) + g / 4);
+      w[g] = x.x; w[g + 1] = x.y; w[g + 2] = x.z; w[g + 3] = x.w;
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(m) + g / 4);
+      s[g / 2] = y.x; s[g / 2 + 1] = y.y;
+    }
+  } else if constexpr (NG == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(c));
+    w[0] = x.x; w[1] = x.y;
+    s[0] = __ldg(reinterpret_cast<const uint32_t*>(m));
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      w[g] = __ldg(reinterpret_cast<const uint32_t*>(c) + g);
+      const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(m) + g);
+      s[g / 2] = g & 1 ? s[g / 2] | h << 16 : h;
+    }
+  }
+}
+// The 8 consecutive elements of group g in such a share, as pairs of numbers.
+template <class E, int NG>
+__device__ __forceinline__ void q4_eight(const uint32_t (&w)[NG], const uint32_t (&m)[(NG + 1) / 2], int g, bool value,
+                                         uint32_t (&y)[4]) {
+  const uint32_t s = mul2<E>(__byte_perm(m[g / 2], 0, g & 1 ? 0x3232 : 0x1010), Elem<E>::kBf16 ? 0x3e003e00u : 0x30003000u);
+  if (value) {
+    // of the share's 16-bit words, number g (elements 0-3) and NG + g (4-7)
+    const uint32_t sel = (g & 1 ? 0x32 : 0x10) | ((NG + g) & 1 ? 0x7600 : 0x5400);
+    uint32_t x[4];
+    q4_pairs<E>(__byte_perm(w[g / 2], w[(NG + g) / 2], sel), s, x);
+    y[0] = __byte_perm(x[0], x[1], 0x5410); y[1] = __byte_perm(x[2], x[3], 0x5410);
+    y[2] = __byte_perm(x[0], x[1], 0x7632); y[3] = __byte_perm(x[2], x[3], 0x7632);
+  } else {
+    q4_pairs<E>(w[g], s, y);
+  }
+}
 
 // Where a token's row begins; page and token of the page from a slot page * P + t % P.
 __device__ __forceinline__ int64_t q4_row(const KvDev& d, int page, int in_page) {
