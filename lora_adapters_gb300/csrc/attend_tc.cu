@@ -25,7 +25,7 @@ cudaError_t prepare_kv_chunk_kernels() {
     for (int cap : {kCapNone, kCapSmall, kCapAny})
       for (int head_dim : {64, 80, 128}) {
         const cudaError_t e = cudaFuncSetAttribute(chunk_kernel(dtype, cap, head_dim),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<false>);
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -35,7 +35,7 @@ int64_t kv_chunk_part_rows(int num_sms) { return (int64_t)num_sms * 4 * kKvTile;
 
 cudaError_t launch_kv_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
   const int cap = a.softcap == 0.f ? kCapNone : a.softcap <= kCapNear ? kCapSmall : kCapAny;
-  chunk_kernel(dtype, cap, a.kv.head_dim)<<<num_sms, kThreads, kSmemBytes, st>>>(a);
+  chunk_kernel(dtype, cap, a.kv.head_dim)<<<num_sms, kThreads, kSmemBytes<false>, st>>>(a);
   return cudaGetLastError();
 }
 

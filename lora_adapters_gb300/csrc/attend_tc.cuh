@@ -31,9 +31,10 @@
 // A position past the request's length, or one whose table entry names no page,
 // reads nothing: its key and value are zeros and its weight is 0.
 //
-// A cache held in 4 bits (kv_q4.cuh): the four warps load codes and scales into
-// registers, a tile ahead, and write the numbers they stand for, which the storage
-// type holds exactly, to the same tiles; everything after them is the same.
+// A cache held in 4 bits (kv_q4.cuh): the four warps copy codes and scales to a ring of
+// three tiles of their own, and write the numbers they stand for, which the storage type
+// holds exactly, to the K and V tiles, three instead of four; everything after them is
+// the same.
 #pragma once
 
 #include <cuda.h>
@@ -41,6 +42,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv.cuh"
 #include "kv.h"
@@ -55,7 +58,9 @@ using namespace ptx;
 constexpr int kRowBytes = 128;                  // 64 elements, one swizzle row
 constexpr int kAtom = kKvTile * kRowBytes;      // 128 rows x 64 elements: 16 KB
 constexpr int kMaxAtoms = 2;                    // head_dim <= 128
-constexpr int kStages = 4;                      // K and V tiles in flight
+constexpr int tc_stages(bool q4) { return q4 ? 3 : 4; }    // K and V tiles in flight
+constexpr int kRawTiles = 3;                    // of a 4-bit cache: tiles of codes on their way
+constexpr int kRawRow = 80;                     // bytes of a row: 64 of codes, 16 of scales (48 and 32)
 constexpr int kQTiles = 3;                      // Q tiles: two in use, one for the next part
 // warps: 0-3 K and V, 4-7 softmax of tile A, 8-11 of tile B, 12 MMAs, 13 Q,
 // 14 the walk
@@ -271,9 +276,13 @@ __device__ __forceinline__ Part walk_next(const KvAttendArgs& a, Walk& w, int64_
   return p;
 }
 
+template <bool Q4>
 struct TcSmem {
+  static constexpr int kStages = tc_stages(Q4);
   uint8_t q[kQTiles][kMaxAtoms][kAtom];
   uint8_t kv[kStages][kMaxAtoms][kAtom];
+  uint8_t raw[Q4 ? kRawTiles : 1][Q4 ? kKvTile * kRawRow : 16];
+  int32_t raw_scale[kRawTiles][4];             // where the head's scales begin in a row's
   uint64_t q_full[kQTiles], q_empty[kQTiles], kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t part_full[kParts], part_empty[kParts];
@@ -285,66 +294,132 @@ struct TcSmem {
   uint32_t tmem_slot;
 };
 
-// The four warps of a 4-bit cache.  Warp w fills rows 32 w .. 32 w + 31 of a tile, four lanes
-// a row, eight rows at a time: a lane loads its share of every group with one load, 8
-// consecutive elements each, and writes each as 16 bytes.  A row's neighbours in the warp
-// are four rows apart, so that eight lanes' pieces lie in different banks.
+// The four warps of a 4-bit cache.  Warp w fills rows 32 w .. 32 w + 31 of a tile.  A lane
+// copies one row's codes and scales, 16 bytes at a time, to the warp's ring, two to three
+// tiles ahead; four lanes a row, eight rows at a time, then write the numbers, a lane its
+// share of every group, 8 consecutive elements each, as 16 bytes.  A row's neighbours in the
+// warp are four rows apart, so that eight lanes' pieces lie in different banks.  V's elements
+// stay in the order of their codes, 0 4 1 5 2 6 3 7 in every eight: the results have it too,
+// and are put in order as they leave (column).
 template <class E, int NG, class Wait, class Next, class Read>
-__device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool& ok, int warp, int lane, Wait wait_warp,
+__device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem<true>& sm, bool& ok, int warp, int lane, Wait wait_warp,
                                         Next next_part, Read part_read) {
+  constexpr int kStages = TcSmem<true>::kStages, kM = (NG + 1) / 2;
+  constexpr int kCodes = 16 * NG, kScales = NG % 2 ? 32 : 16;       // bytes of a row's (odd: across a border of 16)
+  static_assert(kCodes + kScales <= kRawRow, "a row");
   const KvDev& d = a.kv;
   const int64_t plane = (int64_t)d.max_rows * d.max_blocks;
-  const int kk = lane & 3, sub = 4 * (lane >> 2 & 1) + (lane >> 3);      // lane's piece and row (of eight)
-  constexpr int kM = (NG + 1) / 2;
-  struct Tile {
-    uint32_t w[4][NG], m[4][kM];
-  };
-  uint32_t n = 0;      // tiles issued
+  // ---- the tiles on their way: K and V in turn, part after part
   Part p;
-  for (;;) {
-    if (!next_part(p, true)) break;
-    __syncwarp();
-    if (lane == 0) part_read();
-    if (p.i1 == 0) break;
+  p.i1 = 0;
+  int i = 0;                         // key tile
+  bool more = true, value = false;   // tiles are left; the next one is V's
+  // Position 32 warp + lane of the tile: its pages are asked for a tile before its rows are
+  // needed (in_page -1: past the request's end).
+  int kp = 0, vp = 0, in_page = -1;
+  const uint8_t *own = nullptr, *v_row = nullptr;      // NULL: no such position, or no page for it
+  auto lookup = [&]() {
     const int32_t* tab = d.table + 2 * a.layer * plane + (int64_t)dbg_index(p.row, d.max_rows, d.error) * d.max_blocks;
-    const uint8_t* head = reinterpret_cast<const uint8_t*>(d.pool) + (int64_t)p.hk * 16 * NG;
-    const int scales = d.heads_kv * 16 * NG - p.hk * 14 * NG;            // from the head's codes to its scales
-    const uint8_t *k_row, *v_row;      // of position 32 warp + lane of a tile, NULL: none
-    uint32_t holes;
-    auto lookup = [&](int i) {
-      const int j = i * kKvTile + 32 * warp + lane;
-      k_row = v_row = nullptr;
-      if (j < p.len) {
-        const int b = (int)a.per_page_div.div((uint32_t)j), off = j - b * d.per_page;
-        const int kp = __ldg(tab + b), vp = __ldg(tab + plane + b);
-        if ((uint32_t)kp < (uint32_t)d.num_pages && (uint32_t)vp < (uint32_t)d.num_pages) {
-          k_row = head + q4_row(d, kp, off);
-          v_row = head + q4_row(d, vp, off);
+    const int j = i * kKvTile + 32 * warp + lane;
+    in_page = -1;
+    if (j < p.len) {
+      const int b = (int)a.per_page_div.div((uint32_t)j);
+      in_page = j - b * d.per_page;
+      kp = __ldg(tab + b);
+      vp = __ldg(tab + plane + b);
+    }
+  };
+  auto open = [&]() {                // the next part's first tile, if there is one
+    more = next_part(p, true);
+    __syncwarp();
+    if (more && lane == 0) part_read();
+    more = more && p.i1 > 0;
+    i = p.i0;
+    if (more) lookup();
+  };
+  uint32_t n_in = 0;                 // tiles asked for
+  // piece x of the codes of row r of the warp's, the pieces of two rows' neighbours exchanged
+  auto place = [](int r, int x) { return r * kCodes + (NG == 4 ? x ^ (r >> 1 & 3) : x) * 16; };
+  auto issue = [&](uint32_t slot) {  // a group of copies, none when no tile is left
+    if (more) {
+      const int in_row = d.heads_kv * kCodes + p.hk * 2 * NG;
+      const uint32_t to = smem_addr(sm.raw[slot]) + warp * (32 * kRawRow);
+      own = v_row;
+      if (!value) {
+        const bool there = (uint32_t)kp < (uint32_t)d.num_pages && (uint32_t)vp < (uint32_t)d.num_pages;
+        const uint32_t holes = __ballot_sync(0xffffffffu, in_page >= 0 && !there);
+        own = v_row = nullptr;
+        if (in_page >= 0 && there) {
+          own = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, kp, in_page);
+          v_row = reinterpret_cast<const uint8_t*>(d.pool) + q4_row(d, vp, in_page);
+        }
+        if (lane == 0) {
+          sm.holes[(n_in >> 1) & 3][warp] = holes;
+          if (holes) report_err(d.error, kErrInvalid);
         }
       }
-      holes = __ballot_sync(0xffffffffu, j < p.len && !k_row);
-      if (holes && lane == 0) report_err(d.error, kErrInvalid);
-    };
-    auto load = [&](const uint8_t* row, Tile& t) {
+      const uint32_t bytes = own ? 16 : 0;
+      const uint8_t* row = own ? own : reinterpret_cast<const uint8_t*>(d.pool);
+      const uint8_t *codes = row + (own ? p.hk * kCodes : 0), *m = row + (own ? in_row & ~15 : 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* r = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), 8 * j + sub));
-#pragma unroll
-        for (int g = 0; g < NG; ++g) t.w[j][g] = 0;
-#pragma unroll
-        for (int g = 0; g < kM; ++g) t.m[j][g] = 0;
-        if (r) q4_load<NG>(r + kk * 4 * NG, r + scales, t.w[j], t.m[j]);
+      for (int x = 0; x < NG; ++x) cp16(to + place(lane, x), codes + (own ? 16 * x : 0), bytes);
+      cp16(to + 32 * kCodes + lane * kScales, m, bytes);
+      if (kScales == 32 && (in_row & 15) + 2 * NG > 16) cp16(to + 32 * kCodes + lane * kScales + 16, m + bytes, bytes);
+      if (lane == 0) sm.raw_scale[slot][warp] = in_row & 15;
+      ++n_in;
+      value = !value;
+      if (!value) {                  // V is on its way: the next K
+        if (++i < p.i1) lookup();
+        else open();
       }
-    };
-    auto store = [&](const Tile& t, uint32_t st, bool v) {
-      const uint32_t dst = smem_addr(sm.kv[st][0]) + (32 * warp + sub) * kRowBytes;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  open();
+#pragma unroll 1
+  for (uint32_t k = 0; k < kRawTiles; ++k) issue(k);
+  // ---- from codes to numbers
+  const int kk = lane & 3, nn = lane >> 2, sub = 4 * (nn & 1) + (nn >> 1);   // lane's share and row (of eight)
+  uint32_t slot = 0, st = 0, st_ph = 1;
+#pragma unroll 1
+  for (uint32_t n = 0; n < n_in; ++n) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawTiles - 1) : "memory");
+    __syncwarp();                    // the warp's copies of this tile have landed
+    const uint32_t from = smem_addr(sm.raw[slot]) + warp * (32 * kRawRow), at_m = 32 * kCodes + sm.raw_scale[slot][warp];
+    uint32_t words[4][NG], scales[4][kM];        // all rows' first, so that their latencies overlap
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t(&w)[NG] = words[j], (&s)[kM] = scales[j];
+      const int row = 8 * j + sub;
+      const uint32_t c = from + (NG == 4 ? place(row, kk) : row * kCodes + kk * 4 * NG), m = from + at_m + row * kScales;
+      if constexpr (NG == 4) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(c));
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "r"(m));
+      } else if constexpr (NG == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(c));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s[0]) : "r"(m));
+      } else {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          uint16_t h;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[g]) : "r"(c + 4 * g));
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(m + 2 * g));
+          s[g / 2] = g & 1 ? s[g / 2] | (uint32_t)h << 16 : h;
+        }
+      }
+    }
+    if (!wait_warp(&sm.kv_empty[st], st_ph)) {
+      ok = false;
+      break;
+    }
+    const uint32_t dst = smem_addr(sm.kv[st][0]) + (32 * warp + sub) * kRowBytes;
+    auto tile = [&](auto is_value) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           uint32_t y[4];
-          q4_eight<E, NG>(t.w[j], t.m[j], g, v, y);
+          q4_eight<E, NG>(words[j], scales[j], g, decltype(is_value)::value, y);
           const int ch = 4 * g + kk;           // 16-byte piece of the row
           const uint32_t to = dst + 8 * j * kRowBytes + (ch >> 3) * kAtom + (((ch & 7) ^ sub) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
@@ -352,33 +427,20 @@ __device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool&
         }
       }
     };
-    lookup(p.i0);
-    Tile k, v;
-    load(k_row, k);
-    for (int i = p.i0; i < p.i1 && ok; ++i) {
-      load(v_row, v);
-      const uint32_t hc = holes;
-      if (i + 1 < p.i1) lookup(i + 1);
-#pragma unroll
-      for (int half = 0; half < 2; ++half, ++n) {
-        const uint32_t st = n % kStages;
-        if (!wait_warp(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (half == 0) store(k, st, false);
-        else store(v, st, true);
-        fence_async_shared();          // the MMAs read through the async proxy
-        if (half == 0 && lane == 0) {
-          sm.holes[(n >> 1) & 3][warp] = hc;
-          mbar_arrive(&sm.kv_full[st]);
-        }
-        mbar_arrive(&sm.kv_full[st]);
-        if (half == 0 && i + 1 < p.i1) load(k_row, k);
-      }
+    if (n & 1) tile(std::true_type{});
+    else tile(std::false_type{});
+    fence_async_shared();            // the MMAs read through the async proxy
+    __syncwarp();                    // the slot is read
+    if (lane == 0) mbar_arrive(&sm.kv_full[st]);       // (a K tile's holes came with its codes)
+    mbar_arrive(&sm.kv_full[st]);
+    issue(slot);
+    if (++slot == kRawTiles) slot = 0;
+    if (++st == kStages) {
+      st = 0;
+      st_ph ^= 1;
     }
-    if (!ok) break;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // STEPS: 16-element steps of a head, 8 or 4; 0: head_dim 80, 96 or 112 (a
@@ -386,12 +448,19 @@ __device__ __forceinline__ void load_q4(const KvAttendArgs& a, TcSmem& sm, bool&
 // CAP: scores as they are, capped with softcap <= kCapNear, or with any softcap (a
 // 1024-token chunk over 16 K tokens, 40 query heads on 8: 263, 486 and 747 us).
 enum { kCapNone = 0, kCapSmall, kCapAny };
+// The column of element j of eight: in order, or in the order of V's codes.
+template <bool Q4>
+__device__ __forceinline__ constexpr int column(int j) {
+  return Q4 ? 2 * (j & 3) + (j >> 2) : j;
+}
 // NG: 0, or the groups of a head of a 4-bit cache.
 template <class E, int CAP, int STEPS, int NG>
 __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr bool Q4 = NG > 0;
   extern __shared__ uint8_t smem_raw[];
-  TcSmem& sm = *reinterpret_cast<TcSmem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
+  using Smem = TcSmem<Q4>;
+  constexpr int kStages = Smem::kStages;
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023));
   const KvDev& d = a.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t total = (int64_t)__ldg(d.tc_off + a.R) * d.heads_kv;
@@ -404,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   if (warp == kWarpMma) tmem_alloc(&sm.tmem_slot, kTmemCols);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kv_full[s], kLoaders + (s & 1 ? 0 : 4));   // even stages hold K tiles, whose holes come with them
+      mbar_init(&sm.kv_full[s], kLoaders + (Q4 || !(s & 1) ? 4 : 0));   // even stages hold K tiles, whose holes come with them
       mbar_init(&sm.kv_empty[s], 1);
     }
     for (int k = 0; k < kParts; ++k) {
@@ -822,14 +891,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
             for (int k = 0; k < 4; ++k) {
               float y[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(o[k * 8 + j]) * inv;
+              for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(o[k * 8 + column<Q4>(j)]) * inv;
               *reinterpret_cast<uint4*>(mine + ((4 * c + k) ^ (lane & 7)) * 16) = pack8<E>(y);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<uint4*>(mine + ((8 * (c & 1) + k) ^ (lane & 7)) * 16) =
-                  make_uint4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
+                  make_uint4(o[(k & ~1) * 4 + column<Q4>(4 * (k & 1))], o[(k & ~1) * 4 + column<Q4>(4 * (k & 1) + 1)],
+                             o[(k & ~1) * 4 + column<Q4>(4 * (k & 1) + 2)], o[(k & ~1) * 4 + column<Q4>(4 * (k & 1) + 3)]);
             if (c & 1) store_rows(128 * (c - 1), dim * 4 - 128 * (c - 1));
           }
         }
@@ -853,8 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
   }
 }
 
-constexpr size_t kSmemBytes = sizeof(TcSmem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+template <bool Q4>
+constexpr size_t kSmemBytes = sizeof(TcSmem<Q4>) + 1024;
+static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024, "shared memory of one CTA");
 
 }  // namespace
 }  // namespace slora

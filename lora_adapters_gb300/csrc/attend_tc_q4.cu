@@ -28,7 +28,7 @@ cudaError_t prepare_kv_q4_chunk_kernels() {
     for (int cap : {kCapNone, kCapSmall, kCapAny})
       for (int head_dim : {64, 96, 112, 128}) {
         const cudaError_t e = cudaFuncSetAttribute(chunk_kernel(dtype, cap, head_dim, (head_dim + 31) / 32),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<true>);
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -36,7 +36,7 @@ cudaError_t prepare_kv_q4_chunk_kernels() {
 
 cudaError_t launch_kv_q4_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st) {
   const int cap = a.softcap == 0.f ? kCapNone : a.softcap <= kCapNear ? kCapSmall : kCapAny;
-  chunk_kernel(dtype, cap, a.kv.head_dim, a.kv.groups)<<<num_sms, kThreads, kSmemBytes, st>>>(a);
+  chunk_kernel(dtype, cap, a.kv.head_dim, a.kv.groups)<<<num_sms, kThreads, kSmemBytes<true>, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
           uint32_t y[4];
           q4_eight<E, NG>(w, m, g, j == 1, y);
           if (32 * g + 8 * k4 < dim)
-            *reinterpret_cast<uint4*>(out + h * dim + 32 * g + 8 * k4) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(out + h * dim + 32 * g + 8 * k4) =
+                j ? q4_in_order(y) : make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
     }

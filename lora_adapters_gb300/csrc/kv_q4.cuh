@@ -72,24 +72,23 @@ __device__ __forceinline__ uint32_t fma2x16(uint32_t a, uint32_t b, uint32_t c) 
   else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
   return y;
 }
-// Codes become numbers in two steps, both exact: k = c - 7 (from 1024 + c, or 128 + c in
-// bf16, which is the code with an exponent's bits around it), then k M / 8.
-// The codes in bits 0-3, 4-7, 8-11 and 12-15 of both halves of w, as pairs of numbers; s =
-// M / 8 twice.
+// Codes become numbers in two steps, both exact: k / 8 = (c - 7) / 8 (from 1024 + c, or
+// 128 + c in bf16, which is the code with an exponent's bits around it), then k / 8 M.
+// The codes in bits 0-3, 4-7, 8-11 and 12-15 of both halves of w, as pairs of numbers; M twice.
 template <class E>
-__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t s, uint32_t (&y)[4]) {
+__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t M, uint32_t (&y)[4]) {
   if constexpr (Elem<E>::kBf16) {
-    constexpr uint32_t kBase = 0x43004300u, kOne = 0x3f803f80u, kOff = 0xc307c307u;     // 128, 1, -135
+    constexpr uint32_t kBase = 0x43004300u, kEighth = 0x3e003e00u, kOff = 0xc187c187u;    // 128, 1 / 8, -135 / 8
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2<E>(fma2x16<E>((w >> 4 * i & 0x000f000fu) | kBase, kOne, kOff), s);
+    for (int i = 0; i < 4; ++i) y[i] = mul2<E>(fma2x16<E>((w >> 4 * i & 0x000f000fu) | kBase, kEighth, kOff), M);
   } else {
-    constexpr uint32_t kBase = 0x64006400u, kOne = 0x3c003c00u, kOff = 0xe407e407u;     // 1024, 1, -1031
-    constexpr uint32_t kSixteenth = 0x2c002c00u, kOff16 = 0xd470d470u;                  // 1 / 16, -71
+    constexpr uint32_t kBase = 0x64006400u, kEighth = 0x30003000u, kOff = 0xd807d807u;    // 1024, 1 / 8, -1031 / 8
+    constexpr uint32_t kEighth16 = 0x20002000u, kOff16 = 0xc870c870u;                     // 1 / 128, -71 / 8
     const uint32_t h = w >> 8;
-    y[0] = mul2<E>(fma2x16<E>((w & 0x000f000fu) | kBase, kOne, kOff), s);
-    y[1] = mul2<E>(fma2x16<E>((w & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
-    y[2] = mul2<E>(fma2x16<E>((h & 0x000f000fu) | kBase, kOne, kOff), s);
-    y[3] = mul2<E>(fma2x16<E>((h & 0x00f000f0u) | kBase, kSixteenth, kOff16), s);
+    y[0] = mul2<E>(fma2x16<E>((w & 0x000f000fu) | kBase, kEighth, kOff), M);
+    y[1] = mul2<E>(fma2x16<E>((w & 0x00f000f0u) | kBase, kEighth16, kOff16), M);
+    y[2] = mul2<E>(fma2x16<E>((h & 0x000f000fu) | kBase, kEighth, kOff), M);
+    y[3] = mul2<E>(fma2x16<E>((h & 0x00f000f0u) | kBase, kEighth16, kOff16), M);
   }
 }
 // A lane's share of a head: the words that hold 8 elements of every group (c: the
@@ -117,24 +116,23 @@ __device__ __forceinline__ void q4_load(const uint8_t* c, const uint8_t* m, uint
     }
   }
 }
-// The 8 consecutive elements of group g in such a share, as pairs of numbers.
+// The 8 consecutive elements of group g in such a share as pairs of numbers: of a key in
+// their order; of a value (0, 4), (1, 5), (2, 6), (3, 7).
 template <class E, int NG>
 __device__ __forceinline__ void q4_eight(const uint32_t (&w)[NG], const uint32_t (&m)[(NG + 1) / 2], int g, bool value,
                                          uint32_t (&y)[4]) {
-  const uint32_t s = mul2<E>(__byte_perm(m[g / 2], 0, g & 1 ? 0x3232 : 0x1010), Elem<E>::kBf16 ? 0x3e003e00u : 0x30003000u);
-  if (value) {
-    // of the share's 16-bit words, number g (elements 0-3) and NG + g (4-7)
-    const uint32_t sel = (g & 1 ? 0x32 : 0x10) | ((NG + g) & 1 ? 0x7600 : 0x5400);
-    uint32_t x[4];
-    q4_pairs<E>(__byte_perm(w[g / 2], w[(NG + g) / 2], sel), s, x);
-    y[0] = __byte_perm(x[0], x[1], 0x5410); y[1] = __byte_perm(x[2], x[3], 0x5410);
-    y[2] = __byte_perm(x[0], x[1], 0x7632); y[3] = __byte_perm(x[2], x[3], 0x7632);
-  } else {
-    q4_pairs<E>(w[g], s, y);
-  }
+  const uint32_t M = __byte_perm(m[g / 2], 0, g & 1 ? 0x3232 : 0x1010);
+  // (a value's codes: the share's 16-bit words number g, elements 0-3, and NG + g, 4-7)
+  const uint32_t sel = (g & 1 ? 0x32 : 0x10) | ((NG + g) & 1 ? 0x7600 : 0x5400);
+  q4_pairs<E>(value ? __byte_perm(w[g / 2], w[(NG + g) / 2], sel) : w[g], M, y);
+}
+// Such pairs of a value in the order of the elements.
+__device__ __forceinline__ uint4 q4_in_order(const uint32_t (&y)[4]) {
+  return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                    __byte_perm(y[2], y[3], 0x7632));
 }
 
-// Where a token's row begins; page and token of the page from a slot page * P + t % P.
+// Where a token's row begins: token `in_page` of a page.
 __device__ __forceinline__ int64_t q4_row(const KvDev& d, int page, int in_page) {
   return page * d.page_bytes + (int64_t)in_page * d.row_bytes;
 }
