@@ -26,6 +26,8 @@
 // Bound: what four issue slots a clock can do for the bytes of a unit.  Per 32 tokens of
 // a head of 128 there are 4,608 bytes, 196 cycles of an SM's share of the memory, against
 // 550 (two rows) to 700 (eight) instructions of a warp.
+#include <type_traits>
+
 #include "attend.cuh"
 #include "kv_q4.cuh"
 
@@ -101,6 +103,7 @@ struct Ring {
   static constexpr int kUnit = NG <= 4 ? 32 : 16;      // kv_q4_unit
   static constexpr int kStages = 3;
   static constexpr int kCodes = kUnit * 16 * NG;       // of a head
+  static constexpr int kRows = kUnit * 16 + 16;        // where a unit's rows begin, which are there, the block of heads
   // where 16-byte piece p of token t of V lies
   static __device__ __forceinline__ int v_piece(int t, int p) {
     constexpr int kPer = NG == 8 ? 1 : 8 / NG;         // tokens of 128 bytes
@@ -115,6 +118,10 @@ __host__ __device__ __forceinline__ int scale_bytes(int heads, int ng) {
 template <int NG>
 __host__ __device__ __forceinline__ int stage_bytes(int heads, int ng) {
   return 2 * (heads * Ring<NG>::kCodes + Ring<NG>::kUnit * scale_bytes(heads, ng));
+}
+template <int NG>
+__host__ __device__ __forceinline__ int ring_bytes(int heads, int ng) {
+  return Ring<NG>::kStages * stage_bytes<NG>(heads, ng) + 4 * Ring<NG>::kRows;
 }
 
 // D = A B + C.  Not volatile: the compiler may place products that do not depend on each
@@ -138,6 +145,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   using R = Ring<NG>;
   constexpr int UNIT = R::kUnit, NS = UNIT / 16;
   constexpr int NO = RT == 2 ? NG / 2 : NG;            // groups of a lane's results
+  constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;       // of a weight
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const KvDev& d = a.kv;
@@ -188,15 +196,16 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     f.rt = seg - f.hb * f.tiles;
   }
   int r = f.r, hb = f.hb, rt = f.rt, c0 = f.c;          // the segment that is multiplied
-  // A unit's token `lane % UNIT`: its pages on their way, then where its rows begin.  Of a
-  // token past the request's length, or without a page, nothing is read: its codes and
-  // scales are zeros, and its scores are masked.
+  // A unit's rows are looked up by one warp, in turn, and left in shared memory for the others:
+  // asked for one unit before they are needed, written a barrier before.  Of a token past
+  // the request's length, or without a page, nothing is read: its codes and scales are
+  // zeros, and its scores are masked.
   struct Pages {
-    int k, v, in_page, hb;         // in_page -1: no token; hb: block of heads
+    int k, v, in_page;             // of token lane % UNIT, in_page -1: none
   };
-  auto fetch = [&](Pages& p) {
+  auto fetch = [&](Pages& p, bool mine) -> int {         // the unit's block of heads
     p.in_page = -1;
-    if (f.left == 0) return;
+    if (f.left == 0) return 0;
     --f.left;
     if (f.c == f.n) {
       f.c = 0;
@@ -211,54 +220,73 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         }
       }
     }
-    p.hb = f.hb;
     const int j = f.c++ * UNIT + (lane & (UNIT - 1));
-    if (j >= f.len) return;
-    const int b = (int)a.per_page_div.div((uint32_t)j);
-    p.in_page = j - b * P;
-    p.k = __ldg(f.tab + b);
-    p.v = __ldg(f.tab + plane + b);
+    if (mine && j < f.len) {
+      const int b = (int)a.per_page_div.div((uint32_t)j);
+      p.in_page = j - b * P;
+      p.k = __ldg(f.tab + b);
+      p.v = __ldg(f.tab + plane + b);
+    }
+    return f.hb;
   };
   bool missing = false;
-  const int scale_at = d.heads_kv * 16 * ng;
-  // This thread's part of a unit's copies: piece `piece` of head `p_head`'s codes, of the tokens
-  // p_token, p_token + 32 / NG, ...  A token's pieces of all heads are consecutive threads'
-  const int p_token = tid / (heads * NG), p_head = tid % (heads * NG) / NG, piece = tid % NG;
-  // Copies the unit whose pages were looked up to a stage of the ring, and looks the next
-  // one's up; the tokens with both rows, a bit each.
-  auto issue = [&](Pages& p, uint32_t stage) -> uint32_t {
+  const uint32_t rows_at = ring + R::kStages * stage_size;
+  auto publish = [&](const Pages& p, int block, uint32_t slot) {
     const bool token = p.in_page >= 0;
     const bool ok = token && (uint32_t)p.k < (uint32_t)d.num_pages && (uint32_t)p.v < (uint32_t)d.num_pages;
     missing |= token && !ok;
     const int kp = ok ? p.k : 0, vp = ok ? p.v : 0, at = ok ? p.in_page : 0;
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(d.pool);
-    const uint8_t *k_row = pool + q4_row(d, kp, at), *v_row = pool + q4_row(d, vp, at);
-    const uint32_t valid = __ballot_sync(0xffffffffu, ok), own_bytes = ok ? 16 : 0;
-    const uint32_t to = ring + stage * stage_size, to_k = to + p_head * R::kCodes + piece * 16,
-                   to_v = to + at_v + p_head * R::kCodes;
-    const int head0 = p.hb * hbw + hsub0, in_row = ((head0 + p_head) * ng + piece) * 16;
+    const uint32_t to = rows_at + slot * R::kRows, valid = __ballot_sync(0xffffffffu, ok);
+    asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(to + (lane & (UNIT - 1)) * 16), "l"(pool + q4_row(d, kp, at)),
+                 "l"(pool + q4_row(d, vp, at))
+                 : "memory");
+    if (lane == 0)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + UNIT * 16), "r"(valid), "r"(block) : "memory");
+  };
+  const int scale_at = d.heads_kv * 16 * ng;
+  // This thread's part of a unit's copies: piece `piece` of head `p_head`'s codes, of the tokens
+  // p_token, p_token + 32 / NG, ...  A token's pieces of all heads are consecutive threads'
+  const int p_token = tid / (heads * NG), p_head = tid % (heads * NG) / NG, piece = tid % NG;
+  const uint32_t to_k = ring + p_head * R::kCodes + p_token * 16 * NG + piece * 16,
+                 to_v = ring + at_v + p_head * R::kCodes + R::v_piece(p_token, piece);
+  // Copies the unit whose rows are in `slot` to a stage of the ring; the tokens with both
+  // rows, a bit each.
+  auto issue = [&](uint32_t slot, uint32_t stage) -> uint32_t {
+    const uint32_t rows = rows_at + slot * R::kRows, to = stage * stage_size;
+    uint32_t vh[2];
+    lds<2>(rows + UNIT * 16, vh);
+    const uint32_t valid = vh[0];
+    const int head0 = vh[1] * hbw + hsub0, in_row = ((head0 + p_head) * ng + piece) * 16;
+    auto codes = [&](auto all) {
+      constexpr bool kAll = decltype(all)::value;
 #pragma unroll
-    for (int x = 0; x < UNIT * NG / 32; ++x) {
-      const int t = p_token + x * (32 / NG);
-      const uint8_t* src = shfl_ptr(k_row, t) + in_row;
-      if (FULL || piece < ng) cp_async(to_k + t * 16 * NG, src, valid >> t & 1 ? 16 : 0);
-    }
-#pragma unroll
-    for (int x = 0; x < UNIT * NG / 32; ++x) {
-      const int t = p_token + x * (32 / NG);
-      const uint8_t* src = shfl_ptr(v_row, t) + in_row;
-      if (FULL || piece < ng) cp_async(to_v + R::v_piece(t, piece), src, valid >> t & 1 ? 16 : 0);
-    }
+      for (int x = 0; x < UNIT * NG / 32; ++x) {
+        const int t = p_token + x * (32 / NG);
+        const uint8_t *k, *v;
+        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(k), "=l"(v) : "r"(rows + t * 16));
+        const uint32_t bytes = kAll || (valid >> t & 1) ? 16 : 0;
+        if (FULL || piece < ng) {
+          cp_async(to + to_k + x * 512, k + in_row, bytes);
+          // (tokens 32 / NG apart lie 512 bytes apart; NG = 8: with another exchange of the pieces)
+          cp_async(to + (NG == 8 ? to_v ^ (x & 1) << 6 : to_v) + x * 512, v + in_row, bytes);
+        }
+      }
+    };
+    if (valid == ~0u) codes(std::true_type{});
+    else codes(std::false_type{});
     // scales: K's pieces, then V's, one a warp (UNIT = 16: two) for all tokens
     const int s_row = scale_at + head0 * 2 * ng, pieces = ((s_row & 15) + heads * 2 * ng + 15) >> 4;
+    const int own = lane & (UNIT - 1);
     for (int i = tid / UNIT; i < 2 * pieces; i += heads * 32 / UNIT) {
       const bool v = i >= pieces;
       const int from = (v ? i - pieces : i) * 16;
-      cp_async(to + (v ? at_vs : at_ks) + (lane & (UNIT - 1)) * scale_size + from, (v ? v_row : k_row) + (s_row & ~15) + from,
-               own_bytes);
+      const uint8_t* row;
+      asm volatile("ld.shared.u64 %0, [%1];" : "=l"(row) : "r"(rows + own * 16 + (v ? 8 : 0)));
+      cp_async(ring + to + (v ? at_vs : at_ks) + own * scale_size + from, row + (s_row & ~15) + from,
+               valid >> own & 1 ? 16 : 0);
     }
     cp_commit();
-    fetch(p);
     return valid;
   };
   // Scales of a token from the ring.
@@ -273,9 +301,22 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
   };
+  // units 0, 1, 2 published, 0 and 1 on their way, 3 looked up
   Pages next;
-  fetch(next);
-  uint32_t valid = issue(next, 0), valid1 = issue(next, 1), stage = 0;
+  int block;
+  {
+    Pages first[3];
+    int blocks3[3];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) blocks3[x] = fetch(first[x], warp == x % heads);
+    block = fetch(next, warp == 3 % heads);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (warp == x % heads) publish(first[x], blocks3[x], x);
+  }
+  __syncthreads();
+  uint32_t valid = issue(0, 0), valid1 = issue(1, 1), stage = 0, unit = 0;
+  int turn = 3 % heads;            // the warp that looked unit + 3 up
 
   while (left > 0) {
     int4 rq = __ldg(d.req + r);
@@ -360,7 +401,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     for (int c = c0; c < c1; ++c) {
       cp_wait<1>();
       __syncthreads();             // every thread's copies of this unit have landed, the last unit's are read
-      const uint32_t here = ring + stage * stage_size, my_k = here + warp * R::kCodes, my_v = my_k + at_v, valid2 = issue(next, stage == 0 ? 2 : stage - 1);
+      const uint32_t here = ring + stage * stage_size, my_k = here + warp * R::kCodes, my_v = my_k + at_v, valid2 = issue((unit + 2) & 3, stage == 0 ? 2 : stage - 1);
+      if (warp == turn) publish(next, block, (unit + 3) & 3);
+      turn = turn == heads - 1 ? 0 : turn + 1;
+      block = fetch(next, warp == turn);
+      ++unit;
       // ---- scores of tokens nn + 8 x
       float s[2 * NS][NR];
 #pragma unroll
@@ -473,8 +518,10 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           l[y] += p[x][y];
         }
         ph[x] = Elem<__half>::from2(p[x][0], p[x][NR - 1]);
-        const float2 h = Elem<__half>::to2(ph[x]);
-        pl[x] = Elem<__half>::from2(p[x][0] - h.x, p[x][NR - 1] - h.y);
+        if (kParts == 2) {
+          const float2 h = Elem<__half>::to2(ph[x]);
+          pl[x] = Elem<__half>::from2(p[x][0] - h.x, p[x][NR - 1] - h.y);
+        }
       }
       // ---- the token's scales times 2^(7 - E) in fp16, and results
       const float m_up = __uint_as_float((uint32_t)(127 + 7 - top_m) << 23);
@@ -528,9 +575,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             lg[2 * ps][0] = fmaf(p[x][0], mf.x, lg[2 * ps][0]);
             lg[2 * ps + 1][0] = fmaf(p[x][0], mf.y, lg[2 * ps + 1][0]);
           }
-          const uint32_t hi = h2_mul(ph[x], w), lo = h2_fma(pl[x], w, h2_fma(ph[x], w, h2_neg(hi)));
+          const uint32_t hi = h2_mul(ph[x], w);
           bh[x] = trans8x8(hi);
-          bl[x] = trans8x8(lo);
+          if (kParts == 2) bl[x] = trans8x8(h2_fma(pl[x], w, h2_fma(ph[x], w, h2_neg(hi))));
         }
         float acc[GC][2][4];
 #pragma unroll
@@ -543,7 +590,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             const uint32_t tb = __byte_perm(vf[4 * s2 + 2][g / 2], vf[4 * s2 + 3][g / 2], sel);
             const uint32_t ua = ta >> 8, ub = tb >> 8;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+            for (int part = 0; part < kParts; ++part) {
               const uint32_t b0 = part ? bl[2 * s2] : bh[2 * s2], b1 = part ? bl[2 * s2 + 1] : bh[2 * s2 + 1];
               if (s2 == 0 && part == 0) {
                 mma_h(acc[gi][0], ta & kLow, ua & kLow, tb & kLow, ub & kLow, b0, b1, 0.f, 0.f, 0.f, 0.f);
@@ -637,7 +684,7 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
   while (a.kv.heads_kv % heads) --heads;
   a.hbw = std::max(1, 16 / heads) * heads;
   while (a.kv.heads_kv % a.hbw) a.hbw -= heads;
-  const int grid = num_sms * (q4_warps(NG) / heads), smem = Ring<NG>::kStages * stage_bytes<NG>(heads, a.kv.groups);
+  const int grid = num_sms * (q4_warps(NG) / heads), smem = ring_bytes<NG>(heads, a.kv.groups);
   const int threads = heads * 32;
   auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true, FULL> : kv_q4_decode_kernel<E, NG, RT, false, FULL>;
   cudaError_t e;
@@ -670,7 +717,7 @@ template <class E, int NG, int RT, bool FULL = true>
 cudaError_t prepare() {
   for (auto k : {kv_q4_decode_kernel<E, NG, RT, false, FULL>, kv_q4_decode_kernel<E, NG, RT, true, FULL>})
     if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Ring<NG>::kStages * stage_bytes<NG>(kMaxAbreast, NG) + 1024))
+                                             ring_bytes<NG>(kMaxAbreast, NG) + 1024))
       return e;
   return cudaSuccess;
 }
