@@ -101,7 +101,7 @@ __device__ __forceinline__ void sts(uint32_t at, const uint32_t (&w)[N]) {
 template <int NG>
 struct Ring {
   static constexpr int kUnit = NG <= 4 ? 32 : 16;      // kv_q4_unit
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 2;
   static constexpr int kCodes = kUnit * 16 * NG;       // of a head
   static constexpr int kRows = kUnit * 16 + 16;        // where a unit's rows begin, which are there, the block of heads
   // where 16-byte piece p of token t of V lies
@@ -301,22 +301,25 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
   };
-  // units 0, 1, 2 published, 0 and 1 on their way, 3 looked up
+  // units 0 .. kAhead published, all but the last of them on their way, the next looked up
+  constexpr int kAhead = R::kStages - 1;
   Pages next;
   int block;
   {
-    Pages first[3];
-    int blocks3[3];
+    Pages first[kAhead + 1];
+    int first_block[kAhead + 1];
 #pragma unroll
-    for (int x = 0; x < 3; ++x) blocks3[x] = fetch(first[x], warp == x % heads);
-    block = fetch(next, warp == 3 % heads);
+    for (int x = 0; x <= kAhead; ++x) first_block[x] = fetch(first[x], warp == x % heads);
+    block = fetch(next, warp == (kAhead + 1) % heads);
 #pragma unroll
-    for (int x = 0; x < 3; ++x)
-      if (warp == x % heads) publish(first[x], blocks3[x], x);
+    for (int x = 0; x <= kAhead; ++x)
+      if (warp == x % heads) publish(first[x], first_block[x], x);
   }
   __syncthreads();
-  uint32_t valid = issue(0, 0), valid1 = issue(1, 1), stage = 0, unit = 0;
-  int turn = 3 % heads;            // the warp that looked unit + 3 up
+  uint32_t valid[kAhead + 1], stage = 0, unit = 0;
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) valid[x] = issue(x, x);
+  int turn = (kAhead + 1) % heads;           // the warp that looked unit + kAhead + 1 up
 
   while (left > 0) {
     int4 rq = __ldg(d.req + r);
@@ -399,10 +402,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     int top_m = Elem<E>::kBf16 ? -64 : -8;               // E: every |M| so far is below 2^E
 
     for (int c = c0; c < c1; ++c) {
-      cp_wait<1>();
+      cp_wait<kAhead - 1>();
       __syncthreads();             // every thread's copies of this unit have landed, the last unit's are read
-      const uint32_t here = ring + stage * stage_size, my_k = here + warp * R::kCodes, my_v = my_k + at_v, valid2 = issue((unit + 2) & 3, stage == 0 ? 2 : stage - 1);
-      if (warp == turn) publish(next, block, (unit + 3) & 3);
+      const uint32_t here = ring + stage * stage_size, my_k = here + warp * R::kCodes, my_v = my_k + at_v;
+      valid[kAhead] = issue((unit + kAhead) & 3, stage == 0 ? kAhead : stage - 1);
+      if (warp == turn) publish(next, block, (unit + kAhead + 1) & 3);
       turn = turn == heads - 1 ? 0 : turn + 1;
       block = fetch(next, warp == turn);
       ++unit;
@@ -458,12 +462,12 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           for (int x = 0; x < 2 * NS; ++x) s[x][y] = capped<true>(s[x][y] * fac[y], sc, cap_t, cap2);
       }
       // some token is not there, or after the tile's first row
-      if (valid != 0xffffffffu || (c + 1) * UNIT > lim_first) {
+      if (valid[0] != ~0u || (c + 1) * UNIT > lim_first) {
 #pragma unroll
         for (int y = 0; y < NR; ++y)
 #pragma unroll
           for (int x = 0; x < 2 * NS; ++x)
-            if (!(valid >> (nn + 8 * x) & 1) || c * UNIT + nn + 8 * x >= lim[y]) s[x][y] = -INFINITY;
+            if (!(valid[0] >> (nn + 8 * x) & 1) || c * UNIT + nn + 8 * x >= lim[y]) s[x][y] = -INFINITY;
       }
       float n[NR];
 #pragma unroll
@@ -621,8 +625,8 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
               o[2 * ps + j][0][i] += kk & 1 ? acc[2 % GC + j][i & 1][(i & 2) + j] : acc[j % GC][i & 1][(i & 2) + j];
         }
       }
-      valid = valid1;
-      valid1 = valid2;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) valid[x] = valid[x + 1];
       stage = stage == R::kStages - 1 ? 0 : stage + 1;
     }
 #pragma unroll
