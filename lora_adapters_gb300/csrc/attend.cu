@@ -332,7 +332,8 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWideWarps = 16;
 
-template <int V>
+// NORMED: the parts' o are divided by their l already, and so is the sum (4-bit caches).
+template <int V, bool NORMED = false>
 struct JoinSum {
   float m = -INFINITY, l = 0.f, o[V] = {};
   // (a part without weight: its sums may not have been written.  m = -inf alone does
@@ -341,9 +342,17 @@ struct JoinSum {
     if (ml.y == 0.f) return;
     const float mn = fmaxf(m, ml.x), f = ex2(m - mn), w = ex2(ml.x - mn);
     m = mn;
-    l = l * f + ml.y * w;
+    if constexpr (NORMED) {
+      const float a = l * f, b = ml.y * w;
+      l = a + b;
+      const float fo = a / l, wo = b / l;
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = o[j] * f + y[j] * w;
+      for (int j = 0; j < V; ++j) o[j] = o[j] * fo + y[j] * wo;
+    } else {
+      l = l * f + ml.y * w;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = o[j] * f + y[j] * w;
+    }
   }
 };
 // A lane's elements of a row of `cols` floats: 4 consecutive ones of every 128
@@ -376,7 +385,7 @@ __device__ __forceinline__ void store_row(uint16_t* row, int lane, int dim, cons
   }
 }
 
-template <class E, int D, bool WIDE>
+template <class E, int D, bool WIDE, bool NORMED>
 __global__ void __launch_bounds__(WIDE ? kJoinWideWarps * 32 : kJoinThreads)
 kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
   constexpr int V = D / 32;      // elements per lane
@@ -408,7 +417,7 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
     if (g0 == g1) continue;                               // the decode kernel wrote it
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
     waited = true;
-    JoinSum<V> s;
+    JoinSum<V, NORMED> s;
     for (int64_t g = g0 + (WIDE ? warp : 0); g <= g1; g += 4 * W) {   // four parts on their way at a time
       float2 ml[4];
       float y[4][V];
@@ -428,7 +437,7 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
     uint16_t* dst = a.out + (int64_t)dbg_index(rq.x + row / group, a.T, d.error) * a.ldo +
                     (int64_t)(hk * group + row % group) * dim;
     if constexpr (!WIDE) {
-      store_row<E, V>(dst, lane, dim, s.o, s.l);
+      store_row<E, V>(dst, lane, dim, s.o, NORMED && s.l != 0.f ? 1.f : s.l);
     } else {                                              // the warps' sums, in their order
 #pragma unroll
       for (int j = 0; j < V; ++j) s_o[warp][j * 32 + lane] = s.o[j];
@@ -445,15 +454,18 @@ kv_join_kernel(const __grid_constant__ KvAttendArgs a, const int64_t groups) {
         if (lane < W) s_f[lane] = ex2(own - m);
         __syncwarp();
         float l = 0.f, y[V] = {};
+        if (NORMED)
+          for (int k = 0; k < W; ++k) l += s_l[k] == 0.f ? 0.f : s_l[k] * s_f[k];
+        const float all = l;
 #pragma unroll 4
         for (int k = 0; k < W; ++k) {
           if (s_l[k] == 0.f) continue;                    // no weight
-          const float f = s_f[k];
-          l += s_l[k] * f;
+          const float f = NORMED ? s_l[k] * s_f[k] / all : s_f[k];
+          if (!NORMED) l += s_l[k] * f;
 #pragma unroll
           for (int j = 0; j < V; ++j) y[j] += s_o[k][j * 32 + lane] * f;
         }
-        store_row<E, V>(dst, lane, dim, y, l);
+        store_row<E, V>(dst, lane, dim, y, NORMED && l != 0.f ? 1.f : l);
       }
       __syncthreads();
     }
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(kChunkJoinThreads) kv_chunk_join_kernel(const 
 }
 
 // `groups`: the groups of warps that the decode kernel shared the work out to.
-template <class E, int D>
+template <class E, int D, bool NORMED>
 cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
   if (after_chunks) {
     const cudaError_t e = launch_early(kv_chunk_join_kernel<E>, dim3(num_sms, 16), kChunkJoinThreads, 0, st, a);
@@ -510,10 +522,10 @@ cudaError_t launch_join(const KvAttendArgs& a, int num_sms, bool after_chunks, i
   // context, 228 parts a row: 24 us with a warp each, 8 with a block)
   const int64_t segments = (int64_t)a.R * ((a.rows + a.row_tile - 1) / a.row_tile) * (a.kv.heads_kv / a.hbw);
   if (segments * 16 <= groups)
-    return launch_early(kv_join_kernel<E, D, true>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
+    return launch_early(kv_join_kernel<E, D, true, NORMED>, dim3((unsigned)std::min<int64_t>(items, 16 * num_sms)),
                         kJoinWideWarps * 32, 0, st, a, groups);
   const int64_t ctas = (items + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  return launch_early(kv_join_kernel<E, D, false>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, 0,
+  return launch_early(kv_join_kernel<E, D, false, NORMED>, dim3((unsigned)std::min<int64_t>(ctas, 16 * num_sms)), kJoinThreads, 0,
                       st, a, groups);
 }
 
@@ -529,7 +541,7 @@ cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks,
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_join<E, D>(a, num_sms, after_chunks, (int64_t)grid * kDecWarps / a.hbw, st);
+  return launch_join<E, D, false>(a, num_sms, after_chunks, (int64_t)grid * kDecWarps / a.hbw, st);
 }
 
 template <class E>
@@ -540,10 +552,10 @@ cudaError_t decode_dispatch(const KvAttendArgs& a, int num_sms, bool after_chunk
 }
 
 template <class E>
-cudaError_t join_dispatch(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
-  if (a.kv.head_dim <= 64) return launch_join<E, 64>(a, num_sms, after_chunks, groups, st);
-  if (a.kv.head_dim <= 128) return launch_join<E, 128>(a, num_sms, after_chunks, groups, st);
-  return launch_join<E, 256>(a, num_sms, after_chunks, groups, st);
+cudaError_t normed_join(const KvAttendArgs& a, int num_sms, bool after_chunks, int64_t groups, cudaStream_t st) {
+  if (a.kv.head_dim <= 64) return launch_join<E, 64, true>(a, num_sms, after_chunks, groups, st);
+  if (a.kv.head_dim <= 128) return launch_join<E, 128, true>(a, num_sms, after_chunks, groups, st);
+  return launch_join<E, 256, true>(a, num_sms, after_chunks, groups, st);
 }
 }  // namespace
 
@@ -566,10 +578,10 @@ cudaError_t prepare_kv_decode_kernels() {
   return cudaSuccess;
 }
 
-cudaError_t launch_kv_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
+cudaError_t launch_kv_q4_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
                            cudaStream_t st) {
-  return dtype == 0 ? join_dispatch<__half>(a, num_sms, after_chunks, groups, st)
-                    : join_dispatch<__nv_bfloat16>(a, num_sms, after_chunks, groups, st);
+  return dtype == 0 ? normed_join<__half>(a, num_sms, after_chunks, groups, st)
+                    : normed_join<__nv_bfloat16>(a, num_sms, after_chunks, groups, st);
 }
 
 cudaError_t launch_kv_decode(const KvAttendArgs& args, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {

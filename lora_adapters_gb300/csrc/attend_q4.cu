@@ -354,8 +354,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // 2^e <= top < 2^(e + 1); e = -100 where it is less
       const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-      const float down = __uint_as_float((uint32_t)min(127 + 8 + e, 254) << 23) * (CAP ? 1.f : sc);
+      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);   // (infinity, NaN: e = 128)
+      const float size = __uint_as_float((uint32_t)(127 + min(e, 127)) << 23);
+      const float down = CAP ? fminf(size * 256.f, 0x1p127f) : size * (256.f * sc);      // 2^(8 + e)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float x[8], sum = 0.f;
@@ -644,7 +645,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     for (int y = 0; y < NR; ++y) {
       const int row = my_row + y;
       if (row >= rows) continue;
-      const float inv = whole ? (l[y] == 0.f ? 0.f : 1.f / l[y]) : 1.f;
+      const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
       uint16_t* dst = a.out + (int64_t)dbg_index(q0 + row / group, a.T, d.error) * a.ldo +
                       (int64_t)(hk * group + row % group) * dim;
       // slot 0: the segment began in an earlier run; slot 1: it begins here
@@ -655,7 +656,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[i] = fmaf(o[gi][y][i], i & 1 ? 0x1p20f : 0x1p24f, -7.f * lg[gi][y]) * m_down * inv;
+          v[i] = fmaf(o[gi][y][i], i & 1 ? 0x1p20f : 0x1p24f, -7.f * lg[gi][y]) * inv * m_down;
         if (whole) {
           if (e < dim)
             *reinterpret_cast<uint2*>(dst + e) = make_uint2(Elem<E>::from2(v[0], v[1]), Elem<E>::from2(v[2], v[3]));
@@ -699,7 +700,7 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_kv_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, grid / (a.hbw / heads), st);
+  return launch_kv_q4_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, grid / (a.hbw / heads), st);
 }
 template <class E>
 cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {

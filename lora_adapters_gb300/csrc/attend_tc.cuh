@@ -731,7 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
     const float sc = kLog2e * a.scale, cap_t = a.cap_t, cap2 = a.cap2;
-    constexpr float kUp = Elem<E>::kBf16 ? 0.f : 7.f;        // weights are held times 2^kUp
+    // weights are held times 2^kUp (4-bit caches in bf16, whose exponents have the room: so that
+    // sums over 2^16 keys of any size stay below 2^128)
+    constexpr float kUp = !Elem<E>::kBf16 ? 7.f : Q4 ? -24.f : 0.f;
     const int my_tok = rho / group, my_head = rho - my_tok * group;
     uint32_t ns = 0, nf = 0, nq = 0, nk = 0;                  // nk: K tiles of earlier parts
     for (;;) {

@@ -176,9 +176,10 @@ int32_t kv_attend_cols(int32_t head_dim);
 cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
 cudaError_t prepare_kv_q4_chunk_kernels();
 cudaError_t launch_kv_q4_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
-// The joins alone, of what `groups` groups of warps split.
-cudaError_t launch_kv_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
-                           cudaStream_t st);
+// The joins alone, of what `groups` groups of CTAs of the 4-bit decode kernel split, with
+// the parts' results divided by their sums.
+cudaError_t launch_kv_q4_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
+                              cudaStream_t st);
 // The same over a 4-bit cache.
 cudaError_t prepare_kv_q4_decode_kernels();
 cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);

@@ -33,7 +33,9 @@ projections (slora_kv_*): the step's block-table entries and slots are planned
 once, and in every layer the new tokens' queries and keys are rotated, keys and
 values stored in the request's KV pages, and the attention over everything the
 request holds becomes the input of the o projection.  Its time is reported
-apart from the LoRA path's.
+apart from the LoRA path's.  With ``kv_bits`` 4 keys and values are quantised as
+they are stored (slora_kv_q4_create): a page then holds several tokens, and a
+request takes that many times fewer.
 
 Every pool call is logged (``TraceResult.ops``) in the form the oracle's
 allocator replays, so a test can rebuild the pool state independently and
@@ -70,7 +72,7 @@ class TraceSpec:
     # requests' KV (about 45 GB) do not fit, so least-recently-used adapters
     # are evicted and loaded again
     pool_bytes: int = 80 * 10**9
-    kv_pages_per_token: int = 64             # K and V of every layer
+    kv_pages_per_token: int = 64             # K and V of every layer (of kv_tokens_per_page tokens)
     token_budget: int = 1024
     max_running: int = 256                   # requests in the batch at once
     arrivals_per_step: float = 4.0
@@ -83,10 +85,20 @@ class TraceSpec:
     seed: int = 0
     attention: bool = False                  # append and attend between q, k, v and o
     head_dim: int = 128                      # with attention: H / head_dim query and key heads
+    kv_bits: int = 16                        # with attention: bits an element of the KV cache, 16 or 4
 
     @property
     def pool_pages(self) -> int:
         return self.pool_bytes // (self.H * 2)
+
+    @property
+    def kv_tokens_per_page(self) -> int:
+        """Tokens whose K (or V) of one layer a page holds."""
+        return 1 if self.kv_bits == 16 else slora.tokens_per_page(self.H, self.H // self.head_dim, self.head_dim, 4)
+
+    def kv_pages(self, tokens: int) -> int:
+        """Pages of a request of so many tokens."""
+        return -(-tokens // self.kv_tokens_per_page) * self.kv_pages_per_token
 
     @property
     def projections(self) -> Tuple[workloads.Projection, ...]:
@@ -261,6 +273,8 @@ class Trace:
             self.n = n
         self.cache = None
         self.free_rows = list(range(spec.max_running))[::-1]
+        if spec.kv_bits not in (4, 16) or (spec.kv_bits == 4 and not spec.attention):
+            raise ValueError("kv_bits is 16 or, with attention, 4")
         if spec.attention:
             if [p.name for p in spec.layer_projections] != ["q", "k", "v", "o"] or spec.H % spec.head_dim or any(
                     p.h_in != spec.H or p.h_out != spec.H for p in spec.layer_projections):
@@ -270,7 +284,8 @@ class Trace:
             if device is not None:
                 heads = spec.H // spec.head_dim
                 self.cache = slora.KVCache(self.pool, spec.layers, heads, heads, spec.head_dim, spec.max_running,
-                                           spec.prompt_len[1] + spec.output_len[1])
+                                           -(-(spec.prompt_len[1] + spec.output_len[1]) // spec.kv_tokens_per_page),
+                                           bits=spec.kv_bits)
                 freq, mscale = rotary.inv_freq(spec.head_dim)
                 self.cache.set_rotary(spec.head_dim, freq, mscale=mscale)
                 i32 = dict(dtype=torch.int32, device=device)
@@ -373,7 +388,7 @@ class Trace:
                         # the request's KV pages for its whole length come with
                         # admission, so running requests never stall on memory
                         self.refs[rq.adapter] += 1          # its adapter must stay while we make room
-                        h = self._kv_alloc((rq.prompt + rq.output) * sp.kv_pages_per_token)
+                        h = self._kv_alloc(sp.kv_pages(rq.prompt + rq.output))
                         if h is not None:
                             self.resident.move_to_end(rq.adapter)
                             rq.kv_handles.append(h)
@@ -520,15 +535,16 @@ class Trace:
 
     def _plan_step(self, plan, T: int):
         """The step's block-table entries and slots: its requests' lengths and
-        rows, and the pages of the tokens it adds (each request's own list,
+        rows, and the pages of the blocks it opens (each request's own list,
         taken at admission, in order)."""
         import torch
 
-        R, per = len(plan), self.spec.kv_pages_per_token
+        R, per, P = len(plan), self.spec.kv_pages_per_token, self.spec.kv_tokens_per_page
         ctx = np.array([rq.prefilled + rq.generated for rq, _, _ in plan], dtype=np.int32)
         new = np.array([n for _, n, _ in plan], dtype=np.int32)
         rows = np.array([rq.row for rq, _, _ in plan], dtype=np.int32)
-        pages = np.concatenate([self.kv[rq.kv_handles[0]][c * per:(c + n) * per] for (rq, n, _), c in zip(plan, ctx)])
+        pages = np.concatenate([self.kv[rq.kv_handles[0]][-(-c // P) * per:-(-(c + n) // P) * per]
+                                for (rq, n, _), c in zip(plan, ctx)])
         self.plan_dev[:3 * R].copy_(torch.from_numpy(np.concatenate([ctx, new, rows])), non_blocking=True)
         self.pages_dev[:pages.shape[0]].copy_(torch.from_numpy(pages), non_blocking=True)
         return self.cache.plan(self.plan_dev[:R], self.plan_dev[R:2 * R], self.pages_dev[:pages.shape[0]], T,
@@ -554,12 +570,15 @@ def main():
     ap.add_argument("--pool-gb", type=float, default=80.0)
     ap.add_argument("--attention", action="store_true",
                     help="rotate, store and attend between the q, k, v and o projections of every layer")
+    ap.add_argument("--kv-bits", type=int, choices=(4, 16), default=16,
+                    help="with --attention: bits an element of the KV cache")
     args = ap.parse_args()
     from . import build
 
     build.build()
     spec = dataclasses.replace(TraceSpec(), steps=args.steps, layers=args.layers, arrivals_per_step=args.arrivals,
-                               pool_bytes=int(args.pool_gb * 1e9), kv_pages_per_token=2 * args.layers, attention=args.attention)
+                               pool_bytes=int(args.pool_gb * 1e9), kv_pages_per_token=2 * args.layers, attention=args.attention,
+                               kv_bits=args.kv_bits)
     tr = Trace(spec, device=torch.device("cuda", 0))
     res = tr.run()
     s = res.summary()
@@ -571,7 +590,8 @@ def main():
                        "popularity": f"zipf(alpha={spec.zipf_alpha:g})", "pool_gb": spec.pool_bytes / 1e9,
                        "kv_pages_per_token": spec.kv_pages_per_token, "token_budget": spec.token_budget,
                        "arrivals_per_step": spec.arrivals_per_step, "mode": "auto",
-                       **({"attention": True, "head_dim": spec.head_dim} if spec.attention else {})},
+                       **({"attention": True, "head_dim": spec.head_dim, "kv_bits": spec.kv_bits}
+                          if spec.attention else {})},
             "trace": s}
     print(json.dumps(line))
     tr.close()

@@ -410,6 +410,10 @@ ATTEND = {
     "chunk_d256": ([33, 0], [40, 20], 2, 1, 256, 512, "f16", 0.0),
     "chunk_d16": ([5], [300], 4, 4, 16, 256, "bf16", 0.0),
     "mixed": ([9, 600, 0, 77, 0, 300], [1, 1, 90, 1, 400, 33], 8, 4, 128, 1024, "bf16", 0.0),
+    "mixed_tiles_of_2": ([9, 600, 33, 77, 0, 300], [1, 8, 3, 5, 100, 2], 4, 4, 128, 520, "f16", 0.0),
+    "mixed_tiles_of_4": ([9, 600, 33, 77, 0, 300], [2, 1, 2, 1, 50, 2], 12, 3, 128, 520, "bf16", 0.0),
+    "mixed_tiles_of_4_d64": ([9, 600, 33, 77, 0, 300], [1, 8, 3, 5, 100, 2], 4, 4, 64, 520, "f16", 30.0),
+    "mixed_d256": ([9, 600, 33], [1, 3, 2], 3, 3, 256, 1024, "f16", 0.0),
     "mixed_mha": ([9, 600, 0, 77, 0, 300], [1, 1, 90, 1, 400, 33], 4, 4, 128, 520, "f16", 0.0),
 }
 

@@ -89,3 +89,68 @@ def test_rotary_frequencies_of_each_scaling():
                 dict(rot_dim=64, scaling="other"), dict(rot_dim=64, base=1.0), dict(rot_dim=2, scaling="base")):
         with pytest.raises(ValueError):
             rotary.inv_freq(**bad)
+
+
+# ---- caches held in 4 bits ------------------------------------------------------------
+
+
+def test_4_bit_caches_refuse_what_16_bit_ones_do(S):
+    pool = S.Pool(64, 256, "f16", [(8, 8)], 1, 1, max_tokens=4)
+    with pytest.raises(ValueError):
+        S.KVCache(pool, 1, 4, 4, 64, 2, 8, bits=4)
+    for call in (lambda: S.slora_kv_q4_create(pool.handle, 1, 4, 4, 64, 2, 8, 16, 16),
+                 lambda: S.slora_kv_q4_array_ints(pool.handle, 1, 4, 4, 64, 2, 8),
+                 lambda: S.slora_kv_q4_create(0, 1, 4, 4, 64, 2, 8, 16, 16),
+                 lambda: S.slora_kv_q4_array_ints(0, 1, 4, 4, 64, 2, 8),
+                 lambda: S.slora_kv_read(0, 0, 1, 16, 16, 16, 8, 32, 8)):
+        with pytest.raises(S.SloraError) as e:
+            call()
+        assert e.value.code == S.ERR_INVALID
+    for bits in (2, 8, 5, 0):
+        with pytest.raises(ValueError):
+            S.KVCache(pool, 1, 4, 4, 64, 2, 8, bits=bits)
+    pool.close()
+
+
+def test_tokens_per_page(S):
+    assert S.tokens_per_page(4096, 32, 128) == 1 and S.tokens_per_page(4096, 32, 128, 4) == 3
+    assert S.tokens_per_page(5120, 8, 128) == 5 and S.tokens_per_page(5120, 8, 128, 4) == 17
+    assert S.tokens_per_page(40, 1, 80, 4) == 1          # 54 bytes, rounded up to 64, in a page of 80
+    assert S.tokens_per_page(24, 1, 80, 4) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_oracle_quantiser(dtype):
+    """The format by hand, and its bounds on random groups."""
+    from oracle import kv_q4 as oq4
+
+    x = np.zeros((1, 32))
+    x[0, :6] = [8.0, -8.0, 0.5, -0.5, 0.49, 7.6]
+    k, M = oq4.quantise(x, dtype)                        # both signs reach 8: the positive one
+    assert M[0, 0] == 8.0 and k[0, :6].tolist() == [8, -7, 1, 0, 0, 8]
+    assert oq4.values(k, M, 32)[0, :6].tolist() == [8.0, -7.0, 1.0, 0.0, 0.0, 8.0]
+    k, M = oq4.quantise(-x[:, [0, 2, 5] + list(range(6, 32)) + [6, 7, 8]], dtype)
+    assert M[0, 0] == -8.0 and k[0, :3].tolist() == [8, 1, 8]
+    assert oq4.scale(1.0, dtype) == 1.0 and oq4.scale(1.03, dtype) == 1.0625 and oq4.scale(-33.0, dtype) == -34.0
+    assert oq4.scale(1e30, "f16") == 63488.0 and oq4.scale(1e-9, "f16") == 2.0 ** -21 and oq4.scale(0.0, dtype) == 0.0
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((40, 96)) * np.exp(rng.uniform(-6, 6, (40, 1)))
+    k, M = oq4.quantise(x, dtype)
+    assert k.min() >= -7 and k.max() <= 8 and (np.abs(x).reshape(40, 3, 32).max(-1) <= np.abs(M)).all()
+    err, big = np.abs(oq4.values(k, M, 96) - x), np.repeat(np.abs(M), 32, -1)
+    same = np.sign(x) == np.sign(np.repeat(M, 32, -1))
+    assert (err <= np.where(same, big / 16, big / 8) * (1 + 1e-12)).all()
+    held = oq4.values(k, M, 96)                          # eight significant bits: both types hold it
+    assert np.array_equal(held, np.round(held / 2.0 ** np.floor(np.log2(np.abs(held) + (held == 0)) - 7))
+                          * 2.0 ** np.floor(np.log2(np.abs(held) + (held == 0)) - 7))
+    for is_value in (False, True):
+        rows = oq4.pack(k[None], M[None], dtype, is_value)
+        assert rows.shape == (1, oq4.row_bytes(40, 96)) and np.array_equal(oq4.unpack(rows, 40, 96, dtype, is_value)[0], held)
+    # where the header says that codes lie: element 37 = 32 + 5 of a head of 96
+    k = np.zeros((1, 1, 96), np.int64) - 7
+    k[0, 0, 37] = 8
+    M = np.ones((1, 1, 3))
+    row = oq4.pack(k, M, dtype, False)[0, :48].view("<u4")
+    assert row[0 * 3 + 1] == 15 << (16 * 1 + 4 * 2) and (np.delete(row, 1) == 0).all()
+    row = oq4.pack(k, M, dtype, True)[0, :48].view("<u2")
+    assert row[1 * 3 + 1] == 15 << (4 * 1) and (np.delete(row, 4) == 0).all()

@@ -25,3 +25,22 @@ def test_attention_trace_on_a_planning_pool_keeps_the_pool_calls():
         trace.Trace(dataclasses.replace(sp, attention=True, kv_pages_per_token=2 * sp.layers + 1))
     plain.close()
     with_kv.close()
+
+
+def test_4_bit_trace_on_a_planning_pool_takes_fewer_pages():
+    sp = small_spec(steps=60)
+    sp = dataclasses.replace(sp, attention=True, head_dim=64)
+    a, b = (trace.Trace(dataclasses.replace(sp, kv_bits=bits)) for bits in (16, 4))
+    ra, rb = a.run(), b.run()
+    P = b.spec.kv_tokens_per_page
+    assert P > 1 and a.spec.kv_tokens_per_page == 1
+    for tr in (a, b):
+        need = lambda n: -(-n // tr.spec.kv_tokens_per_page) * sp.kv_pages_per_token
+        taken = sorted(tr.kv[rq.kv_handles[0]].shape[0] for rq in tr.running)
+        assert taken == sorted(need(rq.prompt + rq.output) for rq in tr.running)
+    assert rb.peak_kv_pages * (P - 1) < ra.peak_kv_pages * P
+    a.close()
+    b.close()
+    for bad in (dict(kv_bits=8), dict(kv_bits=4, attention=False)):
+        with pytest.raises(ValueError):
+            trace.Trace(dataclasses.replace(sp, **bad))
