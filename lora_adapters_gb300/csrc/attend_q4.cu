@@ -37,6 +37,7 @@ namespace {
 // Warps of a CTA: one for each of the neighbouring key heads that it works on, at most
 // kMaxAbreast; and as many CTAs an SM as make q4_warps.
 constexpr int kMaxAbreast = 6;
+__host__ __device__ constexpr int q4_rounded(int ng) { return ng <= 2 ? 2 : ng <= 4 ? 4 : 8; }
 constexpr int q4_warps(int ng) { return ng <= 4 ? 12 : 6; }   // an SM: 170 or 255 registers a thread
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
@@ -85,9 +86,6 @@ __device__ __forceinline__ uint32_t lds_half(uint32_t at) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
   return v;
 }
-__device__ __forceinline__ void sts_half(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void sts(uint32_t at, const uint32_t (&w)[N]) {
 #pragma unroll
@@ -121,7 +119,7 @@ __host__ __device__ __forceinline__ int stage_bytes(int heads, int ng) {
 }
 template <int NG>
 __host__ __device__ __forceinline__ int ring_bytes(int heads, int ng) {
-  return Ring<NG>::kStages * stage_bytes<NG>(heads, ng) + 4 * Ring<NG>::kRows;
+  return Ring<NG>::kStages * stage_bytes<NG>(heads, ng) + 4 * Ring<NG>::kRows + heads * Ring<NG>::kUnit * 2 * NG;
 }
 
 // D = A B + C.  Not volatile: the compiler may place products that do not depend on each
@@ -134,22 +132,23 @@ __device__ __forceinline__ void mma_h(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// NG: groups of a head, rounded up to 2, 4 or 8 (FULL: just as many); RT: rows that have
-// columns of their own.
-template <class E, int NG, int RT, bool CAP, bool FULL>
-__global__ void __launch_bounds__(kMaxAbreast * 32, q4_warps(NG) / kMaxAbreast)
+// NC: groups of a head, NG: rounded up to 2, 4 or 8; RT: rows that have columns of their own.
+template <class E, int NC, int RT, bool CAP>
+__global__ void __launch_bounds__(kMaxAbreast * 32, q4_warps(NC) / kMaxAbreast)
 kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
+  constexpr int NG = q4_rounded(NC), ng = NC, W = NG / 2;      // W: words of a token's scales
+  constexpr bool FULL = NC == NG;
   constexpr int GC = 8 / RT;        // groups whose weights lie side by side
-  constexpr int PASS = NG / GC;     // sets of weights a token has
+  constexpr int PASS = (NC + GC - 1) / GC;             // sets of weights a token has
   constexpr int NR = RT == 8 ? 2 : 1;                  // rows of a lane
   using R = Ring<NG>;
   constexpr int UNIT = R::kUnit, NS = UNIT / 16;
-  constexpr int NO = RT == 2 ? NG / 2 : NG;            // groups of a lane's results
+  constexpr int NO = RT == 2 ? NG / 2 : NC;            // groups of a lane's results
   constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;       // of a weight
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const KvDev& d = a.kv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ng = d.groups;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // a group of CTAs takes the same units of hbw neighbouring heads, one head a warp
   const int heads = blockDim.x >> 5, hbw = a.hbw, blocks = d.heads_kv / hbw, ctas = hbw / heads;
   const int grp = blockIdx.x / ctas, hsub0 = (blockIdx.x - grp * ctas) * heads, hsub = hsub0 + warp;
@@ -290,17 +289,27 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     return valid;
   };
   // Scales of a token from the ring.
-  auto token_scales = [&](uint32_t at, uint32_t (&w)[NG / 2]) {
+  auto token_scales = [&](uint32_t at, uint32_t (&w)[W]) {
     if constexpr (FULL) {
-      lds<NG / 2>(at, w);
-    } else {
+      lds<W>(at, w);
+    } else {                         // perhaps from the middle of a word on
+      uint32_t v[W] = {};
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t h = g < ng ? lds_half(at + 2 * g) : 0u;
-        w[g / 2] = g & 1 ? w[g / 2] | h << 16 : h;
+      for (int i = 0; i < (NC + 1) / 2; ++i) {
+        uint32_t x[1];
+        lds<1>((at & ~3u) + 4 * i, x);
+        v[i] = x[0];
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        w[i] = at & 2 ? v[i] >> 16 | (i + 1 < W ? v[i + 1] << 16 : 0u) : v[i];
+        if (2 * i >= NC) w[i] = 0;
+        if (2 * i + 1 == NC) w[i] &= 0xffffu;
       }
     }
   };
+  // the values' scales as fp16 times 2^(7 - E), a warp's own
+  const uint32_t my_scales = rows_at + 4 * R::kRows + warp * (UNIT * 2 * NG);
   // units 0 .. kAhead published, all but the last of them on their way, the next looked up
   constexpr int kAhead = R::kStages - 1;
   Pages next;
@@ -331,17 +340,17 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
     const int ctx = len - rq.y;
     // ---- this tile's queries: column n has row n / GC, (token, head of the group).  Eight
     // elements of every group a lane, in the order of K's codes
-    uint32_t qf[NG][4];
-    float c_first[NG][NR], fac[NR];
+    uint32_t qf[NC][4];
+    float c_first[NC][NR], fac[NR];
     {
       const int row = rt * RT + nn / GC;
       const bool in = row < rows;
       const uint16_t* src = a.q + (int64_t)dbg_index(q0 + (in ? row / group : 0), a.T, d.error) * a.ldq +
                             (int64_t)(hk * group + (in ? row % group : 0)) * dim;
       float top = 0.f;
-      uint4 raw[NG];
+      uint4 raw[NC];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int g = 0; g < NC; ++g) {
         const int e = 32 * g + 8 * kk;
         raw[g] = make_uint4(0, 0, 0, 0);
         if (in && e < dim) raw[g] = *reinterpret_cast<const uint4*>(src + e);
@@ -358,7 +367,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       const float size = __uint_as_float((uint32_t)(127 + min(e, 127)) << 23);
       const float down = CAP ? fminf(size * 256.f, 0x1p127f) : size * (256.f * sc);      // 2^(8 + e)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int g = 0; g < NC; ++g) {
         float x[8], sum = 0.f;
         unpack8<E>(raw[g], x);
 #pragma unroll
@@ -415,7 +424,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       float s[2 * NS][NR];
 #pragma unroll
       for (int x = 0; x < 2 * NS; x += 2) {
-        uint32_t kf[2][NG], km[2][NG / 2];
+        uint32_t kf[2][NG], km[2][W];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int t = nn + 8 * (x + z);
@@ -423,9 +432,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             lds<NG>(my_k + t * 16 * NG + kk * 4 * NG, kf[z]);
           } else {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              uint32_t w[1] = {0u};
-              if (g < ng) lds<1>(my_k + t * 16 * NG + (kk * ng + g) * 4, w);
+            for (int g = 0; g < NC; ++g) {
+              uint32_t w[1];
+              lds<1>(my_k + t * 16 * NG + (kk * NC + g) * 4, w);
               kf[z][g] = w[0];
             }
           }
@@ -433,21 +442,21 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         }
 #pragma unroll
         for (int y = 0; y < NR; ++y) s[x][y] = s[x + 1][y] = 0.f;
-        float acc[NG][4];
+        float acc[NC][4];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NC; ++g) {
           const uint32_t w0 = kf[0][g], w1 = kf[1][g], h0 = w0 >> 8, h1 = w1 >> 8;
           mma_h(acc[g], w0 & kLow, w1 & kLow, h0 & kLow, h1 & kLow, qf[g][0], qf[g][1], c_first[g][0], c_first[g][NR - 1],
                 c_first[g][0], c_first[g][NR - 1]);
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NC; ++g) {
           const uint32_t w0 = kf[0][g], w1 = kf[1][g], h0 = w0 >> 8, h1 = w1 >> 8;
           mma_h(acc[g], w0 & kHigh, w1 & kHigh, h0 & kHigh, h1 & kHigh, qf[g][2], qf[g][3], acc[g][0], acc[g][1], acc[g][2],
                 acc[g][3]);
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NC; ++g) {
           const float2 M0 = Elem<E>::to2(km[0][g / 2]), M1 = Elem<E>::to2(km[1][g / 2]);
 #pragma unroll
           for (int y = 0; y < NR; ++y) {
@@ -482,13 +491,10 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         n[y] = fmaxf(n[y], m[y]);
       }
       // the unit's largest |M|, of any group and token
-      uint32_t bits = 0, vm[NG / 2];
-      const uint32_t my_scales = here + at_vs + (lane & (UNIT - 1)) * scale_size + at_scales;
-      token_scales(my_scales, vm);
+      uint32_t bits = 0, vm[W];
+      token_scales(here + at_vs + (lane & (UNIT - 1)) * scale_size + at_scales, vm);
 #pragma unroll
-      for (int g = 0; g < NG / 2; ++g) {
-        bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
-      }
+      for (int g = 0; g < W; ++g) bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
       bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
       const int e_new = max(top_m, Elem<E>::kBf16 ? (int)(bits >> 7) - 126 : (int)(bits >> 10) - 14);
       bool grown = e_new != top_m;
@@ -531,30 +537,31 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       // ---- the token's scales times 2^(7 - E) in fp16, and results
       const float m_up = __uint_as_float((uint32_t)(127 + 7 - top_m) << 23);
 #pragma unroll
-      for (int g = 0; g < NG / 2; ++g) {
+      for (int g = 0; g < W; ++g) {
         const float2 M = Elem<E>::to2(vm[g]);
         vm[g] = Elem<__half>::from2(M.x * m_up, M.y * m_up);
       }
-      __syncwarp();                // (UNIT = 16: two lanes have one token)
-      if constexpr (FULL) {
-        sts<NG / 2>(my_scales, vm);
-      } else {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          if (g < ng) sts_half(my_scales + 2 * g, g & 1 ? vm[g / 2] >> 16 : vm[g / 2]);
-      }
+      __syncwarp();                // (the last unit's are read)
+      sts<W>(my_scales + (lane & (UNIT - 1)) * 2 * NG, vm);
       __syncwarp();
-      uint32_t vf[4 * NS][NG / 2];
+      uint32_t vf[4 * NS][W];
 #pragma unroll
       for (int y = 0; y < 4 * NS; ++y) {
         const int t = (y >> 2) * 16 + 2 * kk + (y & 1) + (y & 2) * 4;
         if constexpr (FULL) {
-          lds<NG / 2>(my_v + R::v_piece(t, nn * NG / 8) + nn * 2 * NG % 16, vf[y]);
+          lds<W>(my_v + R::v_piece(t, nn * NG / 8) + nn * 2 * NG % 16, vf[y]);
+        } else if constexpr (NC == 3) {                  // 6 bytes: two words, from the first's middle for odd nn
+          uint32_t w0[1], w1[1];
+          const int at = nn * 6 & ~3;
+          lds<1>(my_v + R::v_piece(t, at >> 4) + (at & 15), w0);
+          lds<1>(my_v + R::v_piece(t, (at + 4) >> 4) + ((at + 4) & 15), w1);
+          vf[y][0] = nn & 1 ? w0[0] >> 16 | w1[0] << 16 : w0[0];
+          vf[y][1] = nn & 1 ? w1[0] >> 16 : w1[0];
         } else {
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const int at = (nn * ng + g) * 2;
-            const uint32_t h = g < ng ? lds_half(my_v + R::v_piece(t, at >> 4) + (at & 15)) : 0u;
+          for (int g = 0; g < NC; ++g) {
+            const int at = (nn * NC + g) * 2;
+            const uint32_t h = lds_half(my_v + R::v_piece(t, at >> 4) + (at & 15));
             vf[y][g / 2] = g & 1 ? vf[y][g / 2] | h << 16 : h;
           }
         }
@@ -565,12 +572,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 #pragma unroll
         for (int x = 0; x < 2 * NS; ++x) {
           // the scales of the lane's two columns
+          // the scales of the lane's two columns
           uint32_t w1[1];
-          if constexpr (!FULL) {
-            // (RT is 8: one group's scale, perhaps in the middle of a word)
-            const uint32_t h = ps < ng ? lds_half(here + at_vs + (nn + 8 * x) * scale_size + at_scales + ps * 2) : 0u;
-            w1[0] = h | h << 16;
-          } else lds<1>(here + at_vs + (nn + 8 * x) * scale_size + at_scales + (RT == 8 ? ps / 2 : RT == 4 ? ps : 2 * ps + (kk & 1)) * 4, w1);
+          lds<1>(my_scales + (nn + 8 * x) * 2 * NG + (RT == 8 ? ps / 2 : RT == 4 ? ps : 2 * ps + (kk & 1)) * 4, w1);
           const uint32_t w = RT == 8 ? __byte_perm(w1[0], w1[0], ps & 1 ? 0x3232 : 0x1010) : w1[0];
           const float2 mf = Elem<__half>::to2(w);
           if constexpr (RT == 8) {
@@ -578,7 +582,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
             lg[ps][NR - 1] = fmaf(p[x][NR - 1], mf.x, lg[ps][NR - 1]);
           } else {
             lg[2 * ps][0] = fmaf(p[x][0], mf.x, lg[2 * ps][0]);
-            lg[2 * ps + 1][0] = fmaf(p[x][0], mf.y, lg[2 * ps + 1][0]);
+            if (2 * ps + 1 < NO) lg[(2 * ps + 1) % NO][0] = fmaf(p[x][0], mf.y, lg[(2 * ps + 1) % NO][0]);
           }
           const uint32_t hi = h2_mul(ph[x], w);
           bh[x] = trans8x8(hi);
@@ -588,6 +592,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 #pragma unroll
         for (int gi = 0; gi < GC; ++gi) {
           const int g = ps * GC + gi;
+          if (g >= NC) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[gi][i >> 2][i & 3] = 0.f;
+            continue;
+          }
 #pragma unroll
           for (int s2 = 0; s2 < NS; ++s2) {
             const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
@@ -682,16 +691,17 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <class E, int NG, int RT, bool FULL = true>
+template <class E, int NC, int RT>
 cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStream_t st) {
+  constexpr int NG = q4_rounded(NC);
   // heads of a CTA, and as many neighbouring ones at a time as up to 16 that several CTAs share
   int heads = kMaxAbreast;
   while (a.kv.heads_kv % heads) --heads;
   a.hbw = std::max(1, 16 / heads) * heads;
   while (a.kv.heads_kv % a.hbw) a.hbw -= heads;
-  const int grid = num_sms * (q4_warps(NG) / heads), smem = ring_bytes<NG>(heads, a.kv.groups);
+  const int grid = num_sms * (q4_warps(NC) / heads), smem = ring_bytes<NG>(heads, NC);
   const int threads = heads * 32;
-  auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NG, RT, true, FULL> : kv_q4_decode_kernel<E, NG, RT, false, FULL>;
+  auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NC, RT, true> : kv_q4_decode_kernel<E, NC, RT, false>;
   cudaError_t e;
   if (after_chunks) {
     e = launch_early(kernel, dim3(grid), threads, smem, st, a);
@@ -702,48 +712,56 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
   if (e != cudaSuccess) return e;
   return launch_kv_q4_join(a, Elem<E>::kBf16 ? 1 : 0, num_sms, after_chunks, grid / (a.hbw / heads), st);
 }
-template <class E>
-cudaError_t launch_decode(const KvAttendArgs& a, int num_sms, bool after_chunks, cudaStream_t st) {
-  const int ng = a.kv.groups, rt = a.row_tile;       // kv_q4_row_tile
-  switch (ng) {
-    case 1: return launch_rows<E, 2, 8, false>(a, num_sms, after_chunks, st);
-    case 2: return rt == 4 ? launch_rows<E, 2, 4>(a, num_sms, after_chunks, st) : launch_rows<E, 2, 8>(a, num_sms, after_chunks, st);
-    case 3: return launch_rows<E, 4, 8, false>(a, num_sms, after_chunks, st);
-    case 4:
-      return rt == 2   ? launch_rows<E, 4, 2>(a, num_sms, after_chunks, st)
-             : rt == 4 ? launch_rows<E, 4, 4>(a, num_sms, after_chunks, st)
-                       : launch_rows<E, 4, 8>(a, num_sms, after_chunks, st);
-    case 8: return rt == 2 ? launch_rows<E, 8, 2>(a, num_sms, after_chunks, st) : launch_rows<E, 8, 8>(a, num_sms, after_chunks, st);
-    default: return launch_rows<E, 8, 8, false>(a, num_sms, after_chunks, st);
-  }
-}
-
-template <class E, int NG, int RT, bool FULL = true>
-cudaError_t prepare() {
-  for (auto k : {kv_q4_decode_kernel<E, NG, RT, false, FULL>, kv_q4_decode_kernel<E, NG, RT, true, FULL>})
+template <class E, int NC, int RT>
+cudaError_t prepare_rows() {
+  for (auto k : {kv_q4_decode_kernel<E, NC, RT, false>, kv_q4_decode_kernel<E, NC, RT, true>})
     if (cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             ring_bytes<NG>(kMaxAbreast, NG) + 1024))
+                                             ring_bytes<q4_rounded(NC)>(kMaxAbreast, NC) + 1024))
       return e;
   return cudaSuccess;
 }
+// What there is for a number of groups and a row tile (kv_q4_row_tile).
 template <class E>
-cudaError_t prepare_all() {
-  for (auto f : {prepare<E, 2, 4>, prepare<E, 2, 8>, prepare<E, 4, 2>, prepare<E, 4, 4>, prepare<E, 4, 8>, prepare<E, 8, 2>,
-                 prepare<E, 8, 8>, prepare<E, 2, 8, false>, prepare<E, 4, 8, false>, prepare<E, 8, 8, false>})
-    if (cudaError_t e = f()) return e;
+struct Rows {
+  cudaError_t (*launch)(KvAttendArgs, int, bool, cudaStream_t);
+  cudaError_t (*prepare)();
+  template <int NC, int RT>
+  static constexpr Rows of() { return {launch_rows<E, NC, RT>, prepare_rows<E, NC, RT>}; }
+  static Rows get(int groups, int tile) {
+    switch (groups * 16 + tile) {
+      case 2 * 16 + 4: return of<2, 4>();
+      case 2 * 16 + 8: return of<2, 8>();
+      case 3 * 16 + 2: return of<3, 2>();
+      case 3 * 16 + 4: return of<3, 4>();
+      case 3 * 16 + 8: return of<3, 8>();
+      case 4 * 16 + 2: return of<4, 2>();
+      case 4 * 16 + 4: return of<4, 4>();
+      case 4 * 16 + 8: return of<4, 8>();
+      case 5 * 16 + 8: return of<5, 8>();
+      case 6 * 16 + 8: return of<6, 8>();
+      case 7 * 16 + 8: return of<7, 8>();
+      case 8 * 16 + 2: return of<8, 2>();
+      case 8 * 16 + 8: return of<8, 8>();
+      default: return of<1, 8>();
+    }
+  }
+};
+template <class E>
+cudaError_t prepare_all(int groups) {
+  for (int tile : {2, 4, 8})
+    if (cudaError_t e = Rows<E>::get(groups, tile).prepare()) return e;
   return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t prepare_kv_q4_decode_kernels() {
-  if (cudaError_t e = prepare_all<__half>()) return e;
-  return prepare_all<__nv_bfloat16>();
+cudaError_t prepare_kv_q4_decode_kernels(int dtype, int groups) {
+  return dtype == 0 ? prepare_all<__half>(groups) : prepare_all<__nv_bfloat16>(groups);
 }
 
 cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st) {
-  return dtype == 0 ? launch_decode<__half>(a, num_sms, after_chunks, st)
-                    : launch_decode<__nv_bfloat16>(a, num_sms, after_chunks, st);
+  return dtype == 0 ? Rows<__half>::get(a.kv.groups, a.row_tile).launch(a, num_sms, after_chunks, st)
+                    : Rows<__nv_bfloat16>::get(a.kv.groups, a.row_tile).launch(a, num_sms, after_chunks, st);
 }
 
 }  // namespace slora

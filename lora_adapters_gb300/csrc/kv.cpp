@@ -218,7 +218,7 @@ int create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, bool q4, 
   kv->per_page_div.set((uint32_t)d.per_page);
   auto setup = [&]() -> int {
     CUDA_TRY(prepare_kv_kernels());
-    if (q4) CUDA_TRY(prepare_kv_q4_decode_kernels());
+    if (q4) CUDA_TRY(prepare_kv_q4_decode_kernels(pv.dtype, d.groups));
     else CUDA_TRY(prepare_kv_decode_kernels());
     CUDA_TRY(cudaMalloc(&kv->d_freq, sizeof(uint64_t) * (size_t)(c->head_dim / 2)));
     const int64_t parts = kv_attend_parts(pv.num_sms);

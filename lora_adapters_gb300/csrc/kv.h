@@ -31,9 +31,9 @@ constexpr int kKvChunkRows = kKvRowTile;
 // up to kKvChunkRows, but mostly have one new token, `group` rows.
 inline int32_t kv_q4_row_tile(int32_t groups, int32_t group, int64_t rows, bool chunks) {
   const int64_t most = chunks ? group : rows;
-  if (groups % 2 || groups == 6 || most > 4) return kKvRowTile;
+  if (groups == 1 || (groups > 4 && groups < 8) || most > 4) return kKvRowTile;
   if (groups == 2) return 4;
-  return most <= 2 ? 2 : groups == 4 ? 4 : kKvRowTile;
+  return most <= 2 ? 2 : groups <= 4 ? 4 : kKvRowTile;
 }
 // What a pair of chunk tiles costs besides its key tiles (queries in, results
 // out, the first scores waited for), in key tiles' time: about 6,000 cycles
@@ -181,7 +181,7 @@ cudaError_t launch_kv_q4_chunk(const KvAttendArgs& a, int dtype, int num_sms, cu
 cudaError_t launch_kv_q4_join(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, int64_t groups,
                               cudaStream_t st);
 // The same over a 4-bit cache.
-cudaError_t prepare_kv_q4_decode_kernels();
+cudaError_t prepare_kv_q4_decode_kernels(int dtype, int groups);
 cudaError_t launch_kv_q4_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
 
 // What kv.cpp uses of a pool (pool.cpp).

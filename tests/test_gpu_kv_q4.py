@@ -382,6 +382,13 @@ ATTEND = {
     "decode_d64": ([12, 90, 257], [1] * 3, 12, 3, 64, 400, "bf16", 0.0),
     "decode_d80": ([12, 90, 257], [1] * 3, 6, 3, 80, 480, "f16", 0.0),
     "decode_d96_mha": ([12, 90, 257], [1] * 3, 3, 3, 96, 480, "f16", 0.0),
+    "decode_d96_group4": ([12, 90, 257], [1] * 3, 12, 3, 96, 480, "bf16", 0.0),
+    "decode_d80_mha5": ([12, 90, 257, 700], [1] * 4, 5, 5, 80, 480, "f16", 0.0),
+    "decode_d80_two": ([12, 90, 257], [2, 1, 2], 3, 3, 80, 480, "bf16", 30.0),
+    "mixed_d96": ([9, 600, 33, 77], [1, 8, 90, 5], 3, 3, 96, 480, "f16", 0.0),
+    "decode_d48": ([12, 90, 257], [1] * 3, 4, 4, 48, 480, "f16", 0.0),
+    "decode_d176": ([12, 90, 257], [1] * 3, 4, 2, 176, 800, "bf16", 0.0),
+    "decode_d224": ([12, 90, 257], [1] * 3, 3, 3, 224, 800, "f16", 0.0),
     "decode_d256": ([12, 90, 257], [1] * 3, 4, 2, 256, 1536, "bf16", 20.0),
     "decode_d256_mha": ([12, 90, 257], [1] * 3, 2, 2, 256, 1536, "f16", 0.0),
     "decode_d240": ([12, 90, 257], [1] * 3, 8, 1, 240, 700 // 8 * 8, "f16", 0.0),
