@@ -15,7 +15,9 @@ namespace {
 
 // ================================================================ append
 // Norm and rotation as in kv.cu, a warp per token and share of its heads, eight
-// consecutive elements a lane; a group is four lanes.
+// consecutive elements a lane; a group is four lanes.  Bound: instructions, about 150 a
+// lane's eight quantised elements: 8090 tokens of 56 heads, normed, half of each head
+// turned, 64 us (181 MB, 60 % of the issue slots); 256 tokens of 96 heads 12.
 //
 // Codes are those of the formula in exact arithmetic, not of its fp32 evaluation:
 //  - a value that comes straight from 16 bits has at most 11 significant bits, a
@@ -150,18 +152,23 @@ __device__ __noinline__ uint32_t exact_codes(const Exact ex, uint4 r, const floa
   return word;
 }
 
+__device__ __forceinline__ float rcp(float x) {     // to one unit of the last place
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float e) {   // of codes k, the first lowest
   return __float_as_uint(fmaf(fmaf(fmaf(e, 16.f, c), 16.f, b), 16.f, a) + (8388608.f + 0x7777));
 }
 // The codes k of x (inv = 8 / M, bump: by how much 8 x / M is raised), and in d how far
-// they are from it before they are held within -7 .. 8.
+// they are from it before they are held above -8.
 __device__ __forceinline__ void round8(const float (&x)[8], float inv, float bump, float (&k)[8], float (&d)[8]) {
   constexpr float kInt = 12582912.f;               // 1.5 * 2^23: adding it rounds to an integer
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float t = fmaf(x[e], inv, bump), r = (t + kInt) - kInt;
     d[e] = r - t;
-    k[e] = fminf(fmaxf(r, -7.f), 8.f);
+    k[e] = fmaxf(r, -7.f);                         // (above 8 only where M is the type's largest)
   }
 }
 
@@ -210,9 +217,11 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
   }
   constexpr int kPer = Lane::kPerWarp;
   const int nq = (d.heads_q + kPer - 1) / kPer, nk = (d.heads_kv + kPer - 1) / kPer;
-  const int iters = nq + 2 * nk, i0 = iters * part / a.parts, i1 = iters * (part + 1) / a.parts;
+  // a share of the queries, of the keys and of the values: a key costs about three queries
+  const int q0 = nq * part / a.parts, q1 = nq * (part + 1) / a.parts, k0 = nk * part / a.parts,
+            k1 = nk * (part + 1) / a.parts;
   const int at = (ln.lane / G) * D + ln.li * 8, step = kPer * D;
-  ln.template run<true>(a.q + (int64_t)t * a.ldq + at, a.q_out + (int64_t)t * a.ldqo + at, i0, min(i1, nq), d.heads_q, step,
+  ln.template run<true>(a.q + (int64_t)t * a.ldq + at, a.q_out + (int64_t)t * a.ldqo + at, q0, q1, d.heads_q, step,
                         s_w[0] + ln.li * 8);
   // ---- keys, then values
   const int ng = d.groups, g = ln.li >> 2, k4 = ln.li & 3;
@@ -226,6 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
   // the lane's and its group's error bound, in the head's largest element
   const bool group_err = NORM || (ln.li & ~3) < 2 * half;
   constexpr float kErr = NORM ? kErrNormed : kErrTurned;
+  constexpr float kFinest = Elem<E>::kBf16 ? 0x1p-100f : 0x1p-21f, kLargest = Elem<E>::kBf16 ? 31.f * 0x1p123f : 31.f * 0x1p11f;
   const float my_err = NORM || ln.turned ? kErr : 0.f, bump = NORM || ln.turned ? 0.f : 0x1p-15f;
   Exact ex;
   ex.freq = a.freq;
@@ -260,24 +270,36 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
         }
         const float m = hi >= -lo ? hi : lo, am = fabsf(m);
         float M = copysignf(q4_scale<E>(am), m), top = am;
+        float inv = M == 0.f ? 0.f : rcp(M) * 8.f;
         if (!kValue) {
 #pragma unroll
           for (int o = 4; o < G; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));    // the head's largest
+          // M may round otherwise where am lies within its error of a number of five bits: in
+          // units of its last place, at most 2^24 err / am, and am >= 16 / 17 |M|.  (Below 32
+          // units of the finest M its rounding is another: always asked)
           const float err = group_err ? kErr * top : 0.f;
+          const uint32_t ulps = (uint32_t)fminf(err * fabsf(inv) * (0x1p21f * 1.07f) + 2.f, 0x1p18f);
           const bool scale = err > 0.f && am <= 3.402823466e38f &&
-                             (q4_scale<E>(am + err) != q4_scale<E>(fmaxf(am - err, 0.f)) || fabsf(hi + lo) <= 2.f * err);
+                             (((__float_as_uint(am) + ulps) & 0x7ffffu) < 2 * ulps || am < 32.f * kFinest ||
+                              fabsf(hi + lo) <= 2.f * err);
           if (__any_sync(0xffffffffu, scale)) {
             uint32_t largest = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (scale && fabsf(x[e]) >= am - 2.f * err) largest |= 1u << e;
             const float f = exact_scale<E, NORM, INTER, G>(ex, raw[j], kw, largest);
-            if (scale) M = f;
+            if (scale) {
+              M = f;
+              inv = M == 0.f ? 0.f : rcp(M) * 8.f;
+            }
           }
         }
-        const float inv = M == 0.f ? 0.f : 8.f / M;
         float k[8], off[8];
         round8(x, inv, kValue ? 0x1p-15f : bump, k, off);
+        if (__any_sync(0xffffffffu, am > kLargest)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) k[e] = fminf(k[e], 8.f);
+        }
         uint32_t word;
         if (kValue) {
           const uint32_t a0 = nibbles(k[0], k[1], k[2], k[3]), a1 = nibbles(k[4], k[5], k[6], k[7]);
@@ -310,8 +332,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
       }
     }
   };
-  heads(a.k + (int64_t)t * a.ldk + at, row_of(ks), max(i0 - nq, 0), min(i1 - nq, nk), std::false_type{});
-  heads(a.v + (int64_t)t * a.ldv + at, row_of(vs), max(i0 - nq - nk, 0), i1 - nq - nk, std::true_type{});
+  heads(a.k + (int64_t)t * a.ldk + at, row_of(ks), k0, k1, std::false_type{});
+  heads(a.v + (int64_t)t * a.ldv + at, row_of(vs), k0, k1, std::true_type{});
 }
 
 template <class E, bool NORM, bool INTER>
@@ -401,8 +423,10 @@ void (*read_kernel(int groups))(const KvReadArgs) {
 cudaError_t launch_kv_q4_append(const KvAppendArgs& args, int dtype, int num_sms, cudaStream_t st) {
   KvAppendArgs a = args;
   const int lanes = a.kv.head_dim <= 64 ? 8 : a.kv.head_dim <= 128 ? 16 : 32, per_warp = 32 / lanes;
-  const int iters = (a.kv.heads_q + per_warp - 1) / per_warp + 2 * ((a.kv.heads_kv + per_warp - 1) / per_warp);
-  a.parts = std::max(1, std::min(iters, 16 * num_sms / a.T));
+  // Warps for a token: as many as fill the SMs once, 24 warps each (2084 tokens of 96 heads:
+  // 49 us with one, 34 with two; 962: 22 with four).
+  const int most = (std::max(a.kv.heads_q, a.kv.heads_kv) + per_warp - 1) / per_warp;
+  a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, (24 * (int64_t)num_sms + a.T / 2) / a.T));
   const int64_t warps = (int64_t)a.T * a.parts;
   const int grid = (int)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   auto kernel = dtype == 0 ? append_kernel<__half>(a.qw != nullptr, a.interleaved != 0, lanes)
