@@ -387,6 +387,10 @@ ATTEND = {
     "decode_d80_two": ([12, 90, 257], [2, 1, 2], 3, 3, 80, 480, "bf16", 30.0),
     "mixed_d96": ([9, 600, 33, 77], [1, 8, 90, 5], 3, 3, 96, 480, "f16", 0.0),
     "decode_d48": ([12, 90, 257], [1] * 3, 4, 4, 48, 480, "f16", 0.0),
+    "decode_d32": ([12, 90, 257], [1, 3, 2], 8, 2, 32, 480, "bf16", 0.0),
+    "decode_d160": ([12, 90, 257], [1] * 3, 8, 4, 160, 800, "f16", 30.0),
+    "chunk_over_long": ([20000, 300], [40, 9], 8, 2, 128, 1280, "f16", 0.0),
+    "chunk_over_long_d96": ([9000, 1], [60, 200], 6, 3, 96, 1280, "bf16", 0.0),
     "decode_d176": ([12, 90, 257], [1] * 3, 4, 2, 176, 800, "bf16", 0.0),
     "decode_d224": ([12, 90, 257], [1] * 3, 3, 3, 224, 800, "f16", 0.0),
     "decode_d256": ([12, 90, 257], [1] * 3, 4, 2, 256, 1536, "bf16", 20.0),
