@@ -332,7 +332,8 @@ kv_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWideWarps = 16;
 
-// NORMED: the parts' o are divided by their l already, and so is the sum (4-bit caches).
+// NORMED: the parts' o are divided by their l already, and so is the sum (4-bit caches, whose
+// values reach 2^127 in bf16: sums of them over a part's tokens would not be finite).
 template <int V, bool NORMED = false>
 struct JoinSum {
   float m = -INFINITY, l = 0.f, o[V] = {};

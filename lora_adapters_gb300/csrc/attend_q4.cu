@@ -14,18 +14,22 @@
 //    head; the offset 7 sum(q) is the accumulator's first value.  Queries are scaled by
 //    a power of two to below 2^14 first, which fp16's exponents hold for bf16 too (bits
 //    below 2^-24 of a row's largest element are lost);
-//  - V's scale goes into the weights: with every weight as two fp16 parts, p = hi + lo,
-//    and M 2^(7 - E) in fp16 (|M| < 2^E so far), hi M is again two parts, a product and
-//    its exact remainder.  Columns of the product that have no row (fewer than 8 query
-//    rows) take other groups' weights: RT rows times 8 / RT groups fill them, and the
-//    weights of a token are then worked out once instead of once a group;
+//  - V's scale goes into the weights.  bf16 caches have every weight p in one fp16 part:
+//    2^-11 of it, and as much for its product with M 2^(7 - E) (|M| < 2^E so far), are an
+//    eighth of the rounding of a result each.  fp16 caches have two, p = hi + lo, and hi M
+//    is again two parts, a product and its exact remainder.  Columns of the product that
+//    have no row (fewer than 8 query rows) take other groups' weights: RT rows times 8 / RT
+//    groups fill them, and a token's weights are worked out that many times less often;
 //  - each unit's result starts from zero and is added to the running one in fp32: with
 //    codes that are never negative, a running sum in the tensor core would lose bits
 //    to its truncation.
 //
 // Bound: what four issue slots a clock can do for the bytes of a unit.  Per 32 tokens of
 // a head of 128 there are 4,608 bytes, 196 cycles of an SM's share of the memory, against
-// 550 (two rows) to 700 (eight) instructions of a warp.
+// 700 (two rows, weights in two parts) or 810 (eight rows, in one) instructions of a warp,
+// half of them on the integer and logic pipe at half rate.  Measured: 256 requests of 8 to
+// 640 tokens, 32 heads of 128, 111 us (3.5 TB/s of codes and scales; the copies alone 70);
+// 128 requests of 17 to 8192 tokens, 40 heads on 8, 159 us (3.8 TB/s; 105).
 #include <type_traits>
 
 #include "attend.cuh"
@@ -38,7 +42,9 @@ namespace {
 // kMaxAbreast; and as many CTAs an SM as make q4_warps.
 constexpr int kMaxAbreast = 6;
 __host__ __device__ constexpr int q4_rounded(int ng) { return ng <= 2 ? 2 : ng <= 4 ? 4 : 8; }
-constexpr int q4_warps(int ng) { return ng <= 4 ? 12 : 6; }   // an SM: 170 or 255 registers a thread
+// An SM: 170 or 255 registers a thread.  (16 of up to 4 groups, 128 registers: they spill,
+// 185 us instead of 160 for 128 requests of 17 to 8192 tokens, 40 heads on 8.)
+constexpr int q4_warps(int ng) { return ng <= 4 ? 12 : 6; }
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t y;
@@ -99,7 +105,10 @@ __device__ __forceinline__ void sts(uint32_t at, const uint32_t (&w)[N]) {
 template <int NG>
 struct Ring {
   static constexpr int kUnit = NG <= 4 ? 32 : 16;      // kv_q4_unit
-  static constexpr int kStages = 2;
+  // 128 requests of 17 to 2048 tokens, 16 heads of 160: 238 us with 2, 230 with 3; of 192
+  // 227 and 213; of 256 231 and 223 (8 key heads of two rows 123 and 115, of 224 145 and
+  // 154).  256 requests of 8 to 640, 32 heads of 128: 113 and 117.
+  static constexpr int kStages = NG == 8 ? 3 : 2;
   static constexpr int kCodes = kUnit * 16 * NG;       // of a head
   static constexpr int kRows = kUnit * 16 + 16;        // where a unit's rows begin, which are there, the block of heads
   // where 16-byte piece p of token t of V lies
@@ -144,7 +153,10 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   using R = Ring<NG>;
   constexpr int UNIT = R::kUnit, NS = UNIT / 16;
   constexpr int NO = RT == 2 ? NG / 2 : NC;            // groups of a lane's results
-  constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;       // of a weight
+  // Parts of a weight.  256 requests of 8 to 640 tokens, 32 heads of fp16: 113 us with two,
+  // 105 with one, which costs the result's last bit; 128 requests of 17 to 8192, 40 heads
+  // on 8 of bf16: 184 and 164 us.
+  constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const KvDev& d = a.kv;
@@ -167,8 +179,8 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   }
   int left = (int)min(u1 - u, (int64_t)0x7fffffff);
 
-  // The units to do are on their way to shared memory while the two before them are
-  // multiplied, from one segment into the next; their pages are looked up one ahead of that.
+  // Units are on their way to shared memory while the ones before them are multiplied, from
+  // one segment into the next; their pages are looked up one ahead of that.
   struct {
     int left, r, hb, rt, c;        // units left; request, head block, row tile, unit of the segment
     int n, tiles, len;             // units of a segment, row tiles, tokens of the request
@@ -516,7 +528,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           }
         }
       }
-      // ---- weights times 2^7, in two fp16 parts: both rows' or the one row's twice
+      // ---- weights times 2^7, in one or two fp16 parts: both rows' or the one row's twice
       uint32_t ph[2 * NS], pl[2 * NS];
       float p[2 * NS][NR];
 #pragma unroll
@@ -571,7 +583,6 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         uint32_t bh[2 * NS], bl[2 * NS];
 #pragma unroll
         for (int x = 0; x < 2 * NS; ++x) {
-          // the scales of the lane's two columns
           // the scales of the lane's two columns
           uint32_t w1[1];
           lds<1>(my_scales + (nn + 8 * x) * 2 * NG + (RT == 8 ? ps / 2 : RT == 4 ? ps : 2 * ps + (kk & 1)) * 4, w1);
@@ -694,7 +705,10 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
 template <class E, int NC, int RT>
 cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStream_t st) {
   constexpr int NG = q4_rounded(NC);
-  // heads of a CTA, and as many neighbouring ones at a time as up to 16 that several CTAs share
+  // Heads of a CTA, and as many neighbouring ones at a time as up to 16 that several CTAs share:
+  // a head's codes of a token are 64 bytes, and what neighbours read at other times the DRAM
+  // fetches again (32 heads of 128, 256 requests: 119 us with a CTA's heads alone, 113 so; 8 key
+  // heads, 128 long requests: 168 and 164).
   int heads = kMaxAbreast;
   while (a.kv.heads_kv % heads) --heads;
   a.hbw = std::max(1, 16 / heads) * heads;
@@ -737,8 +751,11 @@ struct Rows {
       case 4 * 16 + 2: return of<4, 2>();
       case 4 * 16 + 4: return of<4, 4>();
       case 4 * 16 + 8: return of<4, 8>();
+      case 5 * 16 + 2: return of<5, 2>();
       case 5 * 16 + 8: return of<5, 8>();
+      case 6 * 16 + 2: return of<6, 2>();
       case 6 * 16 + 8: return of<6, 8>();
+      case 7 * 16 + 2: return of<7, 2>();
       case 7 * 16 + 8: return of<7, 8>();
       case 8 * 16 + 2: return of<8, 2>();
       case 8 * 16 + 8: return of<8, 8>();

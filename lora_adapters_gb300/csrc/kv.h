@@ -16,7 +16,9 @@ constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
 constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
 constexpr int kKvUnit = 16;            // tokens of one decode unit
 // The same of a 4-bit cache: twice as many, with the steps of the softmax once for all of
-// them, where registers hold their codes and the result.
+// them, where registers hold their codes and the result (256 requests of 8 to 640 tokens,
+// 32 heads of 128: 113 us with 32 tokens, 129 with 16; 128 of 17 to 8192, 40 heads on 8:
+// 164 and 207).
 inline int32_t kv_q4_unit(int32_t head_dim) { return head_dim <= 128 ? 2 * kKvUnit : kKvUnit; }
 constexpr int kKvTile = 128;           // rows and keys of one chunk tile
 // A request whose new tokens make more rows than this (per key head) goes to the
@@ -28,10 +30,15 @@ constexpr int kKvChunkRows = kKvRowTile;
 // Rows of a decode segment of a 4-bit cache, for a call in which no request has more than
 // `rows` of them: the kernel works a token's weights out 8 / (rows of a tile) times less
 // often with tiles of 2 or 4 (attend_q4.cu).  With chunks in the call the other requests may have
-// up to kKvChunkRows, but mostly have one new token, `group` rows.
+// up to kKvChunkRows, but mostly have one new token, `group` rows.  Tiles by this rule against
+// tiles of 8, 128 requests of 17 to 2048 tokens, one row: 32 heads of 64 111 and 121 us, of
+// 96 166 and 182, 16 of 160 230 and 248, of 192 213 and 235, of 256 223 and 281; two rows,
+// 8 key heads of 224 154 and 182, of 256 115 and 135; four rows, 8 key heads of 64 41 and 45,
+// of 96 57 and 61, of 128 57 and 64 (bf16 51 and 58).  256 requests of 8 to 640, 32 heads of
+// 128: 113 and 133.  One group alone fills no more columns.
 inline int32_t kv_q4_row_tile(int32_t groups, int32_t group, int64_t rows, bool chunks) {
   const int64_t most = chunks ? group : rows;
-  if (groups == 1 || (groups > 4 && groups < 8) || most > 4) return kKvRowTile;
+  if (groups == 1 || most > 4) return kKvRowTile;
   if (groups == 2) return 4;
   return most <= 2 ? 2 : groups <= 4 ? 4 : kKvRowTile;
 }
