@@ -389,6 +389,10 @@ ATTEND = {
     "decode_d48": ([12, 90, 257], [1] * 3, 4, 4, 48, 480, "f16", 0.0),
     "decode_d32": ([12, 90, 257], [1, 3, 2], 8, 2, 32, 480, "bf16", 0.0),
     "decode_d160": ([12, 90, 257], [1] * 3, 8, 4, 160, 800, "f16", 30.0),
+    "decode_seven_heads": ([12, 90, 2570], [1] * 3, 7, 7, 256, 1536, "f16", 0.0),
+    "decode_five_heads": ([12, 900, 2570], [1] * 3, 10, 5, 192, 1280, "bf16", 0.0),
+    "decode_eleven_heads": ([12, 900, 2570], [1, 2, 1], 22, 11, 64, 1280, "f16", 20.0),
+    "decode_thirteen_heads": ([1200, 0, 2570], [1] * 3, 13, 13, 128, 2048, "bf16", 0.0),
     "chunk_over_long": ([20000, 300], [40, 9], 8, 2, 128, 1280, "f16", 0.0),
     "chunk_over_long_d96": ([9000, 1], [60, 200], 6, 3, 96, 1280, "bf16", 0.0),
     "decode_d176": ([12, 90, 257], [1] * 3, 4, 2, 176, 800, "bf16", 0.0),
