@@ -180,8 +180,13 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
   const int tid = threadIdx.x;
   const int D = d.head_dim;
   if (NORM) {
-    for (int i = tid; i < 2 * D; i += kAppendThreads)
-      s_w[i >= D][i >= D ? i - D : i] = Elem<E>::to(i >= D ? a.kw[i - D] : a.qw[i]);
+    // zeros past head_dim: the lanes there have zeros for elements, and where the last group is
+    // half full their products with the weights are among its elements
+    constexpr int kLanes = 8 * G;
+    for (int i = tid; i < 2 * kLanes; i += kAppendThreads) {
+      const int e = i % kLanes;
+      s_w[i / kLanes][e] = e < D ? Elem<E>::to(i < kLanes ? a.qw[e] : a.kw[e]) : 0.f;
+    }
     __syncthreads();
   }
   const int unit = blockIdx.x * (kAppendThreads / 32) + (tid >> 5);     // T * parts < 2^31
