@@ -158,6 +158,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   // on 8 of bf16: 184 and 164 us.
   constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  constexpr uint32_t kNotFinite = Elem<E>::kBf16 ? 0x7f80u : 0x7c00u;    // infinity's bits
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const KvDev& d = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -502,12 +503,22 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         if (!CAP) n[y] *= fac[y];                          // > 0
         n[y] = fmaxf(n[y], m[y]);
       }
-      // the unit's largest |M|, of any group and token
+      // the unit's largest |M|, of any group and token.  Those that are not finite do not count:
+      // against them the other groups' would be zeros (their own products are NaN all the same)
       uint32_t bits = 0, vm[W];
       token_scales(here + at_vs + (lane & (UNIT - 1)) * scale_size + at_scales, vm);
 #pragma unroll
       for (int g = 0; g < W; ++g) bits = __vmaxu2(bits, vm[g] & 0x7fff7fffu);
       bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
+      if (bits >= kNotFinite) {
+        bits = 0;
+#pragma unroll
+        for (int g = 0; g < W; ++g) {
+          const uint32_t lo = vm[g] & 0x7fffu, hi = vm[g] >> 16 & 0x7fffu;
+          bits = max(bits, max(lo < kNotFinite ? lo : 0u, hi < kNotFinite ? hi : 0u));
+        }
+        bits = __reduce_max_sync(0xffffffffu, bits);
+      }
       const int e_new = max(top_m, Elem<E>::kBf16 ? (int)(bits >> 7) - 126 : (int)(bits >> 10) - 14);
       bool grown = e_new != top_m;
 #pragma unroll

@@ -52,3 +52,45 @@ def test_normed_heads_whose_last_group_is_half_full(S, dtype, rot, hkv, d):  # n
             assert np.array_equal(view[slot // s.P, slot % s.P].cpu().numpy()[:used], row[:used]), (t, j)
     other.close()
     s.close()
+
+
+SHAPES = [   # hq, hkv, d: tiles of two, four and eight rows, every number of groups
+    (4, 4, 128), (3, 3, 96), (2, 2, 160), (6, 3, 192), (1, 1, 224), (2, 2, 256),
+    (8, 2, 128), (4, 4, 64), (12, 3, 96), (8, 1, 128), (8, 1, 256), (5, 1, 192), (24, 3, 64), (2, 2, 32)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("new", [1, 60])
+def test_a_value_group_that_is_not_finite_leaves_the_others(S, dtype, hq, hkv, d, new):  # noqa: F811
+    """One token's group of one head's values is NaN: so is that group of the results of that head's
+    queries, and every other element is what it would be without it."""
+    s = Setup(S, [40, 3000, 90], [new, new, 1], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=14)
+    s.oracle_plan()
+    held, ng = s.fill(), oq4.groups(d)
+    where = {}                                     # request: (token, head, group)
+    for r, (p, h, g) in {0: (0, hkv - 1, 0), 1: (1500, 0, ng - 1), 2: (90, hkv - 1, ng // 2)}.items():
+        page, at = (int(x[p]) for x in s.at(r, 0, 1))
+        scale = s.row_view()[page, at, 16 * ng * hkv: 18 * ng * hkv].view(torch.int16)
+        scale[h * ng + g] = 0x7fff
+        held[r][1][p, h, 32 * g: 32 * g + 32] = 0.0
+        where[r] = (h, g)
+    b = s.plan()
+    q, out = s.randn(s.T, hq * d, scale=0.01), torch.empty(s.T, hq * d + 8, dtype=TDT[dtype], device="cuda")
+    out[:, hq * d:] = 3.0
+    s.kv.attend(b, 0, q, out[:, : hq * d])
+    torch.cuda.synchronize()
+    assert s.pool.status() == S.OK
+    t0, group = 0, hq // hkv
+    for r, n in enumerate(s.new):
+        h, g = where[r]
+        bad = torch.zeros(n, hkv, group, d, dtype=torch.bool, device="cuda")
+        bad[:, h, :, 32 * g: 32 * g + 32] = True
+        got = out[t0: t0 + n, : hq * d].unflatten(1, (hkv, group, d))
+        assert torch.equal(got.isnan(), bad), r
+        # (what the group would be without its NaN token: the oracle's, to compare the rest)
+        want = okv.attend(f64(q[t0: t0 + n]).reshape(n, hq, d), *held[r], s.ctx[r], d ** -0.5, 0.0)
+        got[bad] = torch.from_numpy(want).to(got).unflatten(1, (hkv, group))[bad]
+        t0 += n
+    _check(s, held, q, out)
+    s.close()
