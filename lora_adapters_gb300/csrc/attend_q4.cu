@@ -598,15 +598,19 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           uint32_t w1[1];
           lds<1>(my_scales + (nn + 8 * x) * 2 * NG + (RT == 8 ? ps / 2 : RT == 4 ? ps : 2 * ps + (kk & 1)) * 4, w1);
           const uint32_t w = RT == 8 ? __byte_perm(w1[0], w1[0], ps & 1 ? 0x3232 : 0x1010) : w1[0];
-          const float2 mf = Elem<__half>::to2(w);
-          if constexpr (RT == 8) {
-            lg[ps][0] = fmaf(p[x][0], mf.x, lg[ps][0]);
-            lg[ps][NR - 1] = fmaf(p[x][NR - 1], mf.x, lg[ps][NR - 1]);
-          } else {
-            lg[2 * ps][0] = fmaf(p[x][0], mf.x, lg[2 * ps][0]);
-            if (2 * ps + 1 < NO) lg[(2 * ps + 1) % NO][0] = fmaf(p[x][0], mf.y, lg[(2 * ps + 1) % NO][0]);
-          }
           const uint32_t hi = h2_mul(ph[x], w);
+          // sums of p M: with one part of the product's own factors, as it has them, so that what
+          // the codes' offset adds to a rounding cancels (an element that is zero stays zero); with two
+          // of p and M themselves, from which the parts are 2^-21
+          const float2 f = Elem<__half>::to2(kParts == 1 ? hi : w);
+          auto sum = [&](float& to, float weight, float factor) { to = kParts == 1 ? to + factor : fmaf(weight, factor, to); };
+          if constexpr (RT == 8) {
+            sum(lg[ps][0], p[x][0], f.x);
+            sum(lg[ps][NR - 1], p[x][NR - 1], kParts == 1 ? f.y : f.x);
+          } else {
+            sum(lg[2 * ps][0], p[x][0], f.x);
+            if (2 * ps + 1 < NO) sum(lg[(2 * ps + 1) % NO][0], p[x][0], f.y);
+          }
           bh[x] = trans8x8(hi);
           if (kParts == 2) bl[x] = trans8x8(h2_fma(pl[x], w, h2_fma(ph[x], w, h2_neg(hi))));
         }

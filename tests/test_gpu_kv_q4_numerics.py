@@ -13,6 +13,18 @@ from tests.test_gpu_kv_q4 import S, TDT, U, Setup, _attend, _check, f64  # noqa:
 pytestmark = pytest.mark.gpu
 
 
+def _store(s, r, j, k, M):
+    """Codes k [n, heads, 32 ng] and scales M [n, heads, ng] as request r's keys (j 0) or values."""
+    s.row_view()[s.at(r, 0, j)] = torch.from_numpy(oq4.pack(k, M, s.dtype, j == 1)).cuda()
+
+
+def _random(s, n, M):
+    """Codes for n tokens, and scales of random sign and at most five bits near M [n, heads, ng]."""
+    k = s.rng.integers(-7, 9, (n, s.hkv, 32 * oq4.groups(s.d)))
+    round_ = np.vectorize(lambda m: oq4.scale(m, s.dtype), otypes=[np.float64])
+    return k, round_(M * s.rng.choice([-1.0, 1.0], (n, s.hkv, oq4.groups(s.d))))
+
+
 def _leave_nans_in_shared_memory(S):  # noqa: F811
     """A chunk call over queries and a pool whose bits are all ones: they fill every SM's shared memory."""
     s = Setup(S, [0], [2048], 8, 8, 128, 1024, "f16")
@@ -93,4 +105,32 @@ def test_a_value_group_that_is_not_finite_leaves_the_others(S, dtype, hq, hkv, d
         got[bad] = torch.from_numpy(want).to(got).unflatten(1, (hkv, group))[bad]
         t0 += n
     _check(s, held, q, out)
+    s.close()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+def test_zeros_beside_large_elements(S, dtype, hq, hkv, d):  # noqa: F811
+    """Elements that are zero in every token, beside elements as large as M, with weights that
+    differ: zeros come out.  Their codes are 7, so a result is sum(w 7) - 7 sum(w) over the products w
+    of a weight and M / 8, the same w in both but for an fp16 cache's second part, 2^-21 of it: the
+    sums' own rounding is left.  Of it, relative to the largest sum: a unit's product 2^-20 (at
+    most 32 products added up and cut off), the sum over at most 13 units 13 2^-24, a lane's sum 28
+    2^-24, the lanes' and the rest 8 2^-24.  In all below 2^-17, times 7 / 8 of the largest M."""
+    s = Setup(S, [3, 33, 200], [1, 1, 1], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=15)
+    s.oracle_plan()
+    held, ng = s.fill(), oq4.groups(d)
+    top = []
+    for r in range(3):
+        n = s.ctx[r] + 1
+        k, M = _random(s, n, s.rng.uniform(0.5, 1.0, (n, hkv, ng)))
+        k[:, :, ::2] = 0
+        _store(s, r, 1, k, M)
+        held[r][1] = oq4.values(k, M, d)
+        top.append(np.abs(M).max())
+    b, q, out = _attend(s, held)
+    got = f64(out[:, : hq * d]).reshape(3, hq, d)
+    for r in range(3):
+        assert np.abs(got[r, :, ::2]).max() <= 7 / 8 * 2.0 ** -17 * top[r], (r, np.abs(got[r, :, ::2]).max())
+        assert np.abs(got[r, :, 1::2]).max() > 0.01
     s.close()
