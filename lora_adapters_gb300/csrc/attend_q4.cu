@@ -422,7 +422,8 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       }
     }
     const int at_scales = ((scale_at + (hb * hbw + hsub0) * 2 * ng) & 15) + warp * 2 * ng;     // of the head, in a token's
-    int top_m = Elem<E>::kBf16 ? -64 : -8;               // E: every |M| so far is below 2^E
+    // E: every |M| so far is below 2^E.  Begins where the smallest M (bf16 2^-100, fp16 2^-21) is held exactly
+    int top_m = Elem<E>::kBf16 ? -100 : -8;
 
     for (int c = c0; c < c1; ++c) {
       cp_wait<kAhead - 1>();

@@ -134,3 +134,34 @@ def test_zeros_beside_large_elements(S, dtype, hq, hkv, d):  # noqa: F811
         assert np.abs(got[r, :, ::2]).max() <= 7 / 8 * 2.0 ** -17 * top[r], (r, np.abs(got[r, :, ::2]).max())
         assert np.abs(got[r, :, 1::2]).max() > 0.01
     s.close()
+
+
+@pytest.mark.parametrize("dtype,low,high", [("bf16", -99, -93), ("bf16", -97, -96), ("bf16", 124, 127), ("f16", -21, -17),
+                                            ("f16", 14, 15)])
+@pytest.mark.parametrize("hq,hkv,new,d", [(4, 4, 1, 128), (8, 1, 1, 128), (8, 2, 1, 96), (4, 2, 60, 128), (2, 2, 2, 256)])
+def test_values_at_the_ends_of_the_range(S, dtype, low, high, hq, hkv, new, d):  # noqa: F811
+    """Caches whose values are all very small, or all very large, against their largest.  (fp16
+    results below 2^-14 are multiples of 2^-24: the rounding of one is off by up to 2^-25, where
+    2^-11 of the result is less.)"""
+    s = Setup(S, [300, 20], [new, new], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=8)
+    s.oracle_plan()
+    held = s.fill()
+    for r in range(2):
+        n = s.ctx[r] + s.new[r]
+        k, M = _random(s, n, 2.0 ** s.rng.uniform(low, high, (n, hkv, oq4.groups(d))))
+        _store(s, r, 1, k, M)
+        held[r][1] = oq4.values(k, M, d)
+    b = s.plan()
+    q, out = s.randn(s.T, hq * d, scale=2.0), torch.empty(s.T, hq * d, dtype=TDT[dtype], device="cuda")
+    s.kv.attend(b, 0, q, out)
+    assert s.pool.status() == S.OK
+    t0, u = 0, U[dtype]
+    for r, n in enumerate(s.new):
+        want = okv.attend(f64(q[t0: t0 + n]).reshape(n, hq, d), *held[r], s.ctx[r], d ** -0.5, 0.0)
+        vmax = np.repeat(np.abs(held[r][1]).max((0, 2)), hq // hkv)[None, :, None]
+        tol = np.maximum(u * np.abs(want), 2.0 ** -25 if dtype == "f16" else 0.0) + (
+            2.0 ** -12 + (u if new * hq // hkv > 8 else 0.0)) * vmax
+        err = np.abs(f64(out[t0: t0 + n]).reshape(n, hq, d) - want)
+        assert (err <= tol).all(), (r, float((err / tol).max()))
+        t0 += n
+    s.close()
