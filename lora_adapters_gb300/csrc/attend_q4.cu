@@ -378,7 +378,8 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
       const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);   // (infinity, NaN: e = 128)
       const float size = __uint_as_float((uint32_t)(127 + min(e, 127)) << 23);
-      const float down = CAP ? fminf(size * 256.f, 0x1p127f) : size * (256.f * sc);      // 2^(8 + e)
+      // 2^(8 + e), kept finite: a product of 0 has the score 0 for queries of every size
+      const float down = fminf(CAP ? size * 256.f : size * sc * 256.f, 0x1.fffffep127f);
 #pragma unroll
       for (int g = 0; g < NC; ++g) {
         float x[8], sum = 0.f;
@@ -479,12 +480,15 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
           }
         }
       }
-      if (CAP) {
+      // (before masks and maximum: -infinity times a factor that is 0 for a tiny scale would be no
+      // number, and of a large score the maximum's rounding would be left beside it)
 #pragma unroll
-        for (int y = 0; y < NR; ++y)
+      for (int y = 0; y < NR; ++y)
 #pragma unroll
-          for (int x = 0; x < 2 * NS; ++x) s[x][y] = capped<true>(s[x][y] * fac[y], sc, cap_t, cap2);
-      }
+        for (int x = 0; x < 2 * NS; ++x) {
+          s[x][y] *= fac[y];
+          if (CAP) s[x][y] = capped<true>(s[x][y], sc, cap_t, cap2);
+        }
       // some token is not there, or after the tile's first row
       if (valid[0] != ~0u || (c + 1) * UNIT > lim_first) {
 #pragma unroll
@@ -501,7 +505,6 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         for (int x = 2; x < 2 * NS; ++x) n[y] = fmaxf(n[y], s[x][y]);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) n[y] = fmaxf(n[y], __shfl_xor_sync(0xffffffffu, n[y], x));
-        if (!CAP) n[y] *= fac[y];                          // > 0
         n[y] = fmaxf(n[y], m[y]);
       }
       // the unit's largest |M|, of any group and token.  Those that are not finite do not count:
@@ -549,7 +552,7 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
         for (int y = 0; y < NR; ++y) {
           // a row that has seen no key yet has m = -inf; its weights are zeros
           const float z = m[y] == -INFINITY ? 0.f : 7.f - m[y];
-          p[x][y] = ex2(CAP ? s[x][y] + z : fmaf(s[x][y], fac[y], z));
+          p[x][y] = ex2(s[x][y] + z);
           l[y] += p[x][y];
         }
         ph[x] = Elem<__half>::from2(p[x][0], p[x][NR - 1]);

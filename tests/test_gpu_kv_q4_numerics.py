@@ -165,3 +165,50 @@ def test_values_at_the_ends_of_the_range(S, dtype, low, high, hq, hkv, new, d): 
         assert (err <= tol).all(), (r, float((err / tol).max()))
         t0 += n
     s.close()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,new,d", [(4, 4, 1, 128), (8, 2, 1, 64), (8, 1, 1, 256), (4, 2, 60, 128)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_scales_of_scores_that_are_next_to_nothing(S, dtype, hq, hkv, new, d, softcap):  # noqa: F811
+    """A scale so small that every score is zero, and queries of zeros: equal weights for the keys
+    that a row may see, none for the others."""
+    s = Setup(S, [5, 700], [new, new], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=16)
+    s.oracle_plan()
+    held = s.fill()
+    b = s.plan()
+    for q in (s.randn(s.T, hq * d), torch.zeros(s.T, hq * d, dtype=TDT[dtype], device="cuda")):
+        for scale in (1e-20, 1e-38):
+            out = torch.full((s.T, hq * d + 8), 3.0, dtype=TDT[dtype], device="cuda")
+            s.kv.attend(b, 0, q, out[:, : hq * d], scale=scale, softcap=softcap)
+            assert s.pool.status() == S.OK
+            _check(s, held, q, out, softcap, scale)
+    s.close()
+
+
+@pytest.mark.parametrize("hq,hkv,new,d", [(4, 4, 1, 128), (8, 2, 1, 64), (8, 1, 1, 256)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("zero_keys", [False, True])
+def test_scores_near_the_largest_number(S, hq, hkv, new, d, softcap, zero_keys):  # noqa: F811
+    """Queries whose scores reach 2^122: the largest one has all the weight (or what the cap leaves
+    it); keys of zeros have scores of zero all the same."""
+    dtype = "bf16"
+    s = Setup(S, [5, 700], [new, new], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=17)
+    s.oracle_plan()
+    held = s.fill()
+    for r in range(2):
+        n = s.ctx[r] + s.new[r]
+        k, M = _random(s, n, s.rng.uniform(0.25, 1.0, (n, hkv, oq4.groups(d))))
+        if zero_keys:
+            k[:], M[:] = 0, 0.0
+        _store(s, r, 0, k, M)
+        held[r][0] = oq4.values(k, M, d)
+    b = s.plan()
+    q = torch.zeros(s.T, hq, d, dtype=TDT[dtype], device="cuda")
+    q[:, :, 37 % d] = 2.0 ** 125
+    q[:, hq // 2:, 37 % d] *= -1
+    q, out = q.view(s.T, hq * d), torch.full((s.T, hq * d + 8), 3.0, dtype=TDT[dtype], device="cuda")
+    s.kv.attend(b, 0, q, out[:, : hq * d], softcap=softcap)
+    assert s.pool.status() == S.OK
+    _check(s, held, q, out, softcap)
+    s.close()
