@@ -657,7 +657,7 @@ int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, 
  * slora_kv_attend over such a cache: scores from the numbers that the codes stand for; softmax and
  * sums in fp32.  Where a request has at most 8 rows, head_dim is below 64 or above 128, or
  * more than 32 query heads share a key head: of a row of queries, bits below 2^-24 of its largest
- * element are lost.  The softmax weights are held in two fp16 parts, each times the value's M, in
+ * element (2^-23 where head_dim is above 128) are lost.  The softmax weights are held in two fp16 parts, each times the value's M, in
  * an fp16 cache, and in one in a bf16 cache (2^-11 of a weight, and 2^-11 of its product with M;
  * either way relative to the element that the code stands for, so that a zero stays one but for the
  * fp32 sums' rounding).  M is exact down to 2^-27 of the largest finite M among the head's

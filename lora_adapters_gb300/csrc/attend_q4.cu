@@ -12,8 +12,8 @@
 //    16 into Q or the result;
 //  - K's scale multiplies a group's accumulator, a pair of steps of the sum over the
 //    head; the offset 7 sum(q) is the accumulator's first value.  Queries are scaled by
-//    a power of two to below 2^14 first, which fp16's exponents hold for bf16 too (bits
-//    below 2^-24 of a row's largest element are lost);
+//    a power of two to below 2^14 (heads above 128: 2^13) first, which fp16's exponents hold
+//    for bf16 too (bits below 2^-24, or 2^-23, of a row's largest element are lost);
 //  - V's scale goes into the weights.  bf16 caches have every weight p in one fp16 part:
 //    2^-11 of it, and as much for its product with M 2^(7 - E) (|M| < 2^E so far), are an
 //    eighth of the rounding of a result each.  fp16 caches have two, p = hi + lo, and hi M
@@ -152,6 +152,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   constexpr int NR = RT == 8 ? 2 : 1;                  // rows of a lane
   using R = Ring<NG>;
   constexpr int UNIT = R::kUnit, NS = UNIT / 16;
+  // Queries are scaled to below 2^(kQTop + 1): a group's product with codes is then at most 2^-2 (2^-3),
+  // and the sum over 4 (8) groups times M, which reaches 31 2^123, below 2^128
+  constexpr int kQTop = NG == 8 ? 12 : 13;
   constexpr int NO = RT == 2 ? NG / 2 : NC;            // groups of a lane's results
   // Parts of a weight.  256 requests of 8 to 640 tokens, 32 heads of fp16: 113 us with two,
   // 105 with one, which costs the result's last bit; 128 requests of 17 to 8192, 40 heads
@@ -376,10 +379,11 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // 2^e <= top < 2^(e + 1); e = -100 where it is less
       const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);   // (infinity, NaN: e = 128)
+      const float up = __uint_as_float((uint32_t)(127 + kQTop - e) << 23);   // (infinity, NaN: e = 128)
       const float size = __uint_as_float((uint32_t)(127 + min(e, 127)) << 23);
-      // 2^(8 + e), kept finite: a product of 0 has the score 0 for queries of every size
-      const float down = fminf(CAP ? size * 256.f : size * sc * 256.f, 0x1.fffffep127f);
+      // 2^(21 - kQTop + e), kept finite: a product of 0 has the score 0 for queries of every size
+      constexpr float kDown = 1 << (21 - kQTop);
+      const float down = fminf(CAP ? size * kDown : size * sc * kDown, 0x1.fffffep127f);
 #pragma unroll
       for (int g = 0; g < NC; ++g) {
         float x[8], sum = 0.f;

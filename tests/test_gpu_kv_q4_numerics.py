@@ -212,3 +212,27 @@ def test_scores_near_the_largest_number(S, hq, hkv, new, d, softcap, zero_keys):
     assert s.pool.status() == S.OK
     _check(s, held, q, out, softcap)
     s.close()
+
+
+@pytest.mark.parametrize("hq,hkv,new,d", [(4, 4, 1, 128), (4, 4, 1, 160), (2, 2, 1, 256), (8, 1, 1, 256), (4, 2, 60, 128)])
+def test_keys_of_the_largest_numbers(S, hq, hkv, new, d):  # noqa: F811
+    """Keys as large as a bf16 cache holds, all of one sign, against queries of one sign that
+    bring their products back: scores of ordinary size."""
+    s = Setup(S, [5, 300], [new, new], hq, hkv, d, oq4.row_bytes(hkv, d) * 2, "bf16", seed=18)
+    s.oracle_plan()
+    held = s.fill()
+    for r in range(2):
+        n = s.ctx[r] + s.new[r]
+        k = s.rng.integers(7, 9, (n, hkv, 32 * oq4.groups(d)))
+        M = np.full((n, hkv, oq4.groups(d)), oq4.LARGEST["bf16"])
+        k[::3] = s.rng.integers(-7, 9, k[::3].shape)
+        _store(s, r, 0, k, M)
+        held[r][0] = oq4.values(k, M, d)
+    b = s.plan()
+    q = torch.full((s.T, hq * d), 1.9921875 * 2.0 ** -100, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((s.T, hq * d + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    scale = float(np.float32(8.0 / (d * 2.0 ** 29)))
+    s.kv.attend(b, 0, q, out[:, : hq * d], scale=scale)
+    assert s.pool.status() == S.OK
+    _check(s, held, q, out, scale=scale)
+    s.close()
