@@ -560,7 +560,8 @@ cudaError_t normed_join(const KvAttendArgs& a, int num_sms, bool after_chunks, i
 }
 }  // namespace
 
-int64_t kv_attend_parts(int num_sms) { return (int64_t)num_sms * kDecCtas * kDecWarps * 2 * kKvRowTile; }
+static_assert(kDecCtas * kDecWarps <= kKvDecodeWarps, "the scratch has room for every warp's parts");
+int64_t kv_attend_parts(int num_sms) { return (int64_t)num_sms * kKvDecodeWarps * 2 * kKvRowTile; }
 int32_t kv_attend_cols(int32_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
 template <class E, int D>

@@ -736,6 +736,7 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
   while (a.kv.heads_kv % heads) --heads;
   a.hbw = std::max(1, 16 / heads) * heads;
   while (a.kv.heads_kv % a.hbw) a.hbw -= heads;
+  static_assert(q4_warps(NC) <= kKvDecodeWarps, "the scratch has room for every warp's parts");
   const int grid = num_sms * (q4_warps(NC) / heads), smem = ring_bytes<NG>(heads, NC);
   const int threads = heads * 32;
   auto kernel = a.softcap > 0.f ? kv_q4_decode_kernel<E, NC, RT, true> : kv_q4_decode_kernel<E, NC, RT, false>;

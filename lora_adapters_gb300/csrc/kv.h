@@ -15,6 +15,9 @@ constexpr int kKvMaxRequests = 4096;   // == SLORA_KV_MAX_REQUESTS
 constexpr int kKvMaxHeadDim = 256;     // == SLORA_KV_MAX_HEAD_DIM
 constexpr int kKvRowTile = 8;          // query rows (token, head of the group) of one decode segment
 constexpr int kKvUnit = 16;            // tokens of one decode unit
+// Warps an SM that a decode kernel of either kind of cache runs at most: each leaves up to two parts of
+// split segments in the scratch (kv_attend_parts).
+constexpr int kKvDecodeWarps = 12;
 // The same of a 4-bit cache: twice as many, with the steps of the softmax once for all of
 // them, where registers hold their codes and the result (256 requests of 8 to 640 tokens,
 // 32 heads of 128: 113 us with 32 tokens, 129 with 16; 128 of 17 to 8192, 40 heads on 8:
