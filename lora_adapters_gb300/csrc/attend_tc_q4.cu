@@ -23,14 +23,12 @@ void (*chunk_kernel(int dtype, int cap, int head_dim, int groups))(const KvAtten
 
 }  // namespace
 
-cudaError_t prepare_kv_q4_chunk_kernels() {
-  for (int dtype = 0; dtype < 2; ++dtype)
-    for (int cap : {kCapNone, kCapSmall, kCapAny})
-      for (int head_dim : {64, 96, 112, 128}) {
-        const cudaError_t e = cudaFuncSetAttribute(chunk_kernel(dtype, cap, head_dim, (head_dim + 31) / 32),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<true>);
-        if (e != cudaSuccess) return e;
-      }
+cudaError_t prepare_kv_q4_chunk_kernels(int dtype, int head_dim) {
+  for (int cap : {kCapNone, kCapSmall, kCapAny}) {
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel(dtype, cap, head_dim, (head_dim + 31) / 32),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<true>);
+    if (e != cudaSuccess) return e;
+  }
   return cudaSuccess;
 }
 

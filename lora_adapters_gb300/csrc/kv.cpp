@@ -226,7 +226,7 @@ int create(slora_kv** out, slora_pool* pool, const slora_kv_config* c, bool q4, 
     CUDA_TRY(cudaMalloc(&kv->d_part_ml, sizeof(float2) * (size_t)parts));
     kv->tpt = kv_chunk_tokens(d.heads_q / d.heads_kv, d.head_dim);
     if (kv->tpt > 0) {
-      CUDA_TRY(q4 ? prepare_kv_q4_chunk_kernels() : prepare_kv_chunk_kernels());
+      CUDA_TRY(q4 ? prepare_kv_q4_chunk_kernels(pv.dtype, d.head_dim) : prepare_kv_chunk_kernels());
       const int64_t rows = kv_chunk_part_rows(pv.num_sms);
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_o, sizeof(float) * (size_t)rows * kKvTile));
       CUDA_TRY(cudaMalloc(&kv->d_tc_part_ml, sizeof(float2) * (size_t)rows));

@@ -184,7 +184,8 @@ int32_t kv_attend_cols(int32_t head_dim);
 // The decode kernel (after_chunks: while the chunk kernel launched before it
 // still runs), and the joins of what either kernel split.
 cudaError_t launch_kv_decode(const KvAttendArgs& a, int dtype, int num_sms, bool after_chunks, cudaStream_t st);
-cudaError_t prepare_kv_q4_chunk_kernels();
+// (of one type and head size: others are not loaded)
+cudaError_t prepare_kv_q4_chunk_kernels(int dtype, int head_dim);
 cudaError_t launch_kv_q4_chunk(const KvAttendArgs& a, int dtype, int num_sms, cudaStream_t st);
 // The joins alone, of what `groups` groups of CTAs of the 4-bit decode kernel split, with
 // the parts' results divided by their sums.

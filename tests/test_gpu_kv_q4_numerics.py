@@ -236,3 +236,14 @@ def test_keys_of_the_largest_numbers(S, hq, hkv, new, d):  # noqa: F811
     assert s.pool.status() == S.OK
     _check(s, held, q, out, scale=scale)
     s.close()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 80, 96, 112, 128])
+def test_chunks_of_every_head_size_and_cap(S, dtype, d):  # noqa: F811
+    s = Setup(S, [70, 3], [20, 11], 4, 2, d, oq4.row_bytes(2, d) * 2, dtype, seed=19)
+    s.oracle_plan()
+    held = s.fill()
+    for softcap in (0.0, 20.0, 100.0):
+        _attend(s, held, softcap=softcap)
+    s.close()
