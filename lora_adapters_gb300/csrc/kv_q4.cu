@@ -24,13 +24,16 @@ namespace {
 //    border (2n + 1) M / 16 at most 9, so the two are equal or at least 2^-11 of the
 //    border apart.  t = 8 x / M evaluated with an error below 2^-18 and raised by
 //    2^-15 then rounds to the right integer, ties upwards;
-//  - a rotated key has an error of at most 2^-20.7 of the head's largest element (angle
+//  - a rotated key has an error of at most 2^-20.7 of its pair's larger element (angle
 //    2^-23.3, cosine and sine 2^-24 more, mscale's product 2^-24: 2^-22.1 each, times the
-//    sum of two elements, at most twice the largest rotated one; a product's and a sum's
+//    sum of two elements, at most twice the larger rotated one; a product's and a sum's
 //    rounding), a normed one of 2^-19.6 (every element's factor 2^-23, the norm's
 //    2^-20.9: nine roundings of the sum of squares, halved, and the root's two units).  Where
 //    that could change a code, M's rounding or the choice between the two signs, the warp
-//    works the elements in question out again in fp64 (exact_scale, exact_codes).
+//    works the elements in question out again in fp64 (exact_scale, exact_codes).  The bound
+//    counts from the largest finite element of the group and of those with its pairs' other
+//    halves: from the head's largest, one outlier had whole heads worked out again (256 tokens with
+//    an infinite element a head 178 us, 16 so; 8090 normed ones with one 1000 times the rest 264, 64 so)
 constexpr int kAppendThreads = 256;
 constexpr float kErrTurned = 0x1.6p-21f, kErrNormed = 0x1.6p-20f;     // 2^-20.5, 2^-19.5
 
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
     const int page = (int)a.per_page_div.div((uint32_t)slot);
     return reinterpret_cast<uint8_t*>(d.pool) + q4_row(d, page, slot - page * d.per_page);
   };
-  // the lane's and its group's error bound, in the head's largest element
+  // the lane's and its group's error bound, in the largest element of its pairs' groups
   const bool group_err = NORM || (ln.li & ~3) < 2 * half;
   constexpr float kErr = NORM ? kErrNormed : kErrTurned;
   constexpr float kFinest = Elem<E>::kBf16 ? 0x1p-100f : 0x1p-21f, kLargest = Elem<E>::kBf16 ? 31.f * 0x1p123f : 31.f * 0x1p11f;
@@ -274,11 +277,15 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
           lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         }
         const float m = hi >= -lo ? hi : lo, am = fabsf(m);
-        float M = copysignf(q4_scale<E>(am), m), top = am;
+        float M = copysignf(q4_scale<E>(am), m), top = am <= 3.402823466e38f ? am : 0.f;
         float inv = M == 0.f ? 0.f : rcp(M) * 8.f;
         if (!kValue) {
+          if (!INTER) {                          // (each lane's partner may be in another group)
+            float there = __shfl_sync(0xffffffffu, top, ln.partner);
 #pragma unroll
-          for (int o = 4; o < G; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));    // the head's largest
+            for (int o = 1; o < 4; o <<= 1) there = fmaxf(there, __shfl_xor_sync(0xffffffffu, there, o));
+            top = fmaxf(top, there);
+          }
           // M may round otherwise where am lies within its error of a number of five bits: in
           // units of its last place, at most 2^24 err / am, and am >= 16 / 17 |M|.  (Below 32
           // units of the finest M its rounding is another: always asked)

@@ -247,3 +247,70 @@ def test_chunks_of_every_head_size_and_cap(S, dtype, d):  # noqa: F811
     for softcap in (0.0, 20.0, 100.0):
         _attend(s, held, softcap=softcap)
     s.close()
+
+
+OUTLIERS = {"none": 1.0, "64": 64.0, "1000": 1000.0, "infinite": float("inf")}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rot", ["half", "interleaved", "part"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("d", [64, 96, 128, 240])
+@pytest.mark.parametrize("size", OUTLIERS)
+def test_keys_with_outliers(S, dtype, rot, norm, d, size):  # noqa: F811
+    """Heads with an element far above the rest: the bytes are the oracle's in every group."""
+    hkv = 3
+    s = Setup(S, [90], [32], hkv, hkv, d, oq4.row_bytes(hkv, d) * 2, dtype, seed=21)
+    freq = [10000.0 ** (-2 * i / d) for i in range(d // 2)]
+    rot_dim = 16 if rot == "part" else d
+    s.kv.set_rotary(rot_dim, freq, interleaved=rot == "interleaved")
+    b = s.plan()
+    want = s.oracle_plan()
+    k = s.randn(s.T, hkv * d)
+    k[:, 5::d] *= OUTLIERS[size]
+    w = s.randn(d, scale=0.3) + 1 if norm else None
+    s.kv.append(b, 0, k.clone(), k, k, q_out=torch.empty_like(k), q_weight=w, k_weight=w, eps=1e-5)
+    torch.cuda.synchronize()
+    assert s.pool.status() == S.OK
+    used = 18 * oq4.groups(d) * hkv
+    for t in range(s.T):
+        with np.errstate(invalid="ignore"):
+            y = okv.norm_rotate(f64(k[t]).reshape(hkv, d), f64(w) if norm else None, 1e-5, int(want["tok_pos"][t]), freq,
+                                rot_dim, rot == "interleaved", 1.0)
+        slot = int(want["slots"][0, 0, t])
+        got = s.row_view()[slot // s.P, slot % s.P].cpu().numpy()[None]
+        codes, M = oq4.quantise(y, dtype)
+        row = oq4.pack(codes[None], M[None], dtype, False)
+        held, expect = oq4.unpack(got, hkv, d, dtype, False), oq4.unpack(row, hkv, d, dtype, False)
+        assert np.array_equal(held, expect, equal_nan=True), t
+        if not np.isnan(M).any():                  # (the codes of a group that is NaN are not defined)
+            assert np.array_equal(got[0, :used], row[0, :used]), t
+    s.close()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_outliers_do_not_slow_the_append(S, norm):  # noqa: F811
+    """An element far above the rest of its head, or an infinite one, leaves few elements of the other
+    groups near a border: the append takes about as long as without it (it was 4 to 11 times as long)."""
+    hkv, d, T = 32, 128, 512
+    s = Setup(S, [90], [T], hkv, hkv, d, 4096, "f16")
+    s.kv.set_rotary(d, [10000.0 ** (-2 * i / d) for i in range(d // 2)])
+    b = s.plan()
+    plain, w = s.randn(T, hkv * d), s.randn(d, scale=0.3) + 1 if norm else None
+    out, took = torch.empty_like(plain), {}
+    for size in OUTLIERS:
+        k = plain.clone()
+        k[:, 5::d] *= OUTLIERS[size]
+        times = []
+        for _ in range(7):
+            ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            with torch.cuda.stream(s.pool.compute_stream):
+                ev[0].record()
+                for _ in range(8):
+                    s.kv.append(b, 0, plain, k, k, q_out=out, q_weight=w, k_weight=w)
+                ev[1].record()
+            torch.cuda.synchronize()
+            times.append(ev[0].elapsed_time(ev[1]) / 8)
+        took[size] = min(times)
+    assert max(took.values()) < 2.5 * took["none"], took
+    s.close()
