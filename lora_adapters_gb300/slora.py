@@ -576,6 +576,8 @@ class KVBatch:
 
 def tokens_per_page(page_elems: int, heads_kv: int, head_dim: int, bits: int = 16) -> int:
     """Tokens whose K (or V) of one layer a page of a KV cache of 16 or 4 bits holds."""
+    if bits not in (4, 16):
+        raise ValueError(f"a KV cache holds 16 or 4 bits an element, not {bits}")
     if bits == 16:
         return page_elems // max(1, heads_kv * head_dim)
     row = -(-18 * -(-head_dim // 32) * heads_kv // 16) * 16      # bytes: 16 of codes and one M a head and group

@@ -154,3 +154,9 @@ def test_oracle_quantiser(dtype):
     assert row[0 * 3 + 1] == 15 << (16 * 1 + 4 * 2) and (np.delete(row, 1) == 0).all()
     row = oq4.pack(k, M, dtype, True)[0, :48].view("<u2")
     assert row[1 * 3 + 1] == 15 << (4 * 1) and (np.delete(row, 4) == 0).all()
+
+
+def test_tokens_per_page_refuses_other_widths(S):
+    for bits in (0, 2, 8, 32):
+        with pytest.raises(ValueError):
+            S.tokens_per_page(4096, 32, 128, bits)
