@@ -593,7 +593,8 @@ int slora_kv_append(slora_kv* kv, const slora_kv_batch* batch, int32_t layer, co
  * head h / (heads_q / heads_kv),
  *     out = sum_{j <= p} softmax_j(c(scale * q . k_j)) v_j,
  * c(s) = softcap * tanh(s / softcap), or s itself for softcap 0.  The step's
- * own keys and values must be appended first.  scale > 0.  Scores, softmax and sums are
+ * own keys and values must be appended first.  scale > 0.  Scores (below 2^22 in size where a
+ * request has more than 8 rows; larger ones may give results that are not finite), softmax and sums are
  * fp32 (a sum of n keys' products on the tensor cores may come out n 2^-26 of itself too
  * small), the result is rounded once.  For the product with the values the softmax weights
  * are held in the storage type: in two parts, twice its bits, where a request has at most 8
@@ -639,7 +640,8 @@ int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, 
  * computes with, these numbers.  An element is off by at most |M| / 16, one whose
  * sign is not m's by at most |M| / 8.  Keys are quantised from their fp32 value after
  * norm and rotary turn, with no rounding in between, and codes are those of the
- * formula in exact arithmetic (where fp32 cannot tell, it is evaluated in 64 bits).
+ * formula in exact arithmetic (where fp32 cannot tell, it is evaluated in 64 bits; the
+ * mean square that a norm divides by has to be a normal fp32 number).
  * M is kept in the storage type: fp16's is a multiple of 2^-21 and at most 31 * 2^11,
  * bf16's a multiple of 2^-100 and at most 31 * 2^123; larger elements are held as the
  * largest M.  A group with an element that is not finite stands for NaN throughout.
@@ -656,13 +658,14 @@ int slora_kv_read(slora_kv* kv, int32_t layer, int32_t n, const int32_t* d_row, 
  *
  * slora_kv_attend over such a cache: scores from the numbers that the codes stand for; softmax and
  * sums in fp32.  Where a request has at most 8 rows, head_dim is below 64 or above 128, or
- * more than 32 query heads share a key head: of a row of queries, bits below 2^-24 of its largest
- * element (2^-23 where head_dim is above 128) are lost.  The softmax weights are held in two fp16 parts, each times the value's M, in
- * an fp16 cache, and in one in a bf16 cache (2^-11 of a weight, and 2^-11 of its product with M;
- * either way relative to the element that the code stands for, so that a zero stays one but for the
- * fp32 sums' rounding).  M is exact down to 2^-27 of the largest finite M among the head's
- * values, of any group and token.  Elsewhere the weights are in one part of the storage type.  A
- * weight's error is at least 2^-32 of the largest.
+ * more than 32 query heads share a key head, of a row of queries bits below 2^-24 of its
+ * largest element (2^-23 where head_dim is above 128) are lost, and the softmax weights are
+ * held in two fp16 parts, each times the value's M, in an fp16 cache, in one in a bf16 cache (2^-11
+ * of a weight, and 2^-11 of its product with M).  Either error goes with the element that a
+ * code stands for: a zero stays one but for the rounding of the fp32 sums.  M is exact down to
+ * 2^-27 of the largest finite M among the head's values, of any group and token.  Elsewhere
+ * the weights are in one part of the storage type.  A weight's error is at least 2^-32 of the
+ * largest.
  */
 int slora_kv_q4_array_ints(const slora_pool* pool, const slora_kv_config* config, int64_t* n);
 int slora_kv_q4_create(slora_kv** out, slora_pool* pool, const slora_kv_config* config, int32_t* d_table,

@@ -16,20 +16,25 @@
 //    for bf16 too (bits below 2^-24, or 2^-23, of a row's largest element are lost);
 //  - V's scale goes into the weights.  bf16 caches have every weight p in one fp16 part:
 //    2^-11 of it, and as much for its product with M 2^(7 - E) (|M| < 2^E so far), are an
-//    eighth of the rounding of a result each.  fp16 caches have two, p = hi + lo, and hi M
-//    is again two parts, a product and its exact remainder.  Columns of the product that
-//    have no row (fewer than 8 query rows) take other groups' weights: RT rows times 8 / RT
-//    groups fill them, and a token's weights are worked out that many times less often;
+//    eighth of the rounding of a result each, of the element itself (the offset's sum is of
+//    the rounded products too).  fp16 caches have two, p = hi + lo, and hi M is again two
+//    parts, a product and its exact remainder.  Columns of the product that have no row
+//    (fewer than 8 query rows) take other groups' weights: RT rows times 8 / RT groups fill
+//    them, and a token's weights are worked out that many times less often;
 //  - each unit's result starts from zero and is added to the running one in fp32: with
 //    codes that are never negative, a running sum in the tensor core would lose bits
 //    to its truncation.
 //
-// Bound: what four issue slots a clock can do for the bytes of a unit.  Per 32 tokens of
-// a head of 128 there are 4,608 bytes, 196 cycles of an SM's share of the memory, against
-// 700 (two rows, weights in two parts) or 810 (eight rows, in one) instructions of a warp,
-// half of them on the integer and logic pipe at half rate.  Measured: 256 requests of 8 to
-// 640 tokens, 32 heads of 128, 111 us (3.5 TB/s of codes and scales; the copies alone 70);
-// 128 requests of 17 to 8192 tokens, 40 heads on 8, 159 us (3.8 TB/s; 105).
+// Bound: the latency of a unit's steps, which follow each other in every warp (barrier, scores,
+// maximum, weights, results), with three warps a scheduler to hide it.  Per 32 tokens of
+// a head of 128 there are 4,608 bytes, 196 cycles of an SM's share of the memory, against 715
+// (two rows, weights in two parts) or 820 (eight rows, in one) instructions of a warp, 180 or 205
+// cycles of its issue slots, of which 53 and 62 % are taken; the integer and logic pipe is
+// busy 46 and 50 % of the time, and results of a fixed latency are what warps wait for most.
+// Measured: 256 requests of 8 to 640 tokens, 32 heads of 128, 114 us (3.4 TB/s of codes and
+// scales; the copies alone 70); 128 requests of 17 to 8192 tokens, 40 heads on 8, 162 us (3.8
+// TB/s; 105).  The times beside the rules below are single calls' over a cold cache, 115 and 165
+// for these two.
 #include <type_traits>
 
 #include "attend.cuh"
@@ -42,8 +47,8 @@ namespace {
 // kMaxAbreast; and as many CTAs an SM as make q4_warps.
 constexpr int kMaxAbreast = 6;
 __host__ __device__ constexpr int q4_rounded(int ng) { return ng <= 2 ? 2 : ng <= 4 ? 4 : 8; }
-// An SM: 170 or 255 registers a thread.  (16 of up to 4 groups, 128 registers: they spill,
-// 185 us instead of 160 for 128 requests of 17 to 8192 tokens, 40 heads on 8.)
+// An SM: 168 or 255 registers a thread.  (16 of up to 4 groups, 128 registers: they spill,
+// 184 us instead of 165 for 128 requests of 17 to 8192 tokens, 40 heads on 8.)
 constexpr int q4_warps(int ng) { return ng <= 4 ? 12 : 6; }
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
@@ -105,9 +110,9 @@ __device__ __forceinline__ void sts(uint32_t at, const uint32_t (&w)[N]) {
 template <int NG>
 struct Ring {
   static constexpr int kUnit = NG <= 4 ? 32 : 16;      // kv_q4_unit
-  // 128 requests of 17 to 2048 tokens, 16 heads of 160: 238 us with 2, 230 with 3; of 192
-  // 227 and 213; of 256 231 and 223 (8 key heads of two rows 123 and 115, of 224 145 and
-  // 154).  256 requests of 8 to 640, 32 heads of 128: 113 and 117.
+  // 128 requests of 17 to 2048 tokens, 16 heads of 160: 235 us with 2 and with 3; of 192 230
+  // and 229; of 256 233 and 222 (8 key heads of two rows 125 and 119, of 224 145 and
+  // 154).  256 requests of 8 to 640, 32 heads of 128: 115 and 117.
   static constexpr int kStages = NG == 8 ? 3 : 2;
   static constexpr int kCodes = kUnit * 16 * NG;       // of a head
   static constexpr int kRows = kUnit * 16 + 16;        // where a unit's rows begin, which are there, the block of heads
@@ -156,9 +161,9 @@ kv_q4_decode_kernel(const __grid_constant__ KvAttendArgs a) {
   // and the sum over 4 (8) groups times M, which reaches 31 2^123, below 2^128
   constexpr int kQTop = NG == 8 ? 12 : 13;
   constexpr int NO = RT == 2 ? NG / 2 : NC;            // groups of a lane's results
-  // Parts of a weight.  256 requests of 8 to 640 tokens, 32 heads of fp16: 113 us with two,
-  // 105 with one, which costs the result's last bit; 128 requests of 17 to 8192, 40 heads
-  // on 8 of bf16: 184 and 164 us.
+  // Parts of a weight.  256 requests of 8 to 640 tokens, 32 heads of fp16: 115 us with two,
+  // 107 with one, which costs the result's last bit; 128 requests of 17 to 8192, 40 heads
+  // on 8 of bf16: 182 and 165 us.
   constexpr int kParts = Elem<E>::kBf16 ? 1 : 2;
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   constexpr uint32_t kNotFinite = Elem<E>::kBf16 ? 0x7f80u : 0x7c00u;    // infinity's bits
@@ -730,8 +735,8 @@ cudaError_t launch_rows(KvAttendArgs a, int num_sms, bool after_chunks, cudaStre
   constexpr int NG = q4_rounded(NC);
   // Heads of a CTA, and as many neighbouring ones at a time as up to 16 that several CTAs share:
   // a head's codes of a token are 64 bytes, and what neighbours read at other times the DRAM
-  // fetches again (32 heads of 128, 256 requests: 119 us with a CTA's heads alone, 113 so; 8 key
-  // heads, 128 long requests: 168 and 164).
+  // fetches again (32 heads of 128, 256 requests: 121 us with a CTA's heads alone, 115 so; 8 key
+  // heads, 128 long requests: 168 and 165).
   int heads = kMaxAbreast;
   while (a.kv.heads_kv % heads) --heads;
   a.hbw = std::max(1, 16 / heads) * heads;

@@ -20,8 +20,8 @@ constexpr int kKvUnit = 16;            // tokens of one decode unit
 constexpr int kKvDecodeWarps = 12;
 // The same of a 4-bit cache: twice as many, with the steps of the softmax once for all of
 // them, where registers hold their codes and the result (256 requests of 8 to 640 tokens,
-// 32 heads of 128: 113 us with 32 tokens, 129 with 16; 128 of 17 to 8192, 40 heads on 8:
-// 164 and 207).
+// 32 heads of 128: 115 us with 32 tokens, 129 with 16; 128 of 17 to 8192, 40 heads on 8:
+// 165 and 207).
 inline int32_t kv_q4_unit(int32_t head_dim) { return head_dim <= 128 ? 2 * kKvUnit : kKvUnit; }
 constexpr int kKvTile = 128;           // rows and keys of one chunk tile
 // A request whose new tokens make more rows than this (per key head) goes to the
@@ -34,11 +34,15 @@ constexpr int kKvChunkRows = kKvRowTile;
 // `rows` of them: the kernel works a token's weights out 8 / (rows of a tile) times less
 // often with tiles of 2 or 4 (attend_q4.cu).  With chunks in the call the other requests may have
 // up to kKvChunkRows, but mostly have one new token, `group` rows.  Tiles by this rule against
-// tiles of 8, 128 requests of 17 to 2048 tokens, one row: 32 heads of 64 111 and 121 us, of
-// 96 166 and 182, 16 of 160 230 and 248, of 192 213 and 235, of 256 223 and 281; two rows,
-// 8 key heads of 224 154 and 182, of 256 115 and 135; four rows, 8 key heads of 64 41 and 45,
-// of 96 57 and 61, of 128 57 and 64 (bf16 51 and 58).  256 requests of 8 to 640, 32 heads of
-// 128: 113 and 133.  One group alone fills no more columns.
+// tiles of 8, 128 requests of 17 to 2048 tokens, one row: 32 heads of 64 111 and 123 us, of
+// 96 164 and 183, 16 of 160 235 and 248, of 192 229 and 258, of 256 222 and 287; two rows,
+// 8 key heads of 224 154 and 182, of 256 119 and 156; four rows, 8 key heads of 64 41 and 45,
+// of 96 57 and 61, of 128 59 and 62 (bf16 53 and 58).  256 requests of 8 to 640, 32 heads of
+// 128: 115 and 133.  One group alone fills no more columns.
+// With chunks the rule is a guess, since a call's lengths are the GPU's to read: the same 128
+// requests beside a prompt of 512, 32 heads of 128, with 1 and 2 new tokens each 187 and 191 us
+// (214 and 218 with tiles of 8), with 4 and 8, which read the cache two and four times, 332
+// and 621 (224 and 230); 4 heads on each of 4, one token 54 and 57, two 73 and 60.
 inline int32_t kv_q4_row_tile(int32_t groups, int32_t group, int64_t rows, bool chunks) {
   const int64_t most = chunks ? group : rows;
   if (groups == 1 || most > 4) return kKvRowTile;

@@ -17,7 +17,7 @@ namespace {
 // Norm and rotation as in kv.cu, a warp per token and share of its heads, eight
 // consecutive elements a lane; a group is four lanes.  Bound: instructions, about 150 a
 // lane's eight quantised elements: 8090 tokens of 56 heads, normed, half of each head
-// turned, 64 us (181 MB, 60 % of the issue slots); 256 tokens of 96 heads 12.
+// turned, 61 to 63 us (181 MB, 59 % of the issue slots); 256 tokens of 96 heads 12.
 //
 // Codes are those of the formula in exact arithmetic, not of its fp32 evaluation:
 //  - a value that comes straight from 16 bits has at most 11 significant bits, a
