@@ -31,9 +31,10 @@ namespace {
 //    2^-20.9: nine roundings of the sum of squares, halved, and the root's two units).  Where
 //    that could change a code, M's rounding or the choice between the two signs, the warp
 //    works the elements in question out again in fp64 (exact_scale, exact_codes).  The bound
-//    counts from the largest finite element of the group and of those with its pairs' other
-//    halves: from the head's largest, one outlier had whole heads worked out again (256 tokens with
-//    an infinite element a head 178 us, 16 so; 8090 normed ones with one 1000 times the rest 264, 64 so)
+//    counts from the largest element of the group and of those with its pairs' other halves
+//    (one past fp32's range counts as the largest number: its pair's may be finite).  From the
+//    head's largest, one outlier had whole heads worked out again (256 tokens with an infinite
+//    element a head 178 us, 16 so; 8090 normed ones with one 1000 times the rest 264, 64 so)
 constexpr int kAppendThreads = 256;
 constexpr float kErrTurned = 0x1.6p-21f, kErrNormed = 0x1.6p-20f;     // 2^-20.5, 2^-19.5
 
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_q4_append_kernel(const _
           lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         }
         const float m = hi >= -lo ? hi : lo, am = fabsf(m);
-        float M = copysignf(q4_scale<E>(am), m), top = am <= 3.402823466e38f ? am : 0.f;
+        float M = copysignf(q4_scale<E>(am), m), top = fminf(am, 3.402823466e38f);
         float inv = M == 0.f ? 0.f : rcp(M) * 8.f;
         if (!kValue) {
           if (!INTER) {                          // (each lane's partner may be in another group)

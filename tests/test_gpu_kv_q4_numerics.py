@@ -288,6 +288,38 @@ def test_keys_with_outliers(S, dtype, rot, norm, d, size):  # noqa: F811
     s.close()
 
 
+def test_a_pair_of_which_one_leaves_the_range(S):  # noqa: F811
+    """Turned by an eighth of a circle and a little, a pair of the largest keys becomes one past fp32's
+    range, whose group is NaN, and a small one, of which fp32 has no bit: its group's bytes
+    are the oracle's."""
+    d, T = 64, 40
+    s = Setup(S, [0], [T], 1, 1, d, 512, "bf16", seed=22)
+    off = np.logspace(-10, -8, T)
+    freq = [0.0] * (d // 2)
+    k = s.randn(T, d).double() * 3e29
+    k[:, 0] = k[:, 32] = 3.3e38
+    k = k.to(torch.bfloat16)
+    for t in range(1, T):                          # (one token a call: every one has its own angle)
+        s.ctx, s.new, s.T = [t], [1], 1
+        freq[0] = (np.pi / 4 + off[t]) / t
+        s.kv.set_rotary(d, freq)
+        block = t // s.P                           # K's page and V's
+        s.kv.table[0, :, :, block] = s.dev([2 * block, 2 * block + 1])[:, None]
+        opens = s.dev([2 * block, 2 * block + 1]) if t % s.P == 0 else None
+        b = s.kv.plan(s.dev([t]), s.dev([1]), opens, 1, 1, rows=s.dev(s.rows))
+        s.kv.append(b, 0, k[t: t + 1].clone(), k[t: t + 1], k[t: t + 1])
+        torch.cuda.synchronize()
+        assert s.pool.status() == S.OK
+        y = okv.norm_rotate(f64(k[t]).reshape(1, d), None, 0.0, t, freq, d, False, 1.0)
+        assert abs(y[0, 0]) < 1e31 and y[0, 32] > 3.41e38
+        out = torch.empty(1, d, dtype=torch.bfloat16, device="cuda")
+        s.kv.read(0, s.dev(s.rows), s.dev([t]), out)
+        assert out[0, 32:].isnan().all()
+        assert np.array_equal(f64(out)[0, :32], oq4.values(*oq4.quantise(y, "bf16"), d)[0, :32]), t
+    s.close()
+
+
+
 @pytest.mark.parametrize("norm", [False, True])
 def test_outliers_do_not_slow_the_append(S, norm):  # noqa: F811
     """An element far above the rest of its head, or an infinite one, leaves few elements of the other
